@@ -37,7 +37,7 @@ _CODE_DTYPE = {BF16: torch.bfloat16, FP16: torch.float16, FP8_E4M3: torch.float8
 NVFP4_ROW_BYTES = 72
 
 FLAG_NAMES = {1: "SEL_RANGE", 2: "SEL_DUP", 4: "PAGE", 8: "CAUSAL_LEN", 16: "LEN", 32: "TIMEOUT",
-              64: "SCHEDULE", 128: "CU"}
+              64: "SCHEDULE", 128: "CU", 256: "POS", 512: "GROUP"}
 STATUS_NAMES = {0: "MXSA_OK", 1: "MXSA_ERR_INVALID_ARG", 2: "MXSA_ERR_UNSUPPORTED", 3: "MXSA_ERR_WORKSPACE",
                 4: "MXSA_ERR_CUDA", 5: "MXSA_ERR_DATA"}
 EXPORTED = ["mxsa_version", "mxsa_status_string", "mxsa_workspace_size", "mxsa_build_index", "mxsa_schedule",
@@ -45,7 +45,7 @@ EXPORTED = ["mxsa_version", "mxsa_status_string", "mxsa_workspace_size", "mxsa_b
             "mxsa_kvouter_fwd", "mxsa_combine", "mxsa_read_status", "mxsa_index_layout_query",
             "mxsa_sched_layout_query", "mxsa_store_kv", "mxsa_dense_fwd", "mxsa_select_workspace_size",
             "mxsa_select_blocks", "mxsa_dedup_workspace_size", "mxsa_build_index_dedup",
-            "mxsa_attention_noalloc", "mxsa_noalloc_read_status"]
+            "mxsa_attention_noalloc", "mxsa_noalloc_read_status", "mxsa_load_kv", "mxsa_norm_rope_store"]
 
 
 class MxsaError(RuntimeError):
@@ -82,6 +82,13 @@ class SchedLayout(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("items_cap", "tiles_cap")]
 
 
+class NormRope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "idx_q_stride", "idx_k_stride",
+                                              "num_positions")] + \
+               [(n, ctypes.c_int32) for n in ("rot_dim", "interleaved", "weight_per_head", "idx_dim")] + \
+               [("eps", ctypes.c_float)]
+
+
 def _load_library(path: Optional[str] = None) -> ctypes.CDLL:
     path = path or LIB_PATH
     if not os.path.exists(path):
@@ -110,6 +117,8 @@ def _load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "mxsa_build_index_dedup": [P, P, P, P, P, P, S, P, S, P],
         "mxsa_attention_noalloc": [P] * 11,
         "mxsa_noalloc_read_status": [P, P],
+        "mxsa_load_kv": [P, ctypes.c_int64, P, P, P, P, P, P, P, ctypes.c_int32, ctypes.c_int32, P, P],
+        "mxsa_norm_rope_store": [P, P, ctypes.c_int64] + [P] * 19,
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -301,6 +310,104 @@ def store_kv(prob, loc, k, v, k_cache, v_cache, idx_k=None, idx_cache=None, flag
     _need(what, "flags", flags, 4)
     _check(_lib.mxsa_store_kv(ctypes.byref(prob), n, _ptr(loc), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
                               _ptr(idx_k), _ptr(idx_cache), ih, idim, _ptr(flags), _stream(stream)), "mxsa_store_kv")
+
+
+def load_kv(prob, loc, k_cache, v_cache, k, v, idx_cache=None, idx_k=None, flags=None, stream=None):
+    """Paged-cache load, store_kv's other direction: the rows of slots loc
+    (int64 [n], page * page_size + offset; < 0: those rows of k and v are left
+    as they are) widened exactly into k, v ([n, Hkv, 128], the problem's q
+    dtype) and optionally idx_k ([n, idx_heads, idx_dim]).  flags: optional
+    int32 device tensor that receives MXSA_FLAG_PAGE for slots past the
+    cache."""
+    n = loc.numel()
+    ih, idim = (int(idx_k.shape[1]), int(idx_k.shape[2])) if idx_k is not None else (0, 0)
+    what = "mxsa_load_kv"
+    qb, kb = _ELEM_BYTES.get(prob.q_dtype, 2), _ELEM_BYTES.get(prob.kv_dtype, 2)
+    _need(what, "loc", loc, n * 8)
+    _need(what, "k", k, n * prob.num_kv_heads * 128 * qb)
+    _need(what, "v", v, n * prob.num_kv_heads * 128 * qb)
+    cache = max(prob.num_pages, 0) * max(prob.num_kv_heads, 0) * max(prob.page_size, 0)
+    _need(what, "k_cache", k_cache, cache * _ROW_BYTES.get(prob.kv_dtype, 256))
+    _need(what, "v_cache", v_cache, cache * _ROW_BYTES.get(prob.kv_dtype, 256))
+    _need(what, "idx_k", idx_k, n * ih * idim * qb)
+    _need(what, "idx_cache", idx_cache, max(prob.num_pages, 0) * ih * max(prob.page_size, 0) * idim * kb)
+    _need(what, "flags", flags, 4)
+    _check(_lib.mxsa_load_kv(ctypes.byref(prob), n, _ptr(loc), _ptr(k_cache), _ptr(v_cache), _ptr(k), _ptr(v),
+                             _ptr(idx_cache), _ptr(idx_k), ih, idim, _ptr(flags), _stream(stream)), what)
+
+
+def _token_stride(what: str, name: str, t: torch.Tensor, n: int, heads: int, dim: int) -> int:
+    """Elements between the tokens of t [n, heads, dim], a dense tensor or a
+    view of a packed projection (a token's heads next to each other)."""
+    if tuple(t.shape) != (n, heads, dim) or t.element_size() != 2:
+        raise MxsaError(1, f"{what}: {name} is {tuple(t.shape)} of {t.dtype}, the problem needs "
+                           f"{(n, heads, dim)} of a 16-bit type")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != dim):
+        raise MxsaError(1, f"{what}: the heads of {name} are not next to each other")
+    return st[0] if n > 1 else heads * dim
+
+
+def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_cache, q_weight=None, k_weight=None,
+                    eps=1e-6, interleaved=False, idx_q=None, idx_k=None, idx_q_weight=None, idx_k_weight=None,
+                    idx_q_out=None, idx_cache=None, flags=None, stream=None):
+    """RMS norm of every query and key head, rotation by position and the
+    paged-cache store in one launch (mxsa_norm_rope_store).
+
+    q [n, Hq, 128], k and v [n, Hkv, 128] in the problem's q dtype, dense or
+    views of one packed projection; q_out [n, Hq, 128] (may be q when it is
+    dense); cos_sin float32 [positions, rot_dim]: a position's cosines, then
+    its sines; positions, loc int64 [n] (positions < 0: padding).  Weights
+    [128] or per head [heads, 128] (all of one form; None: no norm of those
+    rows).  Index rows, all four or none: idx_q, idx_k [n, Hkv, 64 or 128],
+    idx_q_out of the same shape in the cache dtype, idx_cache.  flags:
+    optional int32 device tensor (MXSA_FLAG_POS, MXSA_FLAG_PAGE)."""
+    what = "mxsa_norm_rope_store"
+    n, hq, hkv = loc.numel(), prob.num_q_heads, prob.num_kv_heads
+    kb = _ELEM_BYTES.get(prob.kv_dtype, 2)
+    cfg = NormRope()
+    cfg.q_stride = _token_stride(what, "q", q, n, hq, 128)
+    cfg.k_stride = _token_stride(what, "k", k, n, hkv, 128)
+    cfg.v_stride = _token_stride(what, "v", v, n, hkv, 128)
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+        raise MxsaError(1, f"{what}: cos_sin must be float32 [positions, rot_dim]")
+    cfg.num_positions, cfg.rot_dim = cos_sin.shape
+    _need(what, "cos_sin", cos_sin, 0)
+    _need(what, "positions", positions, n * 8)
+    _need(what, "loc", loc, n * 8)
+    _need(what, "q_out", q_out, n * hq * 256)
+    rows = max(prob.num_pages, 0) * max(hkv, 0) * max(prob.page_size, 0)
+    _need(what, "k_cache", k_cache, rows * _ROW_BYTES.get(prob.kv_dtype, 256))
+    _need(what, "v_cache", v_cache, rows * _ROW_BYTES.get(prob.kv_dtype, 256))
+    idx = 0
+    if idx_q is not None or idx_k is not None:
+        if idx_q is None or idx_k is None or idx_q_out is None or idx_cache is None:
+            raise MxsaError(1, f"{what}: idx_q, idx_k, idx_q_out and idx_cache come together")
+        idx = int(idx_q.shape[-1])
+        cfg.idx_q_stride = _token_stride(what, "idx_q", idx_q, n, hkv, idx)
+        cfg.idx_k_stride = _token_stride(what, "idx_k", idx_k, n, hkv, idx)
+        _need(what, "idx_q_out", idx_q_out, n * hkv * idx * kb)
+        _need(what, "idx_cache", idx_cache, rows * idx * kb)
+    cfg.idx_dim, cfg.interleaved, cfg.eps = idx, int(bool(interleaved)), eps
+    per_head = None
+    for name, w, heads, dim in (("q_weight", q_weight, hq, 128), ("k_weight", k_weight, hkv, 128),
+                                ("idx_q_weight", idx_q_weight, hkv, idx), ("idx_k_weight", idx_k_weight, hkv, idx)):
+        if w is None:
+            continue
+        ph = w.dim() == 2
+        if per_head not in (None, ph) or tuple(w.shape) != ((heads, dim) if ph else (dim,)):
+            raise MxsaError(1, f"{what}: {name} is {tuple(w.shape)}: all weights are [dim], or all [heads, dim]")
+        if w.element_size() != 2:
+            raise MxsaError(1, f"{what}: {name} is {w.dtype}: the weights have the query's type")
+        _need(what, name, w, 0)
+        per_head = ph
+    cfg.weight_per_head = int(bool(per_head))
+    _need(what, "flags", flags, 4)
+    _check(_lib.mxsa_norm_rope_store(ctypes.byref(prob), ctypes.byref(cfg), n, _ptr(positions), _ptr(loc),
+                                     _ptr(cos_sin), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight),
+                                     _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(idx_q), _ptr(idx_k),
+                                     _ptr(idx_q_weight), _ptr(idx_k_weight), _ptr(idx_q_out), _ptr(idx_cache),
+                                     _ptr(flags), _stream(stream)), what)
 
 
 def select_workspace_size(prob: Problem, idx_dim: int) -> int:

@@ -460,6 +460,66 @@ mxsa_status mxsa_store_kv(const mxsa_problem* problem, int64_t n_tokens, const i
   return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
 }
 
+mxsa_status mxsa_load_kv(const mxsa_problem* problem, int64_t n_tokens, const int64_t* loc, const void* k_cache,
+                         const void* v_cache, void* k, void* v, const void* idx_cache, void* idx_k,
+                         int32_t idx_heads, int32_t idx_dim, int32_t* device_flags, void* stream) {
+  if (!problem) return MXSA_ERR_INVALID_ARG;
+  mxsa_status s = validate_shape(*problem);
+  if (s != MXSA_OK) return s;
+  const mxsa_problem& p = *problem;
+  if (n_tokens < 0 || (idx_k == nullptr) != (idx_cache == nullptr)) return MXSA_ERR_INVALID_ARG;
+  if (p.kv_dtype == MXSA_NVFP4 && idx_k) return MXSA_ERR_UNSUPPORTED;  // index keys stay 16-bit or FP8
+  if (idx_k && (idx_heads <= 0 || idx_dim <= 0 || idx_dim % 8 != 0)) return MXSA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!loc || !k || !v || !k_cache || !v_cache)) return MXSA_ERR_INVALID_ARG;
+  if (!aligned(loc, 8) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(idx_k, 16) || !aligned(idx_cache, 16) || !aligned(device_flags, 4))
+    return MXSA_ERR_INVALID_ARG;
+  cudaError_t e = launch_load(p, n_tokens, loc, k_cache, v_cache, k, v, idx_cache, idx_k, idx_heads, idx_dim,
+                              device_flags, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
+}
+
+mxsa_status mxsa_norm_rope_store(const mxsa_problem* problem, const mxsa_norm_rope* cfg, int64_t n_tokens,
+                                 const int64_t* positions, const int64_t* loc, const float* cos_sin, const void* q,
+                                 const void* k, const void* v, const void* q_weight, const void* k_weight,
+                                 void* q_out, void* k_cache, void* v_cache, const void* idx_q, const void* idx_k,
+                                 const void* idx_q_weight, const void* idx_k_weight, void* idx_q_out,
+                                 void* idx_cache, int32_t* device_flags, void* stream) {
+  if (!problem || !cfg) return MXSA_ERR_INVALID_ARG;
+  mxsa_status s = validate_shape(*problem);
+  if (s != MXSA_OK) return s;
+  const mxsa_problem& p = *problem;
+  const mxsa_norm_rope& c = *cfg;
+  if (n_tokens < 0 || !(c.eps >= 0.f) || !std::isfinite(c.eps) || c.num_positions < 1 ||
+      (c.interleaved != 0 && c.interleaved != 1) || (c.weight_per_head != 0 && c.weight_per_head != 1))
+    return MXSA_ERR_INVALID_ARG;
+  if (c.rot_dim < 16 || c.rot_dim > 128 || c.rot_dim % 16 != 0) return MXSA_ERR_UNSUPPORTED;
+  const bool idx = c.idx_dim != 0;
+  if (idx && c.idx_dim != 64 && c.idx_dim != 128) return MXSA_ERR_UNSUPPORTED;
+  if (idx && p.kv_dtype == MXSA_NVFP4) return MXSA_ERR_UNSUPPORTED;  // index keys stay 16-bit or FP8
+  if (idx && c.rot_dim > c.idx_dim) return MXSA_ERR_INVALID_ARG;
+  if (!idx && (idx_q || idx_k || idx_q_weight || idx_k_weight || idx_q_out || idx_cache)) return MXSA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && (!positions || !loc || !cos_sin || !q || !k || !v || !q_out || !k_cache || !v_cache))
+    return MXSA_ERR_INVALID_ARG;
+  if (n_tokens > 0 && idx && (!idx_q || !idx_k || !idx_q_out || !idx_cache)) return MXSA_ERR_INVALID_ARG;
+  auto stride_ok = [](int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0; };
+  if (!stride_ok(c.q_stride, p.num_q_heads * 128LL) || !stride_ok(c.k_stride, p.num_kv_heads * 128LL) ||
+      !stride_ok(c.v_stride, p.num_kv_heads * 128LL))
+    return MXSA_ERR_INVALID_ARG;
+  if (idx && (!stride_ok(c.idx_q_stride, (int64_t)p.num_kv_heads * c.idx_dim) ||
+              !stride_ok(c.idx_k_stride, (int64_t)p.num_kv_heads * c.idx_dim)))
+    return MXSA_ERR_INVALID_ARG;
+  for (const void* x : {q, k, v, q_weight, k_weight, (const void*)q_out, (const void*)k_cache, (const void*)v_cache,
+                        idx_q, idx_k, idx_q_weight, idx_k_weight, (const void*)idx_q_out, (const void*)idx_cache,
+                        (const void*)cos_sin})
+    if (!aligned(x, 16)) return MXSA_ERR_INVALID_ARG;
+  if (!aligned(positions, 8) || !aligned(loc, 8) || !aligned(device_flags, 4)) return MXSA_ERR_INVALID_ARG;
+  const NormRopePtrs b{positions, loc,   cos_sin,  q,     k,     v,            q_weight,     k_weight,  q_out,
+                       k_cache,   v_cache, idx_q,  idx_k, idx_q_weight, idx_k_weight, idx_q_out, idx_cache, device_flags};
+  cudaError_t e = launch_norm_rope(p, c, b, n_tokens, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
+}
+
 // Shape checks of the top-k selection: the sparse problem's (topk, sizes)
 // plus the selection's own limits.
 static mxsa_status validate_select(const mxsa_problem& p, int32_t idx_dim) {

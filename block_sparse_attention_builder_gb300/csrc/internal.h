@@ -174,6 +174,21 @@ cudaError_t launch_dense(const mxsa_problem& p, const void* q, const void* k_cac
 cudaError_t launch_store(const mxsa_problem& p, long long n, const int64_t* loc, const void* k, const void* v,
                          void* k_cache, void* v_cache, const void* idx_k, void* idx_cache, int idx_heads,
                          int idx_dim, int32_t* flags, cudaStream_t st);
+cudaError_t launch_load(const mxsa_problem& p, long long n, const int64_t* loc, const void* k_cache,
+                        const void* v_cache, void* k, void* v, const void* idx_cache, void* idx_k, int idx_heads,
+                        int idx_dim, int32_t* flags, cudaStream_t st);
+// Buffers of mxsa_norm_rope_store (the entry point's arguments).
+struct NormRopePtrs {
+  const int64_t *positions, *loc;
+  const float* cos_sin;
+  const void *q, *k, *v, *q_weight, *k_weight;
+  void *q_out, *k_cache, *v_cache;
+  const void *idx_q, *idx_k, *idx_q_weight, *idx_k_weight;
+  void *idx_q_out, *idx_cache;
+  int32_t* flags;
+};
+cudaError_t launch_norm_rope(const mxsa_problem& p, const mxsa_norm_rope& cfg, const NormRopePtrs& b, long long n,
+                             cudaStream_t st);
 size_t select_score_bytes(const mxsa_problem& p);
 size_t select_workspace_bytes(const mxsa_problem& p);
 cudaError_t launch_select(const mxsa_problem& p, int idx_dim, const void* iq, const void* ik, const int32_t* bt,
@@ -182,6 +197,14 @@ cudaError_t launch_select(const mxsa_problem& p, int idx_dim, const void* iq, co
 cudaError_t launch_combine(const mxsa_problem& p, const IndexPtrs& ix, const void* part_o,
                            const float* part_lse, void* out, float* lse, cudaStream_t st);
 
+
+// log2(x) when x is a power of two, else -1
+inline int log2_exact(int x) {
+  if (x <= 0 || (x & (x - 1))) return -1;
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
 
 // Launch with programmatic stream serialization: the kernel may be scheduled
 // while the previous kernel on the stream finishes; it waits for that

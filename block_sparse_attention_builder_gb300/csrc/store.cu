@@ -11,11 +11,10 @@
 // an e4m3 cache the values are converted two at a time with the saturating
 // round-to-nearest-even conversion (448 is the largest finite e4m3fn value,
 // so saturating equals clamping first); NaN keeps the sign of its source.
-#include <cuda_fp16.h>
-
 #include <algorithm>
 #include <climits>
 
+#include "cast.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -35,63 +34,6 @@ struct StoreArgs {
   int32_t page_shift, fp8, bf16;
   int32_t* flags;          // may be null
 };
-
-__device__ __forceinline__ float to_f32(uint16_t bits, int bf16) {
-  return bf16 ? __uint_as_float((uint32_t)bits << 16) : __half2float(__ushort_as_half(bits));
-}
-
-// e4m3 codes of two source values (raw 16-bit words b0, b1), b0's in the
-// low byte (no NaN among them)
-__device__ __forceinline__ uint32_t e4m3x2(uint16_t b0, uint16_t b1, int bf16) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(to_f32(b1, bf16)), "f"(to_f32(b0, bf16)));
-  return r;
-}
-
-// the same, for a 16-bit word that may be a NaN: the code takes the NaN's
-// sign from the source bits (the fp16 -> f32 conversion does not keep it)
-__device__ __forceinline__ uint32_t e4m3_nan_aware(uint16_t b, int bf16) {
-  const bool nan = (b & 0x7FFFu) > (bf16 ? 0x7F80u : 0x7C00u);
-  return nan ? ((b & 0x8000u) ? 0xFFu : 0x7Fu) : (e4m3x2(b, 0, bf16) & 0xFFu);
-}
-
-// any NaN among the eight 16-bit values of s
-__device__ __forceinline__ bool any_nan(const uint4& s, int bf16) {
-  const uint32_t thr = bf16 ? 0x7F807F80u : 0x7C007C00u;
-  const uint32_t w[4] = {s.x, s.y, s.z, s.w};
-  uint32_t hit = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) hit |= __vcmpgtu2(w[i] & 0x7FFF7FFFu, thr);
-  return hit != 0;
-}
-
-// one 16-byte source chunk s (8 values) to its destination: 8 e4m3 bytes or
-// the 16 bytes themselves
-__device__ __forceinline__ void put_chunk(const uint4& s, uint8_t* dst, long long dst_elem, int fp8, int bf16) {
-  if (fp8) {
-    uint32_t o[2];
-    if (!any_nan(s, bf16)) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t x = i ? s.z : s.x, y = i ? s.w : s.y;
-        o[i] = e4m3x2((uint16_t)(x & 0xFFFFu), (uint16_t)(x >> 16), bf16) |
-               (e4m3x2((uint16_t)(y & 0xFFFFu), (uint16_t)(y >> 16), bf16) << 16);
-      }
-    } else {
-      const uint32_t w4[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        o[i] = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          o[i] |= e4m3_nan_aware((uint16_t)(w4[2 * i + b / 2] >> (16 * (b & 1))), bf16) << (8 * b);
-      }
-    }
-    *reinterpret_cast<uint2*>(dst + dst_elem) = make_uint2(o[0], o[1]);
-  } else {
-    *reinterpret_cast<uint4*>(dst + 2 * dst_elem) = s;
-  }
-}
 
 // Units: first the K/V chunks (one thread stores the same chunk of K and of
 // V, which share their token, head and destination offset), then the index
@@ -140,23 +82,6 @@ __global__ void __launch_bounds__(256) k_store(StoreArgs a) {
 // to the even code, saturating at 6, with the quotient's sign; NaN elements
 // (which amax ignores) and groups whose scale is 0 store code 0.
 
-// E2M1 code of y: the comparisons put each tie on the even magnitude index
-// (0.25 -> 0, 0.75 and 1.25 -> 1.0, 1.75 and 2.5 -> 2, 3.5 and 5 -> 4)
-__device__ __forceinline__ uint32_t e2m1_code(float y) {
-  const uint32_t sign = (__float_as_uint(y) >> 31) << 3;
-  const float a = fabsf(y);
-  uint32_t i;
-  if (a <= 0.25f) i = 0;
-  else if (a < 0.75f) i = 1;
-  else if (a <= 1.25f) i = 2;
-  else if (a < 1.75f) i = 3;
-  else if (a <= 2.5f) i = 4;
-  else if (a < 3.5f) i = 5;
-  else if (a <= 5.0f) i = 6;
-  else i = 7;
-  return sign | i;
-}
-
 struct StoreFp4Args {
   const int64_t* loc;
   const uint16_t* src[2];  // K, V of this launch's first token
@@ -181,16 +106,12 @@ __device__ __forceinline__ void put_group_fp4(const uint16_t* src, uint8_t* code
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));  // fmaxf drops a NaN operand
-  uint16_t sc;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(sc) : "f"(0.f), "f"(__fdiv_rn(amax, 6.f)));
-  sc &= 0xFFu;
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(sc));
-  const float sd = __half2float(__ushort_as_half((uint16_t)(h2 & 0xFFFFu)));
+  float sd;
+  const uint32_t sc = nvfp4_scale(amax, &sd);
   uint32_t lo = 0, hi = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const uint32_t c = (sd == 0.f || isnan(x[i])) ? 0u : e2m1_code(__fdiv_rn(x[i], sd));
+    const uint32_t c = nvfp4_code(x[i], sd);
     if (i < 8) lo |= c << (4 * i);
     else hi |= c << (4 * (i - 8));
   }
@@ -221,14 +142,6 @@ __global__ void __launch_bounds__(256) k_store_fp4(StoreFp4Args a) {
 }
 
 }  // namespace
-
-// log2(x) when x is a power of two, else -1
-static int log2_exact(int x) {
-  if (x <= 0 || (x & (x - 1))) return -1;
-  int s = 0;
-  while ((1 << s) < x) ++s;
-  return s;
-}
 
 cudaError_t launch_store(const mxsa_problem& p, long long n, const int64_t* loc, const void* k, const void* v,
                          void* k_cache, void* v_cache, const void* idx_k, void* idx_cache, int idx_heads,

@@ -77,6 +77,8 @@ typedef enum { MXSA_BF16 = 0, MXSA_FP16 = 1, MXSA_FP8_E4M3 = 2, MXSA_NVFP4 = 3 }
 #define MXSA_FLAG_TIMEOUT 32    /* an on-device wait gave up (result undefined) */
 #define MXSA_FLAG_SCHEDULE 64   /* schedule and forward disagree on the CTA count */
 #define MXSA_FLAG_CU 128        /* cu_seqlens_q is not a non-decreasing partition of total_q */
+#define MXSA_FLAG_POS 256       /* a token's position lies past the rotation table: token left out */
+#define MXSA_FLAG_GROUP 512     /* group_ptr is not a non-decreasing list of sequences: groups ignored */
 
 /* Problem description (sizes and flags of one call).  The sources: the
  * Quick-start signature and the supported-feature list of the
@@ -274,6 +276,77 @@ mxsa_status mxsa_dense_fwd(const mxsa_problem* problem, const void* q, const voi
 mxsa_status mxsa_store_kv(const mxsa_problem* problem, int64_t n_tokens, const int64_t* loc, const void* k,
                           const void* v, void* k_cache, void* v_cache, const void* idx_k, void* idx_cache,
                           int32_t idx_heads, int32_t idx_dim, int32_t* device_flags, void* stream);
+
+/* Paged-cache load, the read side of mxsa_store_kv (this library's own; no
+ * passage): for each of n_tokens slots loc[t] = page * page_size + offset
+ * (device int64; loc[t] < 0: the token's rows are left as they are)
+ *   k[t][h][:] = widen(k_cache[page][h][offset][:]) and likewise v, h < Hkv;
+ *   idx_k[t][j][:] = widen(idx_cache[page][j][offset][:]), j < idx_heads,
+ * into [n_tokens][heads][dim] rows of problem->q_dtype (BF16 or FP16).  The
+ * widening is exact: 16-bit caches are copied bit for bit, e4m3 values and
+ * the NVFP4 products e2m1 * scale are values of both 16-bit types (a NaN
+ * code or scale gives NaN).  The way from a quantised cache to the calls
+ * that take 16-bit keys (mxsa_dense_fwd, mxsa_dense_shared_fwd), to another
+ * cache type (mxsa_store_kv of the rows), or to a host.  A slot may occur
+ * several times.
+ * Of the problem, the load reads what the store reads; the index arguments
+ * (both NULL or both set, no NVFP4) and device_flags (MXSA_FLAG_PAGE: a slot
+ * past the cache, its token left as it is) are the store's too.
+ * Device pointers, 16-byte aligned (loc 8-byte); the outputs must not overlap
+ * the caches.  One launch, asynchronous on `stream`; MXSA_ERR_INVALID_ARG /
+ * MXSA_ERR_UNSUPPORTED for bad arguments, before any launch. */
+mxsa_status mxsa_load_kv(const mxsa_problem* problem, int64_t n_tokens, const int64_t* loc, const void* k_cache,
+                         const void* v_cache, void* k, void* v, const void* idx_cache, void* idx_k,
+                         int32_t idx_heads, int32_t idx_dim, int32_t* device_flags, void* stream);
+
+/* The prologue of an attention layer (this library's own; no passage): the
+ * RMS norm of every query and key head, the rotation by position and the
+ * paged-cache store in one pass over a projection's output.  A head row x of
+ * D values (D = 128; index rows: idx_dim) with weight row w becomes
+ *   y_i = x_i / sqrt((1/D) sum x_j^2 + eps) * w_i      (no norm when w is NULL)
+ *   (y_a, y_b) <- (y_a c_i - y_b s_i, y_b c_i + y_a s_i),  i < rot_dim / 2,
+ * (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved; columns
+ * from rot_dim on are not rotated.  c_i and s_i are cos_sin[pos][i] and
+ * cos_sin[pos][rot_dim / 2 + i], pos = positions[t].  All in FP32 (so rows
+ * whose squares sum past FP32's range give 0), rounded once:
+ *   q_out[t][h][:]     = the row of q[t][h], in q_dtype, dense;
+ *   k_cache, v_cache   = the rows of k, and v as it is, at slot loc[t], with
+ *                        mxsa_store_kv's casts (applied to the FP32 row of k);
+ *   idx_q_out[t][g][:] = the row of idx_q[t][g], in kv_dtype, dense (what
+ *                        mxsa_select_blocks takes), g < Hkv;
+ *   idx_cache          = the rows of idx_k, at slot loc[t], in kv_dtype.
+ * q, k, v, idx_q and idx_k are in q_dtype, the heads of a token next to each
+ * other and the tokens *_stride elements apart (a multiple of 8, at least
+ * heads * D), so they may be views of one packed projection.  Weights are in
+ * q_dtype: [D], or [heads][D] when weight_per_head.
+ * A token with positions[t] < 0 is padding: nothing of it is written.  One
+ * at or past num_positions is left out too and sets MXSA_FLAG_POS.  loc[t] <
+ * 0: its k, v and idx_k are not stored; past the cache: the same, and
+ * MXSA_FLAG_PAGE.  Slots that occur twice get one token's rows, column by
+ * column (each 16-byte piece of one of them).
+ * idx_dim 0: the idx_* pointers are NULL; else 64 or 128, none of idx_q,
+ * idx_k, idx_q_out, idx_cache NULL, rot_dim <= idx_dim, kv_dtype not NVFP4.
+ * Of the problem, the call reads what mxsa_store_kv reads and num_q_heads.
+ * q_out may be q itself when q is dense; no other output may overlap an
+ * input.  Device pointers, 16-byte aligned (positions, loc 8-byte).  One
+ * launch, asynchronous on `stream`; MXSA_ERR_INVALID_ARG /
+ * MXSA_ERR_UNSUPPORTED before any launch. */
+typedef struct {
+  int64_t q_stride, k_stride, v_stride; /* elements between tokens */
+  int64_t idx_q_stride, idx_k_stride;
+  int64_t num_positions;                /* rows of cos_sin, >= 1 */
+  int32_t rot_dim;                      /* a multiple of 16, 16..128 */
+  int32_t interleaved;                  /* 0 or 1 */
+  int32_t weight_per_head;              /* 0 or 1 */
+  int32_t idx_dim;                      /* 0 (none), 64 or 128 */
+  float eps;                            /* >= 0 */
+} mxsa_norm_rope;
+mxsa_status mxsa_norm_rope_store(const mxsa_problem* problem, const mxsa_norm_rope* cfg, int64_t n_tokens,
+                                 const int64_t* positions, const int64_t* loc, const float* cos_sin, const void* q,
+                                 const void* k, const void* v, const void* q_weight, const void* k_weight,
+                                 void* q_out, void* k_cache, void* v_cache, const void* idx_q, const void* idx_k,
+                                 const void* idx_q_weight, const void* idx_k_weight, void* idx_q_out,
+                                 void* idx_cache, int32_t* device_flags, void* stream);
 
 /* Top-k block selection, the step before mxsa_build_index: which 128-token
  * blocks each (token, kv head) row attends to.  The MSA summary page ("How
