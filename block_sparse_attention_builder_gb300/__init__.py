@@ -45,7 +45,8 @@ EXPORTED = ["mxsa_version", "mxsa_status_string", "mxsa_workspace_size", "mxsa_b
             "mxsa_kvouter_fwd", "mxsa_combine", "mxsa_read_status", "mxsa_index_layout_query",
             "mxsa_sched_layout_query", "mxsa_store_kv", "mxsa_dense_fwd", "mxsa_select_workspace_size",
             "mxsa_select_blocks", "mxsa_dedup_workspace_size", "mxsa_build_index_dedup",
-            "mxsa_attention_noalloc", "mxsa_noalloc_read_status", "mxsa_load_kv", "mxsa_norm_rope_store"]
+            "mxsa_attention_noalloc", "mxsa_noalloc_read_status", "mxsa_load_kv", "mxsa_norm_rope_store",
+            "mxsa_shared_workspace_size", "mxsa_dense_shared_fwd"]
 
 
 class MxsaError(RuntimeError):
@@ -119,6 +120,8 @@ def _load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "mxsa_noalloc_read_status": [P, P],
         "mxsa_load_kv": [P, ctypes.c_int64, P, P, P, P, P, P, P, ctypes.c_int32, ctypes.c_int32, P, P],
         "mxsa_norm_rope_store": [P, P, ctypes.c_int64] + [P] * 19,
+        "mxsa_shared_workspace_size": [P, P],
+        "mxsa_dense_shared_fwd": [P] * 7 + [ctypes.c_int32, P, P, P, S, P, P, P, P],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -289,6 +292,35 @@ def dense_fwd(prob, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_len
     _check(_lib.mxsa_dense_fwd(ctypes.byref(prob), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                _ptr(cu_seqlens_q), _ptr(used_kv_lens), _ptr(out), _ptr(lse), _ptr(flags),
                                _stream(stream)), "mxsa_dense_fwd")
+
+
+def dense_shared_workspace_size(prob: Problem) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.mxsa_shared_workspace_size(ctypes.byref(prob), ctypes.byref(n)), "mxsa_shared_workspace_size")
+    return n.value
+
+
+def dense_shared_fwd(prob, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens, group_ptr, prefix_lens, ws,
+                     out, lse=None, flags=None, stream=None):
+    """dense_fwd for a batch whose sequences share prefixes: the first
+    prefix_lens[j] keys of sequences group_ptr[j] .. group_ptr[j + 1] - 1 are
+    read once, through the first one's block table row (int32 [groups + 1] and
+    [groups]; both None: no groups, which still splits long sequences over
+    the GPU).  ws: uint8 device tensor of dense_shared_workspace_size bytes."""
+    what = "mxsa_dense_shared_fwd"
+    if (group_ptr is None) != (prefix_lens is None):
+        raise MxsaError(1, f"{what}: group_ptr and prefix_lens come together")
+    ng = 0 if prefix_lens is None else prefix_lens.numel()
+    _need_attention(what, prob, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                    cu_seqlens_q=cu_seqlens_q, used_kv_lens=used_kv_lens, out=out, lse=lse)
+    _need(what, "group_ptr", group_ptr, (ng + 1) * 4)
+    _need(what, "prefix_lens", prefix_lens, ng * 4)
+    _need(what, "ws", ws, 0)
+    _need(what, "flags", flags, 4)
+    _check(_lib.mxsa_dense_shared_fwd(ctypes.byref(prob), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                                      _ptr(cu_seqlens_q), _ptr(used_kv_lens), ng, _ptr(group_ptr), _ptr(prefix_lens),
+                                      _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), _ptr(lse), _ptr(flags),
+                                      _stream(stream)), what)
 
 
 def store_kv(prob, loc, k, v, k_cache, v_cache, idx_k=None, idx_cache=None, flags=None, stream=None):

@@ -441,6 +441,48 @@ mxsa_status mxsa_dense_fwd(const mxsa_problem* problem, const void* q, const voi
   return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
 }
 
+// Shape checks of the dense path over shared prefixes.
+static mxsa_status validate_shared(const mxsa_problem& p) {
+  mxsa_status s = validate_shape(p);
+  if (s != MXSA_OK) return s;
+  if (p.kv_dtype != p.q_dtype || p.num_seqs > 1024) return MXSA_ERR_UNSUPPORTED;
+  if ((int64_t)p.total_q * p.num_kv_heads >= (1ll << 31)) return MXSA_ERR_UNSUPPORTED;
+  return MXSA_OK;
+}
+
+mxsa_status mxsa_shared_workspace_size(const mxsa_problem* problem, size_t* shared_bytes) {
+  if (!problem || !shared_bytes) return MXSA_ERR_INVALID_ARG;
+  mxsa_status s = validate_shared(*problem);
+  if (s != MXSA_OK) return s;
+  *shared_bytes = shared_workspace_bytes(*problem);
+  return MXSA_OK;
+}
+
+mxsa_status mxsa_dense_shared_fwd(const mxsa_problem* problem, const void* q, const void* k_cache,
+                                  const void* v_cache, const int32_t* block_tables, const int64_t* cu_seqlens_q,
+                                  const int32_t* used_kv_lens, int32_t num_groups, const int32_t* group_ptr,
+                                  const int32_t* prefix_lens, void* ws, size_t shared_bytes, void* out, float* lse,
+                                  int32_t* device_flags, void* stream) {
+  if (!problem) return MXSA_ERR_INVALID_ARG;
+  mxsa_status s = validate_shared(*problem);
+  if (s != MXSA_OK) return s;
+  const mxsa_problem& p = *problem;
+  if (num_groups < 0 || num_groups > p.num_seqs) return MXSA_ERR_INVALID_ARG;
+  if (!block_tables || !cu_seqlens_q || !used_kv_lens || !ws) return MXSA_ERR_INVALID_ARG;
+  if (num_groups > 0 && (!group_ptr || !prefix_lens)) return MXSA_ERR_INVALID_ARG;
+  if (p.total_q > 0 && (!q || !k_cache || !v_cache || !out)) return MXSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(block_tables, 4) || !aligned(cu_seqlens_q, 8) || !aligned(used_kv_lens, 4) || !aligned(lse, 4) ||
+      !aligned(group_ptr, 4) || !aligned(prefix_lens, 4) || !aligned(ws, 256) || !aligned(device_flags, 4))
+    return MXSA_ERR_INVALID_ARG;
+  if (shared_bytes < shared_workspace_bytes(p)) return MXSA_ERR_WORKSPACE;
+  if (!kernel_writable(out) || !kernel_writable(lse)) return MXSA_ERR_INVALID_ARG;
+  cudaError_t e = launch_dense_shared(p, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens, num_groups,
+                                      num_groups > 0 ? group_ptr : nullptr, prefix_lens, ws, out, lse, device_flags,
+                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
+}
+
 mxsa_status mxsa_store_kv(const mxsa_problem* problem, int64_t n_tokens, const int64_t* loc, const void* k,
                           const void* v, void* k_cache, void* v_cache, const void* idx_k, void* idx_cache,
                           int32_t idx_heads, int32_t idx_dim, int32_t* device_flags, void* stream) {

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(256) k_load(LoadArgs a) {
     const int hs = kv ? a.heads_shift[0] : a.heads_shift[1];
     const uint32_t row = rcs >= 0 ? cc >> rcs : cc / rc, part = cc - row * rc;
     const uint32_t t = hs >= 0 ? row >> hs : row / heads, h = row - t * heads;
-    const long long l = __ldg(a.loc + t);
+    const long long l = a.loc[t];
     if (l < 0) continue;  // the token's rows are left as they are
     if (l >= a.slots) {
       if (a.flags && kv && h == 0 && part == 0) atomicOr(a.flags, MXSA_FLAG_PAGE);

@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_norm_rope(const __grid_constan
 #pragma unroll
   for (int u = 0; u < kRopeRows; ++u) {
     const int h = h0 + u * rpp;
-    raw[u] = live && h < p.heads ? __ldg(reinterpret_cast<const uint4*>(src + (long long)h * p.dim))
+    raw[u] = live && h < p.heads ? *reinterpret_cast<const uint4*>(src + (long long)h * p.dim)
                                  : make_uint4(0, 0, 0, 0);
   }
   const long long pos = a.positions[t];
@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(kRopeThreads) k_norm_rope(const __grid_constan
     const int j = kInter ? e >> 1 : (e < half ? e : e - half);
 #pragma unroll
     for (int i = 0; i < (kInter ? 1 : 2); ++i) {
-      const float4 cv = __ldg(reinterpret_cast<const float4*>(cs + j) + i);
-      const float4 sv = __ldg(reinterpret_cast<const float4*>(cs + half + j) + i);
+      const float4 cv = reinterpret_cast<const float4*>(cs + j)[i];
+      const float4 sv = reinterpret_cast<const float4*>(cs + half + j)[i];
       c[4 * i] = cv.x, c[4 * i + 1] = cv.y, c[4 * i + 2] = cv.z, c[4 * i + 3] = cv.w;
       s[4 * i] = sv.x, s[4 * i + 1] = sv.y, s[4 * i + 2] = sv.z, s[4 * i + 3] = sv.w;
     }
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_norm_rope(const __grid_constan
     if (p.w && row) {
       const uint16_t* wr = p.w + (long long)h * p.w_stride;
       float w[8];
-      unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(wr + e)), w);
+      unpack8<kBf16>(*reinterpret_cast<const uint4*>(wr + e), w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = x[i] * rms * w[i];
     } else {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_norm_rope(const __grid_constan
         unpack8<kBf16>(other, yo);
         if (p.w && row) {
           float w[8];
-          unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(p.w + (long long)h * p.w_stride + pe)), w);
+          unpack8<kBf16>(*reinterpret_cast<const uint4*>(p.w + (long long)h * p.w_stride + pe), w);
 #pragma unroll
           for (int i = 0; i < 8; ++i) yo[i] = yo[i] * rms * w[i];
         }

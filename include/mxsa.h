@@ -246,6 +246,46 @@ mxsa_status mxsa_dense_fwd(const mxsa_problem* problem, const void* q, const voi
                            const int32_t* block_tables, const int64_t* cu_seqlens_q, const int32_t* used_kv_lens,
                            void* out, float* lse, int32_t* device_flags, void* stream);
 
+/* Dense paged attention of a batch whose sequences share prefixes (this
+ * library's own; the plain dense path is mxsa_dense_fwd, the sparse one with
+ * shared blocks mxsa_build_index_dedup): out and lse of mxsa_dense_fwd, each
+ * common key loaded once for all the sequences that have it, and every
+ * sequence's keys split over the whole GPU (also without groups: a batch of
+ * few sequences with many keys).  Group j is the sequences group_ptr[j] <= s <
+ * group_ptr[j + 1]; its prefix is
+ *   P_j = prefix_lens[j], at least 0 and at most the smallest used_kv_len
+ *         among its sequences with new tokens (0 for a group of one sequence);
+ *   keys p < P_j of all its sequences are read through the block_tables row
+ *   of sequence group_ptr[j], keys p >= P_j through their own.
+ * P_j need not fill a block or a page (a page that holds a prefix's end is
+ * read twice, by both ways).  Entries of the other rows for pages wholly
+ * below P_j are not read.  Sequences in no group have no prefix.
+ *   group_ptr    device int32 [num_groups + 1], 0 <= non-decreasing <= B;
+ *                else MXSA_FLAG_GROUP and no group at all
+ *   prefix_lens  device int32 [num_groups]
+ *   num_groups   0 (both may be NULL) .. num_seqs
+ *   ws           device, shared_bytes from mxsa_shared_workspace_size: plan
+ *                and partial rows (FP32); needs no initialisation, keeps
+ *                nothing between calls
+ * The other arguments and limits are mxsa_dense_fwd's: kv_dtype = q_dtype,
+ * num_seqs <= 1024, topk unused; also total_q * num_kv_heads < 2^31.  The
+ * softmax weights are rounded to q_dtype before they multiply V, everything
+ * else is FP32.  A NaN or infinity at a key outside [0, used_kv_len) of a
+ * sequence does not reach its rows; under causal masking the V rows of a
+ * sequence's own later tokens have to be finite.  Results do not depend on
+ * timing: the same call gives the same bits.
+ * cu_seqlens_q must be non-decreasing within [0, total_q], else MXSA_FLAG_CU
+ * and nothing is written; tokens before cu_seqlens_q[0] and from
+ * cu_seqlens_q[B] on are not written.  device_flags (may be NULL) also gets
+ * MXSA_FLAG_LEN (clamped length), MXSA_FLAG_PAGE and MXSA_FLAG_TIMEOUT as
+ * for mxsa_dense_fwd.  Three launches, asynchronous on `stream`. */
+mxsa_status mxsa_shared_workspace_size(const mxsa_problem* problem, size_t* shared_bytes);
+mxsa_status mxsa_dense_shared_fwd(const mxsa_problem* problem, const void* q, const void* k_cache,
+                                  const void* v_cache, const int32_t* block_tables, const int64_t* cu_seqlens_q,
+                                  const int32_t* used_kv_lens, int32_t num_groups, const int32_t* group_ptr,
+                                  const int32_t* prefix_lens, void* ws, size_t shared_bytes, void* out, float* lse,
+                                  int32_t* device_flags, void* stream);
+
 /* Paged-cache store, the write side of the caches the forward reads (a
  * sglang pull request on these pages, "Summary": the fused K/V/index store
  * with an unscaled bf16-to-fp8_e4m3 cast).  For each of n_tokens new tokens

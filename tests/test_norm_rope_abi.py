@@ -129,3 +129,39 @@ def test_binding_refuses_what_the_shapes_rule_out(lib):
         with pytest.raises(mx.MxsaError) as ei:
             mx.load_kv(p, **dict(a, **kw))
         assert ei.value.status == 1
+
+
+def test_dense_shared_arguments(lib):
+    p = _prob(num_seqs=3)
+    nbytes = mx.dense_shared_workspace_size(p)
+
+    def call(prob=p, q=FAKE, k=FAKE, v=FAKE, bt=FAKE, cu=FAKE, lens=FAKE, ng=1, gp=FAKE, pl=FAKE, ws=FAKE, n=nbytes,
+             out=FAKE, lse=None, flags=None):
+        pr = ctypes.byref(prob) if prob is not None else None
+        return lib.mxsa_dense_shared_fwd(pr, q, k, v, bt, cu, lens, ng, gp, pl, ws, n, out, lse, flags, None)
+
+    assert call(prob=None) == 1
+    for name in ("q", "k", "v", "bt", "cu", "lens", "gp", "pl", "ws", "out"):
+        assert call(**{name: None}) == 1, name
+        assert call(**{name: P((1 << 20) + 2)}) == 1, name
+    assert call(ws=P((1 << 20) + 128)) == 1 and call(lse=P((1 << 20) + 2)) == 1 and call(flags=P((1 << 20) + 1)) == 1
+    assert call(ng=-1) == 1 and call(ng=4) == 1
+    assert call(n=nbytes - 1) == 3
+    assert call(prob=_prob(num_seqs=1025)) == 2 and call(prob=_prob(kv_dtype=torch.float8_e4m3fn)) == 2
+    assert call(prob=_prob(num_q_heads=256, num_kv_heads=1)) == 2 and call(prob=_prob(page_size=16)) == 2
+    big = _prob(total_q=(1 << 31) - 1)
+    assert call(prob=big) == 2
+    assert lib.mxsa_shared_workspace_size(ctypes.byref(big), ctypes.byref(ctypes.c_size_t())) == 2
+    assert lib.mxsa_shared_workspace_size(ctypes.byref(p), None) == 1
+    # more tokens, more workspace; the index's limits do not apply
+    assert mx.dense_shared_workspace_size(_prob(total_q=1 << 20, topk=256)) > nbytes
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    cache, i32 = bf(10, 2, 64, 128), lambda *s: torch.zeros(*s, dtype=torch.int32)
+    good = dict(q=bf(4, 16, 128), k_cache=cache, v_cache=cache, block_tables=i32(3, 10),
+                cu_seqlens_q=torch.zeros(4, dtype=torch.int64), used_kv_lens=i32(3), group_ptr=i32(2),
+                prefix_lens=i32(1), ws=torch.zeros(nbytes, dtype=torch.uint8), out=bf(4, 16, 128))
+    for kw in (dict(group_ptr=i32(1)), dict(group_ptr=None), dict(prefix_lens=None), dict(q=bf(3, 16, 128)),
+               dict(out=bf(4, 15, 128)), dict(block_tables=i32(3, 9)), dict(ws=good["ws"][::2])):
+        with pytest.raises(mx.MxsaError) as ei:
+            mx.dense_shared_fwd(p, **dict(good, **kw))
+        assert ei.value.status == 1

@@ -1,0 +1,328 @@
+"""CPU models of the dense path over shared prefixes (mxsa_dense_shared_fwd).
+
+The plan: jobs, tiles, the line of steps and its cut into ranges, restated in
+Python; random problems check that every visible (token, key) pair lies in
+exactly one segment, that a row's partials are distinct and that the tile and
+partial-row bounds that size the workspace hold.
+
+The forward's mbarrier protocol (producer, MMA issuer, two softmax groups,
+five K/V stages, two q buffers) under random interleavings: no deadlock, and
+no buffer is refilled or overwritten before its readers are done.
+"""
+import random
+
+import pytest
+
+from tests.test_barrier_models import Bar
+
+MAXC, WR, WK, STAGES = 160, 2, 1, 5
+
+
+def cdiv(a, b):
+    return -(-a // b)
+
+
+def plan(p):
+    """p: cu, lens, gp, prefix, hkv, hq, causal, ctas.  Returns (jobs, tiles, share)."""
+    G = p["hq"] // p["hkv"]
+    T, B, cu = 128 // G, len(p["lens"]), p["cu"]
+    seq_group, prefix = [-1] * B, []
+    for j, P in enumerate(p["prefix"]):
+        members = range(p["gp"][j], p["gp"][j + 1])
+        P = min([max(P, 0)] + [p["lens"][s] for s in members if cu[s + 1] > cu[s]])
+        prefix.append(P if len(members) > 1 else 0)
+        for s in members:
+            seq_group[s] = j if prefix[j] > 0 else -1
+    jobs = []
+    for s in range(B):
+        jobs.append(dict(tok0=cu[s], ntok=cu[s + 1] - cu[s], lo=prefix[seq_group[s]] if seq_group[s] >= 0 else 0,
+                         hi=p["lens"][s], own=True))
+    for j, P in enumerate(prefix):
+        on = P > 0
+        jobs.append(dict(tok0=cu[p["gp"][j]] if on else 0, ntok=cu[p["gp"][j + 1]] - cu[p["gp"][j]] if on else 0, lo=0,
+                         hi=P, own=False))
+    total = 0
+    for j in jobs:
+        j["nb"] = cdiv(j["hi"], 128) - j["lo"] // 128 if j["ntok"] > 0 and j["hi"] > j["lo"] else 0
+        rem = j["ntok"] % (2 * T)
+        j["nrt"] = cdiv(j["ntok"], 2 * T) if j["nb"] else 0
+        keys = int(0 < rem <= T)
+        j["w"] = WR if j["nrt"] > keys else WK
+        total += p["hkv"] * j["nb"] * ((j["nrt"] - keys) * WR + keys * WK) if j["nb"] else 0
+    goal = max(cdiv(total, p["ctas"]), 1)
+    tiles = []
+    for j in jobs:
+        j["chunk"] = min(cdiv(goal, j["w"]), max(j["nb"], 1))
+        j["nch"] = cdiv(j["nb"], j["chunk"])
+        j["tile0"] = len(tiles)
+        for g in range(p["hkv"]):
+            for ch in range(j["nch"]):
+                for rt in range(j["nrt"]):
+                    ntok = min(2 * T, j["ntok"] - rt * 2 * T)
+                    end = cdiv(j["hi"], 128)
+                    if p["causal"] and j["own"]:
+                        end = min(end, cdiv(max(j["hi"] - j["ntok"] + rt * 2 * T + ntok, 0), 128))
+                    b0 = j["lo"] // 128 + ch * j["chunk"]
+                    tiles.append(dict(tok0=j["tok0"] + rt * 2 * T, ntok=ntok, g=g, lo=j["lo"], hi=j["hi"], b0=b0,
+                                      n=max(min(b0 + j["chunk"], end) - b0, 0), keys=ntok <= T, job=j))
+    cost = 0
+    for t in tiles:
+        t["w"] = WK if t["keys"] else WR
+        t["cost0"] = cost
+        cost += t["n"] * t["w"]
+    share = max(cdiv(cost, p["ctas"]), WR)
+    part = 0
+    for t in tiles:
+        t["cta0"] = t["cost0"] // share
+        t["nseg"] = (t["cost0"] + (t["n"] - 1) * t["w"]) // share - t["cta0"] + 1 if t["n"] else 0
+        assert t["cta0"] + t["nseg"] <= p["ctas"] or t["n"] == 0
+        t["part0"] = part
+        part += t["nseg"] * t["ntok"] * G * (2 if t["keys"] else 1)
+    return jobs, tiles, share, part
+
+
+def cut(t, share, c):
+    at = lambda x: 0 if x <= t["cost0"] else min(cdiv(x - t["cost0"], t["w"]), t["n"])
+    i0, i1 = at(c * share), at((c + 1) * share)
+    return i0, i1 - i0
+
+
+def random_problem(r):
+    hq, hkv = r.choice([(8, 1), (16, 2), (12, 4), (4, 4), (128, 1), (10, 2)])
+    B = r.choice([1, 2, 5, 17, 40])
+    tq = [r.choice([0, 1, 1, 1, 3, r.randint(1, 90)]) for _ in range(B)]
+    off = r.randint(0, 2)
+    cu = [off]
+    for x in tq:
+        cu.append(cu[-1] + x)
+    lens = [r.choice([0, 1, 127, 128, 129, r.randint(1, 6000)]) for _ in range(B)]
+    ng = r.randint(0, min(B, 4))
+    gp = sorted(r.randint(0, B) for _ in range(ng + 1)) if ng else [0]
+    prefix = [r.choice([0, 1, 128, r.randint(-3, 7000)]) for _ in range(ng)]
+    return dict(hq=hq, hkv=hkv, cu=cu, lens=lens, gp=gp, prefix=prefix, causal=r.random() < 0.5,
+                ctas=r.choice([1, 3, 148, 152, 160]), total_q=cu[-1] + r.randint(0, 3))
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_plan_covers_every_key_once_within_its_bounds(seed):
+    p = random_problem(random.Random(seed))
+    G, B = p["hq"] // p["hkv"], len(p["lens"])
+    T = 128 // G
+    jobs, tiles, share, part = plan(p)
+    assert len(tiles) <= p["hkv"] * (2 * (p["total_q"] // (2 * T)) + 2 * B) + 2 * MAXC
+    assert part <= 4 * p["total_q"] * p["hq"] + 256 * 3 * MAXC
+    first, last = {}, {}
+    for i, t in enumerate(tiles):
+        got = 0
+        for k in range(t["nseg"]):
+            c = t["cta0"] + k
+            i0, n = cut(t, share, c)
+            assert n > 0 and i0 == got  # each range between the first and the last holds a step
+            got += n
+            first[c] = min(first.get(c, i), i)
+            last[c] = max(last.get(c, i), i)
+        assert got == t["n"]
+        for c in (t["cta0"] - 1, t["cta0"] + t["nseg"]):
+            assert t["n"] == 0 or cut(t, share, c)[1] == 0
+    # tokens: the key blocks of its tiles, masked, make up its visible keys
+    for s in range(B):
+        for tok in range(p["cu"][s], p["cu"][s + 1]):
+            L = p["lens"][s]
+            see = max(L - (p["cu"][s + 1] - tok) + 1, 0) if p["causal"] else L
+            for g in {0, p["hkv"] - 1}:
+                got, parts = [], 0
+                for t in tiles:
+                    if t["g"] == g and t["tok0"] <= tok < t["tok0"] + t["ntok"] and t["n"]:
+                        got.append((max(t["b0"] * 128, t["lo"]), min((t["b0"] + t["n"]) * 128, t["hi"], see)))
+                        parts += t["nseg"] * (2 if t["keys"] else 1)
+                assert parts <= 2 * (2 + 3 * MAXC)
+                got = sorted(x for x in got if x[1] > x[0])
+                at = 0
+                for lo, hi in got:
+                    assert lo == at
+                    at = hi
+                assert at == min(see, L)
+
+
+def place_k(i):
+    return 0 if i == 0 else 2 * i - 1
+
+
+def place_v(i, n):
+    return 2 * i + 2 if i < n - 1 else 2 * n - 1
+
+
+@pytest.mark.parametrize("n", range(1, 9))
+def test_ring_places_are_the_producers_order(n):
+    order = [place_k(i) if kv == 0 else place_v(i - 1, n) for i in range(n + 1) for kv in range(2)
+             if not (kv == 0 and i >= n) and not (kv == 1 and i == 0)]
+    assert order == list(range(2 * n))
+
+
+def run_protocol(segs, seed):
+    """segs: (blocks, keys, edge) of the CTA's segments; edge: the groups wait for V to clear rows of it."""
+    rnd = random.Random(seed)
+    B, pending = {}, {}
+
+    def bar(n, c=1):
+        B[n] = Bar(n, c)
+
+    for i in range(2):
+        for n in ("q_full", "q_empty", "s_full", "p_full", "o_full", "o_empty"):
+            bar(f"{n}{i}")
+    for i in range(STAGES):
+        bar(f"kv_full{i}")
+        bar(f"kv_empty{i}")
+
+    def later(src, cb):
+        pending.setdefault(src, []).append(cb)
+
+    stage, qbuf = {}, {}          # landed place / q number
+    reads = {}                    # place -> products still to come that read it
+    qreads = {}
+    S, O = [None, None], [None, None]
+    finished = [0, 0]
+
+    def producer():
+        at = qn = 0
+        for n, keys, _ in segs:
+            for _h in range(1 if keys else 2):
+                b = qn & 1
+                yield ("wait", B[f"q_empty{b}"], ((qn >> 1) & 1) ^ 1)
+                assert qn < 2 or qreads[qn - 2] == 0, "q refilled early"
+
+                def land(b=b, qn=qn):
+                    qbuf[b] = qn
+                    B[f"q_full{b}"].arrive()
+                later(f"q{b}", land)
+                qn += 1
+            for x in range(2 * n):
+                st = at % STAGES
+                yield ("wait", B[f"kv_empty{st}"], ((at // STAGES) & 1) ^ 1)
+                assert at < STAGES or reads[at - STAGES] == 0, "stage refilled early"
+
+                def land(st=st, at=at):
+                    stage[st] = at
+                    B[f"kv_full{st}"].arrive()
+                later(f"kv{st}", land)
+                at += 1
+
+    def mma():
+        at = qn = 0
+        npv, no, owed = [0, 0], [0, 0], [None, None]
+
+        def pv(h):
+            pl, firstp, lastp, free = owed[h]
+            owed[h] = None
+            st = pl % STAGES
+            yield ("wait", B[f"p_full{h}"], npv[h] & 1)
+            yield ("wait", B[f"kv_full{st}"], (pl // STAGES) & 1)
+            assert stage[st] == pl and S[h][0] == "P"
+            npv[h] += 1
+            if firstp and no[h]:
+                yield ("wait", B[f"o_empty{h}"], (no[h] - 1) & 1)
+                assert O[h] == "read", "O overwritten before it was read"
+
+            def done(h=h, pl=pl, st=st, free=free, lastp=lastp):
+                assert S[h][0] == "P"
+                S[h] = ("used",)
+                O[h] = "done" if lastp else "acc"
+                reads[pl] -= 1
+                if free:
+                    B[f"kv_empty{st}"].arrive()
+                if lastp:
+                    B[f"o_full{h}"].arrive()
+            later("mma", done)
+            if lastp:
+                no[h] += 1
+
+        for n, keys, _ in segs:
+            for i in range(n):
+                reads[at + place_k(i)] = reads[at + place_v(i, n)] = 1 if keys else 2
+            for x in range(1 if keys else 2):
+                qreads[qn + x] = n
+            for j in range((n + 1) // 2 if keys else n):
+                for h in range(2):
+                    i = 2 * j + h if keys else j
+                    if owed[h]:
+                        yield from pv(h)
+                    if i >= n:
+                        continue
+                    qp, kp = qn if keys else qn + h, at + place_k(i)
+                    st = kp % STAGES
+                    if j == 0:
+                        yield ("wait", B[f"q_full{qp & 1}"], (qp >> 1) & 1)
+                    yield ("wait", B[f"kv_full{st}"], (kp // STAGES) & 1)
+                    assert qbuf[qp & 1] == qp and stage[st] == kp
+                    both = not keys and h == 0
+
+                    def done(h=h, qp=qp, kp=kp, st=st, both=both, end=i == n - 1):
+                        assert S[h] is None or S[h][0] == "used", "S overwritten before its product"
+                        S[h] = ("S",)
+                        reads[kp] -= 1
+                        qreads[qp] -= 1
+                        B[f"s_full{h}"].arrive()
+                        if not both:
+                            B[f"kv_empty{st}"].arrive()
+                        if end:
+                            assert qreads[qp] == 0
+                            B[f"q_empty{qp & 1}"].arrive()
+                    later("mma", done)
+                    owed[h] = (at + place_v(i, n), j == 0, (i + 2 if keys else i + 1) >= n, not both)
+                    yield None
+            at += 2 * n
+            qn += 1 if keys else 2
+        for h in range(2):
+            if owed[h]:
+                yield from pv(h)
+
+    def softmax(h):
+        at = ns = no = 0
+        for n, keys, edge in segs:
+            mine = False
+            for i in range(h if keys else 0, n, 2 if keys else 1):
+                yield ("wait", B[f"s_full{h}"], ns & 1)
+                ns += 1
+                assert S[h] == ("S",)
+                if edge and i in (0, n - 1):
+                    pl = at + place_v(i, n)
+                    yield ("wait", B[f"kv_full{pl % STAGES}"], (pl // STAGES) & 1)
+                    assert stage[pl % STAGES] == pl, "rows cleared in another block's stage"
+                if mine:
+                    assert O[h] == "acc", "O rescaled while a product writes it"
+                S[h] = ("P",)
+                B[f"p_full{h}"].arrive()
+                mine = True
+            at += 2 * n
+            if mine:
+                yield ("wait", B[f"o_full{h}"], no & 1)
+                no += 1
+                assert O[h] == "done"
+                O[h] = "read"
+                B[f"o_empty{h}"].arrive()
+                finished[h] += 1
+
+    roles = {"p": producer(), "m": mma(), "s0": softmax(0), "s1": softmax(1)}
+    blocked = dict.fromkeys(roles)
+    while roles or any(pending.values()):
+        ready = [k for k in roles if blocked[k] is None or blocked[k][1].ready(blocked[k][2])]
+        sources = [k for k, v in pending.items() if v]
+        assert ready or sources, f"deadlock: {segs} {blocked}"
+        k = rnd.choice(ready + sources)
+        if k in sources and k not in roles:
+            pending[k].pop(0)()
+            continue
+        try:
+            blocked[k] = next(roles[k])
+        except StopIteration:
+            del roles[k]
+    assert finished[0] == len(segs) and all(v == 0 for v in reads.values())
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_forward_protocol(seed):
+    r = random.Random(seed)
+    for x in range(8):
+        segs = [(r.choice([1, 1, 2, 3, r.randint(1, 9)]), r.random() < 0.6, r.random() < 0.5)
+                for _ in range(r.randint(1, 7))]
+        run_protocol(segs, seed * 100 + x)
