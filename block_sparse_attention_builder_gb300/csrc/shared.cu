@@ -37,14 +37,15 @@ namespace {
 
 constexpr int kHMaxSeqs = 1024;
 constexpr int kHMaxCtas = 160;     // ranges; workspaces are sized for this many
-constexpr int kHCostRows = 2;      // cost of one block for a tile of two halves
-constexpr int kHCostKeys = 1;      // ... of one half (the halves then split the blocks)
+constexpr int kHCostRows = 4;      // cost of one block for a tile of two halves
+constexpr int kHCostKeys = 2;      // ... of one half (the halves then split the blocks)
+constexpr int kHCostTile = 2;      // a tile's own: its q, the first block's latency, the epilogue
 
 // One tile: keys [128 blk0, 128 (blk0 + nblk)) of [lo, hi) for ntok tokens.
 struct alignas(16) HTile {
   int32_t tok0, ntok, g, row;      // first token, tokens, kv head, block table row
   int32_t lo, hi, blk0, nblk;
-  long long cost0;                 // steps' cost before this tile
+  long long cost0;                 // cost before its first step
   long long part0;                 // first partial row
   int32_t cta0;                    // first range that holds a step of it
   int32_t nseg;                    // ranges that do
@@ -267,7 +268,8 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     j.nrt = nb > 0 ? (j.ntok + T2 - 1) / T2 : 0;
     j.chunk = j.nrt > keys ? kHCostRows : kHCostKeys;  // the cost of a block that sets the chunk, for now
     j.nch = nb;
-    cost += (long long)a.Hkv * nb * ((j.nrt - keys) * kHCostRows + (nb > 0 ? keys * kHCostKeys : 0));
+    if (nb > 0)
+      cost += (long long)a.Hkv * ((j.nrt - keys) * (nb * kHCostRows + kHCostTile) + keys * (nb * kHCostKeys + kHCostTile));
     s.job[q] = j;
   }
   block_scan(cost, s.scan, &total);
@@ -314,7 +316,7 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     t->nblk = max(min(t->blk0 + j.chunk, end) - t->blk0, 0);
     t->keys = t->ntok <= a.T;
     t->pad = 0;
-    return (long long)t->nblk * (t->keys ? kHCostKeys : kHCostRows);
+    return t->nblk ? (long long)t->nblk * (t->keys ? kHCostKeys : kHCostRows) + kHCostTile : 0LL;
   };
   const int tper = (ntiles + kHPlanThreads - 1) / kHPlanThreads;
   const int i0 = min(ntiles, tid * tper), i1 = min(ntiles, (tid + 1) * tper);
@@ -326,6 +328,7 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
   // a tile's ranges: those that hold the start of one of its steps
   auto ranges = [&](HTile* x, long long c0) {
     const int w = x->keys ? kHCostKeys : kHCostRows;
+    c0 += kHCostTile;
     x->cost0 = c0;
     x->cta0 = (int)(c0 / share);
     x->nseg = x->nblk > 0 ? (int)((c0 + (long long)(x->nblk - 1) * w) / share) - x->cta0 + 1 : 0;
@@ -373,18 +376,18 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
 
 // ---------------------------------------------------------------- forward
 // 384 threads: two softmax groups (warps 0-3 and 4-7; thread = TMEM lane =
-// row), a producer warp and an MMA warp, and two warps that only make the
-// last warpgroup whole: it gives registers to the softmax groups, whose
+// row), a producer warp, two MMA issuers, and a warp that only makes the last
+// warpgroup whole: it gives registers to the softmax groups, whose
 // threads hold a row's 128 scores.  A tile of two halves gives each
 // group its own 128 rows over the same blocks; a tile of one half gives both
 // groups the same rows and alternate blocks (each then makes a partial of
 // its own).  Per block: S = q k^T (TMEM), a lazily raised running maximum
 // (raised when a score passes it by 2^8, O in TMEM is then rescaled),
 // P = exp2(S - m) rounded to the 16-bit type over S, l += sum P, O += P V.
-// The issuer's order is P V of group 0, q k^T of its next block, then the
-// same for group 1: while one group runs its softmax the tensor pipe has the
-// other's two products.  S is overwritten by the MMA after the one that
-// reads P from it; both are issued by one thread, which the pipe keeps in
+// Each group has an issuer: P V of a block, then q k^T of the group's next
+// one, so that while one group runs its softmax the tensor pipe has the
+// other's two products.  S is overwritten by the MMA after the one that reads
+// P from it; both are issued by one thread, which the pipe keeps in
 // order.  K and V blocks have a stage of 32 KB each in a ring of five, in the
 // order in which the issuer takes them (K0 K1 V0 K2 V1 ... ), so 160 KB of
 // loads are in flight when the CTA waits for memory.
@@ -395,14 +398,19 @@ constexpr int kHStages = 5;
 constexpr float kHRescale = 8.f;         // log2 units
 constexpr uint32_t kHOffKV = 2 * kHTileBytes;
 constexpr uint32_t kHOffCtrl = kHOffKV + kHStages * kHTileBytes;
-// registers of a softmax thread and of the others: 256 x 208 + 128 x 88 is
+// registers of a softmax thread and of the others: 256 x 216 + 128 x 72 is
 // the launch's 384 x 168
-constexpr int kHSoftmaxRegs = 208, kHOtherRegs = 88;
+constexpr int kHSoftmaxRegs = 216, kHOtherRegs = 72;
 constexpr int kHSmallQ = 4;              // halves of at most this many tokens load their q token by token
 
+// A role may pass over places and q slots of the other group without looking
+// at their barriers.  A parity only tells a phase from the one before, so a
+// stage's (and a q buffer's) uses alternate between two "full" barriers: to
+// mistake a phase a role would have to be two uses ahead of the copies, and
+// each wait comes after one for a copy that was issued later than that.
 struct HCtrl {
-  uint64_t q_full[2], q_empty[2], kv_full[kHStages], kv_empty[kHStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], done;
+  uint64_t q_full[4], q_empty[2], kv_full[2 * kHStages], kv_empty[kHStages];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2], turn[2], done;
   uint32_t tmem_base;
   int32_t abort_flag, local_flags;
 };
@@ -481,6 +489,95 @@ __device__ __forceinline__ void st_global_v8(float* p, const float* v) {
                : "memory");
 }
 
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Low words of the operands' shared-memory descriptors (the high word is the
+// same for all: 1024 bytes between groups of 8 rows, version 1, 128-byte
+// swizzle); the address field counts 16 bytes and does not overflow below.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t saddr) { return saddr >> 4; }
+__device__ __forceinline__ uint32_t desc_mn_major(uint32_t saddr) { return (saddr >> 4) | ((16384u >> 4) << 16); }
+// a value that all lanes hold, in a form the compiler knows to be uniform
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// The eight products over 16 columns each of one block.  S = q k^T: both
+// operands K-major, 64 columns to a 16 KB half, 32 bytes a step.  O (+)= P V:
+// P in TMEM, 8 columns a step, V MN-major, 16 rows (2 KB) a step.
+template <int kStep>
+__device__ __forceinline__ void mma_qk_step(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
+  constexpr int off = ((kStep >> 2) * 16384 + (kStep & 3) * 32) >> 4;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 u, v;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tadd.u32 u, %1, %5;\n\tadd.u32 v, %2, %5;\n\t"
+      "mov.b64 x, {u, %6};\n\tmov.b64 y, {v, %6};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(q), "r"(k), "r"(idesc), "n"(kStep > 0), "n"(off), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_qk(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
+  mma_qk_step<0>(d, q, k, idesc);
+  mma_qk_step<1>(d, q, k, idesc);
+  mma_qk_step<2>(d, q, k, idesc);
+  mma_qk_step<3>(d, q, k, idesc);
+  mma_qk_step<4>(d, q, k, idesc);
+  mma_qk_step<5>(d, q, k, idesc);
+  mma_qk_step<6>(d, q, k, idesc);
+  mma_qk_step<7>(d, q, k, idesc);
+}
+template <int kStep>
+__device__ __forceinline__ void mma_pv_step(uint32_t d, uint32_t tp, uint32_t v, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t.reg .b32 x, v;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tadd.u32 x, %1, %5;\n\tadd.u32 v, %2, %6;\n\tmov.b64 y, {v, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n\t}" ::"r"(d),
+      "r"(tp), "r"(v), "r"(idesc), "r"(acc), "n"(kStep * 8), "n"(kStep * (2048 >> 4)), "r"(kDescHi)
+      : "memory");
+}
+// the first and the second 64 keys
+__device__ __forceinline__ void mma_pv_lo(uint32_t d, uint32_t tp, uint32_t v, uint32_t idesc, uint32_t acc) {
+  mma_pv_step<0>(d, tp, v, idesc, acc);
+  mma_pv_step<1>(d, tp, v, idesc, 1u);
+  mma_pv_step<2>(d, tp, v, idesc, 1u);
+  mma_pv_step<3>(d, tp, v, idesc, 1u);
+}
+__device__ __forceinline__ void mma_pv_hi(uint32_t d, uint32_t tp, uint32_t v, uint32_t idesc) {
+  mma_pv_step<4>(d, tp, v, idesc, 1u);
+  mma_pv_step<5>(d, tp, v, idesc, 1u);
+  mma_pv_step<6>(d, tp, v, idesc, 1u);
+  mma_pv_step<7>(d, tp, v, idesc, 1u);
+}
+
+// two floats in a 64-bit register, and their packed arithmetic
+__device__ __forceinline__ uint64_t pack_f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
 // a warpgroup's registers per thread, from or to the launch's pool
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
@@ -503,17 +600,21 @@ __global__ void __launch_bounds__(kHThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.q_full[i], 1);
-      mbar_init(&c.q_empty[i], 1);
+      mbar_init(&c.q_full[i + 2], 1);
+      mbar_init(&c.q_empty[i], 2);  // (see the issuers)
       mbar_init(&c.s_full[i], 1);
+      mbar_init(&c.p_half[i], 4);
       mbar_init(&c.p_full[i], 4);   // one arrival per warp of the group
       mbar_init(&c.o_full[i], 1);
+      mbar_init(&c.turn[i], 1);
       mbar_init(&c.o_empty[i], 4);
     }
     for (int i = 0; i < kHStages; ++i) {
       mbar_init(&c.kv_full[i], 1);
-      mbar_init(&c.kv_empty[i], 1);
+      mbar_init(&c.kv_full[i + kHStages], 1);
+      mbar_init(&c.kv_empty[i], 2);
     }
-    mbar_init(&c.done, 1);
+    mbar_init(&c.done, 2);
     c.abort_flag = 0;
     c.local_flags = 0;
     fence_mbar_init();
@@ -548,10 +649,8 @@ __global__ void __launch_bounds__(kHThreads, 1)
       int at = 0, qn = 0;  // ring places taken so far
       bool ok = true;
       HSeg s;
-      HTile next = range.x <= range.y ? load_tile(a.ws.tiles + range.x) : HTile{};
       for (int ti = range.x; ti <= range.y && ok; ++ti) {
-        s.t = next;
-        if (ti < range.y) next = load_tile(a.ws.tiles + ti + 1);
+        s.t = load_tile(a.ws.tiles + ti);  // (the ring holds loads for longer than this takes)
         cut(&s, share, cta);
         if (s.n <= 0) continue;
         const int nh = s.t.keys ? 1 : 2;
@@ -562,46 +661,49 @@ __global__ void __launch_bounds__(kHThreads, 1)
           if (!ok) break;
           if (lane == 0) {
             uint8_t* qd = sm + b * kHTileBytes;
+            uint64_t* full = &c.q_full[qn & 3];
             const int t0 = s.t.tok0 + h * a.T, nt = min(a.T, s.t.ntok - h * a.T);
             if (nt > kHSmallQ) {  // one box; rows past the tile's tokens are never used
-              mbar_arrive_expect_tx(&c.q_full[b], (uint32_t)(G * a.T) * 256u);
-              tma_load_3d(qd, &tmq, &c.q_full[b], 0, s.t.g * G, t0);
-              tma_load_3d(qd + 16384, &tmq, &c.q_full[b], 64, s.t.g * G, t0);
+              mbar_arrive_expect_tx(full, (uint32_t)(G * a.T) * 256u);
+              tma_load_3d(qd, &tmq, full, 0, s.t.g * G, t0);
+              tma_load_3d(qd + 16384, &tmq, full, 64, s.t.g * G, t0);
             } else {
-              mbar_arrive_expect_tx(&c.q_full[b], (uint32_t)(G * nt) * 256u);
+              mbar_arrive_expect_tx(full, (uint32_t)(G * nt) * 256u);
               for (int x = 0; x < nt; ++x) {
-                tma_load_3d(qd + x * G * 128, &tmq1, &c.q_full[b], 0, s.t.g * G, t0 + x);
-                tma_load_3d(qd + 16384 + x * G * 128, &tmq1, &c.q_full[b], 64, s.t.g * G, t0 + x);
+                tma_load_3d(qd + x * G * 128, &tmq1, full, 0, s.t.g * G, t0 + x);
+                tma_load_3d(qd + 16384 + x * G * 128, &tmq1, full, 64, s.t.g * G, t0 + x);
               }
             }
           }
         }
-        // block i's pages come from a window of 32 blocks that the lanes hold
-        const int32_t* row = a.block_tables + (size_t)s.t.row * a.max_pages;
-        int win[2] = {-1, -1}, prev[2] = {-1, -1};
-        for (int i = 0; i <= s.n && ok; ++i) {
-          int cur[2] = {-1, -1};
-          if (i < s.n) {
-            if ((i & 31) == 0) {
+        // block i's pages come from a window of 32 blocks that the lanes hold;
+      // the next window is loaded while this one is used
+      const int32_t* row = a.block_tables + (size_t)s.t.row * a.max_pages;
+      auto pages_at = [&](int i, int pg) -> int {  // lane's page pg of block i + lane, -1: none or not needed
+        const int b = s.b0 + i + lane;
+        const int p0 = b * 128 + pg * 64;  // its first key
+        if (pg >= npg || i + lane >= s.n || p0 >= s.t.hi || p0 + ps <= s.t.lo) return -1;
+        const int phys = row[p0 >> a.page_shift];
+        if (phys >= 0 && phys < a.num_pages) return phys;
+        atomicOr(fl, MXSA_FLAG_PAGE);
+        return -1;
+      };
+      int win[2] = {pages_at(0, 0), pages_at(0, 1)}, ahead[2] = {pages_at(32, 0), pages_at(32, 1)};
+      int prev[2] = {-1, -1};
+      for (int i = 0; i <= s.n && ok; ++i) {
+        int cur[2] = {-1, -1};
+        if (i < s.n) {
+          if ((i & 31) == 0 && i > 0) {
 #pragma unroll
-              for (int pg = 0; pg < 2; ++pg) {
-                const int b = s.b0 + i + lane;
-                const int p0 = npg == 2 ? b * 128 + pg * 64 : b * 128;  // the page's first key
-                int phys = -1;
-                if (pg < npg && i + lane < s.n && p0 < s.t.hi && p0 + ps > s.t.lo) {
-                  phys = row[p0 >> a.page_shift];
-                  if (phys < 0 || phys >= a.num_pages) {
-                    atomicOr(fl, MXSA_FLAG_PAGE);
-                    phys = -1;
-                  }
-                }
-                win[pg] = phys;
-              }
+            for (int pg = 0; pg < 2; ++pg) {
+              win[pg] = ahead[pg];
+              ahead[pg] = pages_at(i + 32, pg);
             }
-            cur[0] = __shfl_sync(0xffffffffu, win[0], i & 31);
-            cur[1] = __shfl_sync(0xffffffffu, win[1], i & 31);
           }
-          // K of block i, then V of block i - 1: the ring's order
+          cur[0] = __shfl_sync(0xffffffffu, win[0], i & 31);
+          cur[1] = __shfl_sync(0xffffffffu, win[1], i & 31);
+        }
+        // K of block i, then V of block i - 1: the ring's order
 #pragma unroll
           for (int kv = 0; kv < 2 && ok; ++kv) {
             if (kv == 0 ? i >= s.n : i == 0) continue;
@@ -611,15 +713,16 @@ __global__ void __launch_bounds__(kHThreads, 1)
             if (!ok) break;
             ++at;
             if (lane == 0) {
+              uint64_t* full = &c.kv_full[(at - 1) % (2 * kHStages)];
               uint8_t* dst = sm + kHOffKV + st * kHTileBytes;
               const int present = (pg[0] >= 0) + (pg[1] >= 0);
               const CUtensorMap* tm = kv == 0 ? &tmk : &tmv;
-              mbar_arrive_expect_tx(&c.kv_full[st], (uint32_t)present * (uint32_t)ps * 256u);
+              mbar_arrive_expect_tx(full, (uint32_t)present * (uint32_t)ps * 256u);
               for (int x = 0; x < npg; ++x) {
                 if (pg[x] < 0) continue;
                 const int z = pg[x] * a.Hkv + s.t.g;
-                tma_load_3d(dst + x * 8192, tm, &c.kv_full[st], 0, 0, z);
-                tma_load_3d(dst + 16384 + x * 8192, tm, &c.kv_full[st], 64, 0, z);
+                tma_load_3d(dst + x * 8192, tm, full, 0, 0, z);
+                tma_load_3d(dst + 16384 + x * 8192, tm, full, 64, 0, z);
               }
             }
           }
@@ -630,85 +733,145 @@ __global__ void __launch_bounds__(kHThreads, 1)
       // drain: the copies in flight land before the CTA may exit
       if (lane == 0) {
         for (int k = max(0, at - kHStages); k < at; ++k)
-          mbar_drain(&c.kv_full[k % kHStages], (k / kHStages) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
+          mbar_drain(&c.kv_full[k % (2 * kHStages)], (k / (2 * kHStages)) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
         for (int k = max(0, qn - 2); k < qn; ++k)
-          mbar_drain(&c.q_full[k & 1], (k >> 1) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
+          mbar_drain(&c.q_full[k & 3], (k >> 2) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
       }
       __syncwarp();
-    } else if (warp == kHMma) {
-      // ------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
-        const uint32_t id_qk = idesc_f16(128, 128, kBf16 ? 1u : 0u, 0, 0);
-        const uint32_t id_pv = idesc_f16(128, 128, kBf16 ? 1u : 0u, 0, 1);
-        int at = 0, qn = 0;
-        int np[2] = {0, 0}, no[2] = {0, 0};          // p v products and finished tiles of each group
-        int pv_place[2] = {-1, -1}, pv_bits[2] = {0, 0};  // the product a group still owes; bit 0: first of its tile,
-                                                          // 1: last, 2: frees V
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, int parity) {
-          ok = ok && mbar_wait(bar, parity, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
-          return ok;
-        };
-        auto pv = [&](int h) {  // the owed P V of group h
-          const int pl = pv_place[h], st = pl % kHStages, bits = pv_bits[h];
-          pv_place[h] = -1;
-          if (!wait(&c.p_full[h], np[h] & 1) || !wait(&c.kv_full[st], (pl / kHStages) & 1)) return;
-          ++np[h];
-          // O of the group's previous tile has been read out
-          if ((bits & 1) && no[h] > 0 && !wait(&c.o_empty[h], (no[h] - 1) & 1)) return;
-          tc_fence_after();
-          const uint32_t tS = tmem + h * 256;
-          const uint64_t dv = smem_desc_sw128(sbase + kHOffKV + st * kHTileBytes, 16384, 1024);
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)  // (the address field counts 16 bytes and does not overflow)
-            mma_f16_ts(tS + 128, tS + ks * 8, dv + ks * (2048u >> 4), id_pv, (!(bits & 1) || ks > 0) ? 1u : 0u);
-          if (bits & 4) mma_commit(&c.kv_empty[st]);
-          if (bits & 2) {
-            mma_commit(&c.o_full[h]);
-            ++no[h];
-          }
-        };
+    } else if (warp == kHMma || warp == kHMma + 1) {
+      // --------------------------------------------------------- MMA issuers
+      // One warp per group.  The whole warp walks the loop and one elected
+      // lane issues: what the instructions take from uniform registers is
+      // then uniform.  After a run of products the warp stands still until
+      // the pipe has taken them, so P V and the next q k^T go out together
+      // when K is there, and the other warp's products fill the time between.
+      const int h = warp - kHMma;
+      const uint32_t id_qk = idesc_f16(128, 128, kBf16 ? 1u : 0u, 0, 0);
+      const uint32_t id_pv = idesc_f16(128, 128, kBf16 ? 1u : 0u, 0, 1);
+      int at = 0, qn = 0;
+      int np = 0, no = 0;           // products P V issued, tiles finished
+      int nt = 0;                   // turns taken
+      int owed = -1, bits = 0;      // ring place of the V that the next P V takes; bit 0: first of its tile, 1: last,
+                                    // 2: no other group reads V
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) {
+        ok = ok && hwarp_all(mbar_wait(bar, parity, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
+      };
+      auto wait_v = [&] {  // V and, at a tile's start, O of the group's previous tile read out
+        wait(&c.kv_full[owed % (2 * kHStages)], (owed / (2 * kHStages)) & 1);
+        if ((bits & 1) && no > 0) wait(&c.o_empty[h], (no - 1) & 1);
+      };
+      // P V: its first half once P's first 64 keys are there, the second by
+      // `rest` (the elected lane, after P's second half)
+      auto start_pv = [&](uint32_t tS, uint32_t dv) {
+        wait(&c.p_half[h], np & 1);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one()) mma_pv_lo(tS + 128, tS, dv, id_pv, (bits & 1) ? 0u : 1u);
+        __syncwarp();
+        wait(&c.p_full[h], np & 1);
+      };
+      auto rest_pv = [&](uint32_t tS, uint32_t dv, uint64_t* empty) {
+        mma_pv_hi(tS + 128, tS, dv, id_pv);
+        mma_commit(empty);
+        if (bits & 4) mma_commit(empty);
+        if (bits & 2) mma_commit(&c.o_full[h]);
+      };
+      auto done_pv = [&] {
+        ++np;
+        no += (bits >> 1) & 1;
+        owed = -1;
+      };
+      const uint32_t tS = uniform(tmem + h * 256);
+      for (int ti = range.x; ti <= range.y && ok; ++ti) {
         HSeg s;
-        HTile next = range.x <= range.y ? load_tile(a.ws.tiles + range.x) : HTile{};
-        for (int ti = range.x; ti <= range.y && ok; ++ti) {
-          s.t = next;
-          if (ti < range.y) next = load_tile(a.ws.tiles + ti + 1);
-          cut(&s, share, cta);
-          if (s.n <= 0) continue;
-          const int keys = s.t.keys;
-          const int rounds = keys ? (s.n + 1) >> 1 : s.n;
-          for (int j = 0; j < rounds && ok; ++j) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int i = keys ? 2 * j + h : j;  // the block
-              if (ok && pv_place[h] >= 0) pv(h);
-              if (!ok || i >= s.n) continue;
-              const int qp = keys ? qn : qn + h, kp = at + place_k(i), st = kp % kHStages;
-              if (j == 0 && !wait(&c.q_full[qp & 1], (qp >> 1) & 1)) continue;
-              if (!wait(&c.kv_full[st], (kp / kHStages) & 1)) continue;
+        s.t = load_tile(a.ws.tiles + ti);  // (the last blocks' softmax takes longer than this)
+        cut(&s, share, cta);
+        if (s.n <= 0) continue;
+        const int n = s.n, keys = s.t.keys, stride = keys ? 2 : 1;
+        const int half = keys ? h ^ (qn & 1) : 0;  // (see the softmax)
+        const int qp = keys ? qn : qn + h;
+        for (int i = half; i < n && ok; i += stride) {
+          const int kp = at + place_k(i), st = kp % kHStages;
+          const int sv = max(owed, 0) % kHStages;
+          const uint32_t dv = uniform(desc_mn_major(sbase + kHOffKV + sv * kHTileBytes));
+          const uint32_t dq = uniform(desc_k_major(sbase + (qp & 1) * kHTileBytes));
+          const uint32_t dk = uniform(desc_k_major(sbase + kHOffKV + st * kHTileBytes));
+          // In a tile of two halves the groups take turns at the pipe: left
+          // alone they can fall into step, both in their softmax at once and
+          // then both waiting for each other's products.
+          if (!keys) {
+            if (h == 1 || nt > 0) wait(&c.turn[h], (nt + h + 1) & 1);
+            ++nt;
+            if (!ok) break;
+          }
+          if (owed >= 0) {
+            wait_v();
+            // P V alone when K (or a new tile's q) may not be there yet
+            const bool alone =
+                i == half || !hwarp_all(mbar_test(&c.kv_full[kp % (2 * kHStages)], (kp / (2 * kHStages)) & 1));
+            start_pv(tS, dv);
+            if (!ok) break;
+            if (alone) {
               tc_fence_after();
-              const uint64_t dq = smem_desc_sw128(sbase + (qp & 1) * kHTileBytes, 0, 1024);
-              const uint64_t dk = smem_desc_sw128(sbase + kHOffKV + st * kHTileBytes, 0, 1024);
-              const uint32_t tS = tmem + h * 256;
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks) {
-                const uint32_t off = ((ks >> 2) * 16384u + (ks & 3) * 32u) >> 4;
-                mma_f16_ss(tS, dq + off, dk + off, id_qk, ks > 0);
-              }
-              mma_commit(&c.s_full[h]);
-              const bool both = !keys && h == 0;  // group 1 reads this stage too
-              if (!both) mma_commit(&c.kv_empty[st]);
-              if (i == s.n - 1) mma_commit(&c.q_empty[qp & 1]);
-              pv_place[h] = at + place_v(i, s.n);
-              pv_bits[h] = (j == 0 ? 1 : 0) | ((keys ? i + 2 : i + 1) >= s.n ? 2 : 0) | (both ? 0 : 4);
+              if (elect_one()) rest_pv(tS, dv, &c.kv_empty[sv]);
+              __syncwarp();
+              done_pv();
             }
           }
-          at += 2 * s.n;
-          qn += keys ? 1 : 2;
+          if (owed < 0) {
+            if (i == half) wait(&c.q_full[qp & 3], (qp >> 2) & 1);
+            wait(&c.kv_full[kp % (2 * kHStages)], (kp / (2 * kHStages)) & 1);
+            if (!ok) break;
+          }
+          const bool last = i + stride >= n;
+          tc_fence_after();
+          if (elect_one()) {
+            if (owed >= 0) rest_pv(tS, dv, &c.kv_empty[sv]);
+            mma_qk(tS, dq, dk, id_qk);
+            mma_commit(&c.s_full[h]);
+            // (two arrivals free a stage or a q buffer: one of each group, or both of the only one)
+            mma_commit(&c.kv_empty[st]);
+            if (keys) mma_commit(&c.kv_empty[st]);
+            if (last) mma_commit(&c.q_empty[qp & 1]);
+            if (last && !keys) mma_commit(&c.q_empty[qp & 1]);
+            if (!keys) mbar_arrive(&c.turn[h ^ 1]);
+          }
+          __syncwarp();
+          if (owed >= 0) done_pv();
+          owed = at + place_v(i, n);
+          bits = (i == half ? 1 : 0) | (last ? 2 : 0) | (keys ? 4 : 0);
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (ok && pv_place[h] >= 0) pv(h);
+        if (half >= n && ok) {  // no block of this tile is the group's: nothing else would free what it owes
+          if (owed >= 0) {
+            const int sv = owed % kHStages;
+            const uint32_t dv = uniform(desc_mn_major(sbase + kHOffKV + sv * kHTileBytes));
+            wait_v();
+            start_pv(tS, dv);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) rest_pv(tS, dv, &c.kv_empty[sv]);
+            __syncwarp();
+            done_pv();
+          }
+          wait(&c.q_full[qp & 3], (qp >> 2) & 1);
+          if (!ok) break;
+          if (elect_one()) mma_commit(&c.q_empty[qp & 1]);
+          __syncwarp();
+        }
+        at += 2 * n;
+        qn += keys ? 1 : 2;
+      }
+      if (ok && owed >= 0) {
+        const int sv = owed % kHStages;
+        const uint32_t dv = uniform(desc_mn_major(sbase + kHOffKV + sv * kHTileBytes));
+        wait_v();
+        start_pv(tS, dv);
+        tc_fence_after();
+        if (ok && elect_one()) rest_pv(tS, dv, &c.kv_empty[sv]);
+        __syncwarp();
+      }
+      if (elect_one()) {
         mma_commit(&c.done);
         mbar_drain(&c.done, 0, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
       }
@@ -721,40 +884,46 @@ __global__ void __launch_bounds__(kHThreads, 1)
     const int r = tid & 127;  // row of the half == TMEM lane
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + h * 256 + lane_addr, tO = tS + 128;
-    const int rt = r / G, rh = r - rt * G;
-    int at = 0, n_s = 0, n_o = 0;
+    const int rt = r / G;
+    int at = 0, qn = 0, n_s = 0, n_o = 0;
     bool ok = true;
-    HSeg s;
     HTile next = range.x <= range.y ? load_tile(a.ws.tiles + range.x) : HTile{};
     for (int ti = range.x; ti <= range.y && ok; ++ti) {
+      // what the block loop and the epilogue need of the tile, and no more:
+      // a row's 128 scores leave few registers
+      HSeg s;
       s.t = next;
-      if (ti < range.y) next = load_tile(a.ws.tiles + ti + 1);
       cut(&s, share, cta);
-      if (s.n <= 0) continue;
-      const int keys = s.t.keys, stride = keys ? 2 : 1;
+      const int n = s.n, b0 = s.b0, lo = s.t.lo, key_end = s.t.hi, keys = s.t.keys, stride = keys ? 2 : 1;
+      // the group that takes a one-half tile's first block changes with the q
+      // buffer, so that short tiles keep both groups busy
+      const int half = keys ? h ^ (qn & 1) : 0;
+      if (n > 0) qn += keys ? 1 : 2;
       const int tt = rt + (keys ? 0 : h * a.T);  // the row's token within the tile
       const bool live = rt < a.T && tt < s.t.ntok;
+      const long long rows = (long long)s.t.ntok * G;
+      const long long pr =
+          s.t.part0 + (cta - s.t.cta0) * rows * stride + half * rows + tt * G + (r - rt * G);
       const bool warp_live = __any_sync(0xffffffffu, live);
-      // keys the row sees: [lo, hi)
-      const int lo = s.t.lo;
-      int hi = s.t.hi;
-      if (a.causal && live) hi = min(hi, a.ws.tok[s.t.tok0 + tt].y);
+      int hi = key_end;  // the row sees the keys [lo, hi), all of the warp's rows [lo, warp_hi)
+      if (n > 0 && a.causal && live) hi = min(hi, a.ws.tok[s.t.tok0 + tt].y);
+      const int warp_hi = __reduce_min_sync(0xffffffffu, hi);
       float m = -INFINITY, l = 0.f;
       bool mine = false;  // this group has blocks of the segment
-      for (int i = keys ? h : 0; i < s.n && ok; i += stride, ++n_s) {
-        const int k0 = (s.b0 + i) << 7;  // the block's first key
+      for (int i = half; i < n && ok; i += stride, ++n_s) {
+        const int k0 = (b0 + i) << 7;  // the block's first key
         ok = hwarp_all(mbar_wait(&c.s_full[h], n_s & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
         if (!ok) break;
-        if (k0 < lo || k0 + 128 > s.t.hi) {
+        if (k0 < lo || k0 + 128 > key_end) {
           // V rows of keys outside [lo, hi): zeros, since a stale row may hold
           // NaN bits and 0 * NaN would reach O.  (Their stage has landed
           // once its barrier says so; the writers' proxy fence orders them
           // before the product.)
-          const int pl = at + place_v(i, s.n), st = pl % kHStages;
-          ok = hwarp_all(mbar_wait(&c.kv_full[st], (pl / kHStages) & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT,
-                                   kWaitLimitNs));
+          const int pl = at + place_v(i, n), st = pl % kHStages;
+          ok = hwarp_all(mbar_wait(&c.kv_full[pl % (2 * kHStages)], (pl / (2 * kHStages)) & 1, abort_flag, fl,
+                                   MXSA_FLAG_TIMEOUT, kWaitLimitNs));
           if (!ok) break;
-          if (k0 + r < lo || k0 + r >= s.t.hi) {
+          if (k0 + r < lo || k0 + r >= key_end) {
             const uint32_t vs = sbase + kHOffKV + st * kHTileBytes + r * 128;
             for (int ch = 0; ch < 16; ++ch)
               st_shared_v4(vs + (ch >> 3) * 16384u + (((ch & 7) ^ (r & 7)) << 4), 0, 0, 0, 0);
@@ -767,9 +936,8 @@ __global__ void __launch_bounds__(kHThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sv + q * 32);
           tmem_ld_wait();
-          const int rlo = lo - k0, rhi = hi - k0;
-          const bool full = __all_sync(0xffffffffu, !live || (rlo <= 0 && rhi >= 128));
-          if (!full) {
+          if (k0 < lo || k0 + 128 > warp_hi) {
+            const int rlo = lo - k0, rhi = hi - k0;
 #pragma unroll
             for (int k = 0; k < 128; ++k) sv[k] = k >= rlo && k < rhi ? sv[k] : -INFINITY;
           }
@@ -789,14 +957,13 @@ __global__ void __launch_bounds__(kHThreads, 1)
               // O holds the segment's blocks so far and is complete: S's
               // barrier follows every product issued before
 #pragma unroll
-              for (int cb = 0; cb < 4; ++cb) {
-                float ov[32];
-                tmem_ld32(tO + cb * 32, ov);
+              for (int cb = 0; cb < 8; ++cb) {  // 16 columns at a time: the scores keep their registers
+                uint32_t w[16];
+                tmem_ld16(tO + cb * 16, w);
                 tmem_ld_wait();
-                uint32_t w[32];
 #pragma unroll
-                for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(ov[k] * f);
-                tmem_st32(tO + cb * 32, w);
+                for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
+                tmem_st16(tO + cb * 16, w);
               }
             }
             if (raise) {
@@ -805,29 +972,41 @@ __global__ void __launch_bounds__(kHThreads, 1)
             }
           }
           const float mm = m == -INFINITY ? 0.f : m;
-          float l0 = 0.f, l1 = 0.f;
+          const uint64_t scale2 = pack_f2(a.scale_log2, a.scale_log2), off2 = pack_f2(-mm, -mm);
+          uint64_t l0 = pack_f2(0.f, 0.f), l1 = l0;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t pk[32];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t pk[16];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float p0 = ex2_approx(fmaf(sv[64 * q + 2 * k], a.scale_log2, -mm));
-              const float p1 = ex2_approx(fmaf(sv[64 * q + 2 * k + 1], a.scale_log2, -mm));
-              l0 += p0;
-              l1 += p1;
+            for (int k = 0; k < 16; ++k) {
+              const float2 x = unpack_f2(fma_f2(pack_f2(sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]), scale2, off2));
+              const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+              if (k & 1) l1 = add_f2(l1, pack_f2(p0, p1));
+              else l0 = add_f2(l0, pack_f2(p0, p1));
               pk[k] = hpack2<kBf16>(p0, p1);
             }
-            tmem_st32(tS + 32 * q, pk);
+            tmem_st16(tS + 16 * q, pk);
+            if (q == 1) {  // the first 64 keys: their half of P V may start
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&c.p_half[h]);
+            }
           }
-          l += l0 + l1;
+          const float2 ls = unpack_f2(add_f2(l0, l1));
+          l += ls.x + ls.y;
           tmem_st_wait();
+        } else {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.p_half[h]);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c.p_full[h]);
         mine = true;
       }
-      at += 2 * s.n;
+      at += 2 * max(n, 0);
+      if (ti < range.y) next = load_tile(a.ws.tiles + ti + 1);
       if (!ok || !mine) continue;
       // ---- the segment's partial rows
       ok = hwarp_all(mbar_wait(&c.o_full[h], n_o & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
@@ -836,8 +1015,6 @@ __global__ void __launch_bounds__(kHThreads, 1)
       if (warp_live) {
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN stays one)
-        const long long rows = (long long)s.t.ntok * G;
-        const long long pr = s.t.part0 + (cta - s.t.cta0) * rows * stride + (keys ? h * rows : 0) + tt * G + rh;
         float* po = a.ws.part_o + pr * 128;
 #pragma unroll
         for (int cb = 0; cb < 4; ++cb) {

@@ -5,7 +5,7 @@ Python; random problems check that every visible (token, key) pair lies in
 exactly one segment, that a row's partials are distinct and that the tile and
 partial-row bounds that size the workspace hold.
 
-The forward's mbarrier protocol (producer, MMA issuer, two softmax groups,
+The forward's mbarrier protocol (producer, two MMA issuers, two softmax groups,
 five K/V stages, two q buffers) under random interleavings: no deadlock, and
 no buffer is refilled or overwritten before its readers are done.
 """
@@ -15,7 +15,7 @@ import pytest
 
 from tests.test_barrier_models import Bar
 
-MAXC, WR, WK, STAGES = 160, 2, 1, 5
+MAXC, WR, WK, TILE, STAGES = 160, 4, 2, 2, 5
 
 
 def cdiv(a, b):
@@ -48,7 +48,8 @@ def plan(p):
         j["nrt"] = cdiv(j["ntok"], 2 * T) if j["nb"] else 0
         keys = int(0 < rem <= T)
         j["w"] = WR if j["nrt"] > keys else WK
-        total += p["hkv"] * j["nb"] * ((j["nrt"] - keys) * WR + keys * WK) if j["nb"] else 0
+        if j["nb"]:
+            total += p["hkv"] * ((j["nrt"] - keys) * (j["nb"] * WR + TILE) + keys * (j["nb"] * WK + TILE))
     goal = max(cdiv(total, p["ctas"]), 1)
     tiles = []
     for j in jobs:
@@ -68,8 +69,8 @@ def plan(p):
     cost = 0
     for t in tiles:
         t["w"] = WK if t["keys"] else WR
-        t["cost0"] = cost
-        cost += t["n"] * t["w"]
+        t["cost0"] = cost + TILE
+        cost += t["n"] * t["w"] + TILE if t["n"] else 0
     share = max(cdiv(cost, p["ctas"]), WR)
     part = 0
     for t in tiles:
@@ -168,11 +169,21 @@ def run_protocol(segs, seed):
         B[n] = Bar(n, c)
 
     for i in range(2):
-        for n in ("q_full", "q_empty", "s_full", "p_full", "o_full", "o_empty"):
+        for n in ("s_full", "p_half", "p_full", "o_full", "o_empty"):
             bar(f"{n}{i}")
+        bar(f"q_empty{i}", 2)
+    for i in range(4):
+        bar(f"q_full{i}")
     for i in range(STAGES):
         bar(f"kv_full{i}")
-        bar(f"kv_empty{i}")
+        bar(f"kv_full{i + STAGES}")
+        bar(f"kv_empty{i}", 2)
+
+    def q_full(x):
+        return ("wait", B[f"q_full{x & 3}"], (x >> 2) & 1)
+
+    def kv_full(x):
+        return ("wait", B[f"kv_full{x % (2 * STAGES)}"], (x // (2 * STAGES)) & 1)
 
     def later(src, cb):
         pending.setdefault(src, []).append(cb)
@@ -193,7 +204,7 @@ def run_protocol(segs, seed):
 
                 def land(b=b, qn=qn):
                     qbuf[b] = qn
-                    B[f"q_full{b}"].arrive()
+                    B[f"q_full{qn & 3}"].arrive()
                 later(f"q{b}", land)
                 qn += 1
             for x in range(2 * n):
@@ -203,93 +214,118 @@ def run_protocol(segs, seed):
 
                 def land(st=st, at=at):
                     stage[st] = at
-                    B[f"kv_full{st}"].arrive()
+                    B[f"kv_full{at % (2 * STAGES)}"].arrive()
                 later(f"kv{st}", land)
                 at += 1
 
-    def mma():
-        at = qn = 0
-        npv, no, owed = [0, 0], [0, 0], [None, None]
+    def issuer(h):
+        at = qn = npv = no = 0
+        owed = None
 
-        def pv(h):
-            pl, firstp, lastp, free = owed[h]
-            owed[h] = None
-            st = pl % STAGES
-            yield ("wait", B[f"p_full{h}"], npv[h] & 1)
-            yield ("wait", B[f"kv_full{st}"], (pl // STAGES) & 1)
-            assert stage[st] == pl and S[h][0] == "P"
-            npv[h] += 1
-            if firstp and no[h]:
-                yield ("wait", B[f"o_empty{h}"], (no[h] - 1) & 1)
+        def wait_v():
+            pl, first, _, _ = owed
+            yield kv_full(pl)
+            assert stage[pl % STAGES] == pl
+            if first and no:
+                yield ("wait", B[f"o_empty{h}"], (no - 1) & 1)
                 assert O[h] == "read", "O overwritten before it was read"
 
-            def done(h=h, pl=pl, st=st, free=free, lastp=lastp):
+        def start_pv():
+            yield ("wait", B[f"p_half{h}"], npv & 1)
+            pl = owed[0]
+
+            def low():
+                assert S[h][0] in ("half", "P") and stage[pl % STAGES] == pl
+                O[h] = "acc"
+            later(f"mma{h}", low)
+            yield ("wait", B[f"p_full{h}"], npv & 1)
+            assert S[h][0] == "P"
+
+        def rest_pv():
+            pl, _, last, alone = owed
+
+            def done():
                 assert S[h][0] == "P"
                 S[h] = ("used",)
-                O[h] = "done" if lastp else "acc"
+                O[h] = "done" if last else "acc"
                 reads[pl] -= 1
-                if free:
-                    B[f"kv_empty{st}"].arrive()
-                if lastp:
+                for _x in range(2 if alone else 1):
+                    B[f"kv_empty{pl % STAGES}"].arrive()
+                if last:
                     B[f"o_full{h}"].arrive()
-            later("mma", done)
-            if lastp:
-                no[h] += 1
+            later(f"mma{h}", done)
 
         for n, keys, _ in segs:
-            for i in range(n):
-                reads[at + place_k(i)] = reads[at + place_v(i, n)] = 1 if keys else 2
-            for x in range(1 if keys else 2):
-                qreads[qn + x] = n
-            for j in range((n + 1) // 2 if keys else n):
-                for h in range(2):
-                    i = 2 * j + h if keys else j
-                    if owed[h]:
-                        yield from pv(h)
-                    if i >= n:
-                        continue
-                    qp, kp = qn if keys else qn + h, at + place_k(i)
-                    st = kp % STAGES
-                    if j == 0:
-                        yield ("wait", B[f"q_full{qp & 1}"], (qp >> 1) & 1)
-                    yield ("wait", B[f"kv_full{st}"], (kp // STAGES) & 1)
-                    assert qbuf[qp & 1] == qp and stage[st] == kp
-                    both = not keys and h == 0
+            half = h ^ (qn & 1) if keys else 0
+            qp = qn if keys else qn + h
+            for i in range(half, n, 2 if keys else 1):
+                kp = at + place_k(i)
+                st = kp % STAGES
+                if owed:
+                    yield from wait_v()
+                    alone = i == half or not kv_full(kp)[1].ready(kv_full(kp)[2])
+                    yield from start_pv()
+                    if alone:
+                        rest_pv()
+                        npv, no, owed = npv + 1, no + owed[2], None
+                if not owed:
+                    if i == half:
+                        yield q_full(qp)
+                    yield kv_full(kp)
+                assert qbuf[qp & 1] == qp and stage[st] == kp
+                last = i + (2 if keys else 1) >= n
+                if owed:
+                    rest_pv()
 
-                    def done(h=h, qp=qp, kp=kp, st=st, both=both, end=i == n - 1):
-                        assert S[h] is None or S[h][0] == "used", "S overwritten before its product"
-                        S[h] = ("S",)
-                        reads[kp] -= 1
-                        qreads[qp] -= 1
-                        B[f"s_full{h}"].arrive()
-                        if not both:
-                            B[f"kv_empty{st}"].arrive()
-                        if end:
-                            assert qreads[qp] == 0
-                            B[f"q_empty{qp & 1}"].arrive()
-                    later("mma", done)
-                    owed[h] = (at + place_v(i, n), j == 0, (i + 2 if keys else i + 1) >= n, not both)
-                    yield None
+                def done(qp=qp, kp=kp, st=st, last=last, keys=keys):
+                    assert S[h] is None or S[h][0] == "used", "S overwritten before its product"
+                    S[h] = ("S",)
+                    reads[kp] -= 1
+                    qreads[qp] -= 1
+                    B[f"s_full{h}"].arrive()
+                    for _x in range(2 if keys else 1):
+                        B[f"kv_empty{st}"].arrive()
+                    for _x in range((1 if keys else 2) if last else 0):
+                        B[f"q_empty{qp & 1}"].arrive()
+                later(f"mma{h}", done)
+                if owed:
+                    npv, no = npv + 1, no + owed[2]
+                owed = (at + place_v(i, n), i == half, int(last), keys)
+                yield None
+            if half >= n:
+                if owed:
+                    yield from wait_v()
+                    yield from start_pv()
+                    rest_pv()
+                    npv, no, owed = npv + 1, no + owed[2], None
+                yield q_full(qp)
+                later(f"mma{h}", lambda qp=qp: B[f"q_empty{qp & 1}"].arrive())
             at += 2 * n
             qn += 1 if keys else 2
-        for h in range(2):
-            if owed[h]:
-                yield from pv(h)
+        if owed:
+            yield from wait_v()
+            yield from start_pv()
+            rest_pv()
 
     def softmax(h):
-        at = ns = no = 0
+        at = ns = no = qn = 0
         for n, keys, edge in segs:
             mine = False
-            for i in range(h if keys else 0, n, 2 if keys else 1):
+            half = h ^ (qn & 1) if keys else 0
+            qn += 1 if keys else 2
+            for i in range(half, n, 2 if keys else 1):
                 yield ("wait", B[f"s_full{h}"], ns & 1)
                 ns += 1
                 assert S[h] == ("S",)
                 if edge and i in (0, n - 1):
                     pl = at + place_v(i, n)
-                    yield ("wait", B[f"kv_full{pl % STAGES}"], (pl // STAGES) & 1)
+                    yield kv_full(pl)
                     assert stage[pl % STAGES] == pl, "rows cleared in another block's stage"
                 if mine:
                     assert O[h] == "acc", "O rescaled while a product writes it"
+                S[h] = ("half",)
+                B[f"p_half{h}"].arrive()
+                yield None
                 S[h] = ("P",)
                 B[f"p_full{h}"].arrive()
                 mine = True
@@ -302,7 +338,16 @@ def run_protocol(segs, seed):
                 B[f"o_empty{h}"].arrive()
                 finished[h] += 1
 
-    roles = {"p": producer(), "m": mma(), "s0": softmax(0), "s1": softmax(1)}
+    # products still to read a place or a q buffer, by number
+    at = qn = 0
+    for n, keys, _ in segs:
+        for i in range(n):
+            reads[at + place_k(i)] = reads[at + place_v(i, n)] = 1 if keys else 2
+        for x in range(1 if keys else 2):
+            qreads[qn + x] = n
+        at += 2 * n
+        qn += 1 if keys else 2
+    roles = {"p": producer(), "m0": issuer(0), "m1": issuer(1), "s0": softmax(0), "s1": softmax(1)}
     blocked = dict.fromkeys(roles)
     while roles or any(pending.values()):
         ready = [k for k in roles if blocked[k] is None or blocked[k][1].ready(blocked[k][2])]
@@ -316,7 +361,7 @@ def run_protocol(segs, seed):
             blocked[k] = next(roles[k])
         except StopIteration:
             del roles[k]
-    assert finished[0] == len(segs) and all(v == 0 for v in reads.values())
+    assert sum(finished) >= len(segs) and all(v == 0 for v in reads.values())
 
 
 @pytest.mark.parametrize("seed", range(40))
