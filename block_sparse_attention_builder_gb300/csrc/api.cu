@@ -446,7 +446,7 @@ static mxsa_status validate_shared(const mxsa_problem& p) {
   mxsa_status s = validate_shape(p);
   if (s != MXSA_OK) return s;
   if (p.kv_dtype != p.q_dtype || p.num_seqs > 1024) return MXSA_ERR_UNSUPPORTED;
-  if ((int64_t)p.total_q * p.num_kv_heads >= (1ll << 31)) return MXSA_ERR_UNSUPPORTED;
+  if ((int64_t)p.total_q * p.num_kv_heads >= (1ll << 31) || !shared_rows_fit(p)) return MXSA_ERR_UNSUPPORTED;
   return MXSA_OK;
 }
 

@@ -172,6 +172,7 @@ cudaError_t launch_dense(const mxsa_problem& p, const void* q, const void* k_cac
                          const int32_t* block_tables, const int64_t* cu, const int32_t* lens, void* out, float* lse,
                          int32_t* flags, cudaStream_t st);
 size_t shared_workspace_bytes(const mxsa_problem& p);
+bool shared_rows_fit(const mxsa_problem& p);
 cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void* k_cache, const void* v_cache,
                                 const int32_t* block_tables, const int64_t* cu, const int32_t* lens, int num_groups,
                                 const int32_t* group_ptr, const int32_t* prefix_lens, void* ws, void* out, float* lse,

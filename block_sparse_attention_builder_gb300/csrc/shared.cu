@@ -37,16 +37,20 @@ namespace {
 
 constexpr int kHMaxSeqs = 1024;
 constexpr int kHMaxCtas = 160;     // ranges; workspaces are sized for this many
-constexpr int kHCostRows = 4;      // cost of one block for a tile of two halves
-constexpr int kHCostKeys = 2;      // ... of one half (the halves then split the blocks)
-constexpr int kHCostTile = 2;      // a tile's own: its q, the first block's latency, the epilogue
+// Costs, in units of about 0.2 us: one block of a tile of two halves, of one
+// half (whose halves then split the blocks), and a tile's own (its q, the
+// first block's latency, the epilogue).  From the times of CTAs with one
+// kind of work each, all kinds running at once (256 sequences over 65536
+// common keys): 1.5 us, 0.9 us and 1.9 us.
+constexpr int kHCostRows = 8, kHCostKeys = 5, kHCostTile = 10;
+constexpr int kHCostRatio = (kHCostRows + kHCostKeys - 1) / kHCostKeys;
 
 // One tile: keys [128 blk0, 128 (blk0 + nblk)) of [lo, hi) for ntok tokens.
 struct alignas(16) HTile {
   int32_t tok0, ntok, g, row;      // first token, tokens, kv head, block table row
   int32_t lo, hi, blk0, nblk;
   long long cost0;                 // cost before its first step
-  long long part0;                 // first partial row
+  long long part0;                 // partial row of the tile's first segment
   int32_t cta0;                    // first range that holds a step of it
   int32_t nseg;                    // ranges that do
   int32_t keys;                    // 1: one half of rows, the halves take alternate blocks
@@ -59,24 +63,30 @@ struct HJob {
   int32_t nch, chunk, nrt;         // chunks, blocks of one, row tiles
 };
 
+// A token: its sequence (-1: none), the keys it sees, and the tiles of its
+// sequence's own keys and of its group's prefix: for kv head g and chunk c <
+// nch, tile base + (g * nch + c) * nrt.
+struct alignas(16) HTok {
+  int32_t seq, keys, own_base, own_nch;
+  int32_t own_nrt, pre_base, pre_nch, pre_nrt;
+};
+
 struct HHeader {
   long long share;                 // cost of one range
-  int32_t tiles, pad;
+  long long cuts;                  // partial row of range 0's cut (see part_row)
   int2 range[kHMaxCtas];           // first and last tile of each CTA's range (first > last: none)
 };
 
 struct HPtrs {
   HHeader* hdr;
-  HJob* jobs;                      // [2 * num_seqs]: sequences' own keys, then the groups' prefixes
-  int32_t* seq_job;                // [num_seqs]: the sequence's prefix job or -1
-  int2* tok;                       // [total_q]: sequence (-1: none) and visible keys
+  HTok* tok;                       // [total_q]
   HTile* tiles;
   float* part_o;
   float* part_lse;                 // log2 units
 };
 
 struct HLayout {
-  size_t hdr, jobs, seq_job, tok, tiles, part_o, part_lse, total;
+  size_t hdr, tok, tiles, part_o, part_lse, total;
   long long tile_cap, row_cap;
 };
 
@@ -85,9 +95,9 @@ HLayout shared_layout(const mxsa_problem& p) {
   // (job, kv head, row tile) triples: each token lies in at most two jobs, a
   // job's last row tile may be short, and there are at most B + B / 2 jobs
   const long long triples = p.num_kv_heads * (2 * (p.total_q / (2 * T)) + 2LL * p.num_seqs);
-  // chunks beyond the first: at most the CTAs' ranges, twice where a tile of
-  // one half (half the cost) takes its job's longer chunk
-  const long long extra = (kHCostRows / kHCostKeys) * kHMaxCtas;
+  // chunks beyond the first: at most the CTAs' ranges, kHCostRatio times as
+  // many where a tile of one half takes its job's chunk of two
+  const long long extra = kHCostRatio * kHMaxCtas;
   HLayout L;
   L.tile_cap = triples + extra;
   // a row and its twin (halves that split the blocks) in two jobs, and the
@@ -100,9 +110,7 @@ HLayout shared_layout(const mxsa_problem& p) {
     return at;
   };
   L.hdr = take(sizeof(HHeader));
-  L.jobs = take(sizeof(HJob) * 2 * p.num_seqs);
-  L.seq_job = take(4ull * p.num_seqs);
-  L.tok = take(8ull * p.total_q);
+  L.tok = take(sizeof(HTok) * (size_t)p.total_q);
   L.tiles = take(sizeof(HTile) * L.tile_cap);
   L.part_o = take(512ull * L.row_cap);
   L.part_lse = take(4ull * L.row_cap);
@@ -114,13 +122,23 @@ HPtrs shared_ptrs(const HLayout& L, void* ws) {
   uint8_t* b = static_cast<uint8_t*>(ws);
   HPtrs x;
   x.hdr = reinterpret_cast<HHeader*>(b + L.hdr);
-  x.jobs = reinterpret_cast<HJob*>(b + L.jobs);
-  x.seq_job = reinterpret_cast<int32_t*>(b + L.seq_job);
-  x.tok = reinterpret_cast<int2*>(b + L.tok);
+  x.tok = reinterpret_cast<HTok*>(b + L.tok);
   x.tiles = reinterpret_cast<HTile*>(b + L.tiles);
   x.part_o = reinterpret_cast<float*>(b + L.part_o);
   x.part_lse = reinterpret_cast<float*>(b + L.part_lse);
   return x;
+}
+
+// First partial row of the part of tile t that range c holds.  A range begins
+// with at most one tile that an earlier range began, so the cuts' rows lie at
+// a fixed distance, behind those of the tiles' first segments.
+constexpr int kHCutRows = 256;
+__device__ __forceinline__ long long part_row(const HTile& t, int c, long long cuts) {
+  return c == t.cta0 ? t.part0 : cuts + (long long)c * kHCutRows;
+}
+
+__device__ __forceinline__ long long ceil_div(long long x, int y) {
+  return x < INT_MAX - 4096 ? (uint32_t)(x + y - 1) / (uint32_t)y : (x + y - 1) / y;
 }
 
 // ------------------------------------------------------------------- plan
@@ -135,19 +153,24 @@ struct HPlanArgs {
   int32_t num_seqs, num_groups, total_q, Hkv, G, T, max_len, causal, ctas;
 };
 
-constexpr int kHPlanThreads = 1024;
+// One CTA that the forward waits for: few barriers, and what a thread does
+// per tile kept short (256, 512 and 1024 threads take the same time within
+// 2 us).
+constexpr int kHPlanThreads = 512;
 
 struct HPlanSmem {
   int32_t cu[kHMaxSeqs + 1], len[kHMaxSeqs], seq_group[kHMaxSeqs];
-  int32_t gp[kHMaxSeqs + 1], prefix[kHMaxSeqs];  // prefix: the group's shortest length, then its prefix length
-  int32_t tile0[2 * kHMaxSeqs + 1];
+  int32_t gp[kHMaxSeqs + 1], want[kHMaxSeqs], shortest[kHMaxSeqs];
+  int32_t tile0[2 * kHMaxSeqs];
   HJob job[2 * kHMaxSeqs];
-  long long scan[32];
-  int32_t first[kHMaxCtas], last[kHMaxCtas];
+  long long scan[4][kHPlanThreads / 32];
+  int32_t first[kHMaxCtas + 1];
 };
 
-// exclusive sum over the block; *total gets the whole (1024 threads)
+// exclusive sum over the block; *total gets the whole.  `s`: one word per
+// warp, not used by another call of the launch.
 __device__ __forceinline__ long long block_scan(long long v, long long* s, long long* total) {
+  constexpr int kWarps = kHPlanThreads / 32;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   long long x = v;
 #pragma unroll
@@ -155,17 +178,16 @@ __device__ __forceinline__ long long block_scan(long long v, long long* s, long 
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();  // the previous scan's readers are done
   if (lane == 31) s[w] = x;
   __syncthreads();
-  long long y = s[lane];
+  long long y = s[lane & (kWarps - 1)];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < kWarps; o <<= 1) {
     const long long z = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) y += z;
+    if ((lane & (kWarps - 1)) >= o) y += z;
   }
-  const long long before = __shfl_sync(0xffffffffu, y, (w + 31) & 31);
-  *total = __shfl_sync(0xffffffffu, y, 31);
+  const long long before = __shfl_sync(0xffffffffu, y, max(w - 1, 0));
+  *total = __shfl_sync(0xffffffffu, y, kWarps - 1);
   return x - v + (w ? before : 0);
 }
 
@@ -180,6 +202,11 @@ __device__ __forceinline__ int last_le(const int32_t* a, int n, int x) {
   return lo;
 }
 
+// A place in the line of tiles: row tile fastest, then chunk, kv head, job.
+struct HCursor {
+  int q, g, ch, rt;
+};
+
 __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   HPlanSmem& s = *reinterpret_cast<HPlanSmem*>(smem_raw);
@@ -187,38 +214,34 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
   pdl_launch_dependents();
   pdl_wait();
 
-  bool cu_ok = true, gp_ok = true;
+  int bad = 0;  // status bits
   for (int i = tid; i <= B; i += kHPlanThreads) {
     const long long v = a.cu[i], nx = i < B ? a.cu[i + 1] : a.total_q;
-    if (v < 0 || v > nx) cu_ok = false;
+    if (v < 0 || v > nx) bad |= MXSA_FLAG_CU;
     s.cu[i] = (int)v;
   }
   for (int i = tid; i < B; i += kHPlanThreads) {
     const int L = a.lens[i];
-    if ((L < 0 || L > a.max_len) && a.flags) atomicOr(a.flags, MXSA_FLAG_LEN);
+    if (L < 0 || L > a.max_len) bad |= MXSA_FLAG_LEN;
     s.len[i] = min(max(L, 0), a.max_len);
     s.seq_group[i] = -1;
   }
   for (int i = tid; i <= NG && NG > 0; i += kHPlanThreads) {  // (no groups: the pointer may be null)
     const int v = a.group_ptr[i], nx = i < NG ? a.group_ptr[i + 1] : B;
-    if (v < 0 || v > nx) gp_ok = false;
+    if (v < 0 || v > nx) bad |= MXSA_FLAG_GROUP;
     s.gp[i] = v;
-    if (i < NG) s.prefix[i] = a.max_len;
+    if (i < NG) {
+      s.want[i] = a.prefix_lens[i];
+      s.shortest[i] = a.max_len;
+    }
   }
-  for (int i = tid; i < a.ctas; i += kHPlanThreads) {
-    s.first[i] = INT_MAX;
-    s.last[i] = -1;
-  }
-  cu_ok = __syncthreads_and(cu_ok);
-  gp_ok = __syncthreads_and(gp_ok);
-  if (tid == 0 && a.flags) {
-    if (!cu_ok) atomicOr(a.flags, MXSA_FLAG_CU);
-    if (!gp_ok) atomicOr(a.flags, MXSA_FLAG_GROUP);
-  }
+  for (int i = tid; i <= a.ctas; i += kHPlanThreads) s.first[i] = -1;
+  const bool cu_ok = !__syncthreads_or(bad & MXSA_FLAG_CU), gp_ok = !__syncthreads_or(bad & MXSA_FLAG_GROUP);
+  if (bad && a.flags) atomicOr(a.flags, bad);
   if (!cu_ok) {  // no sequence has tokens: no tile, no row
-    for (int t = tid; t < a.total_q; t += kHPlanThreads) a.ws.tok[t] = make_int2(-1, 0);
+    for (int t = tid; t < a.total_q; t += kHPlanThreads) a.ws.tok[t] = HTok{-1, 0, 0, 0, 0, 0, 0, 0};
     for (int c = tid; c < a.ctas; c += kHPlanThreads) a.ws.hdr->range[c] = make_int2(0, -1);
-    if (tid == 0) a.ws.hdr->share = 1, a.ws.hdr->tiles = 0;
+    if (tid == 0) a.ws.hdr->share = 1, a.ws.hdr->cuts = 0;
     return;
   }
   // a group's prefix is at most its shortest sequence with tokens
@@ -228,149 +251,183 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
       const int j = last_le(s.gp, NG + 1, i);
       if (s.gp[j + 1] - s.gp[j] < 2) continue;  // one sequence alone shares nothing
       s.seq_group[i] = j;
-      if (s.cu[i + 1] > s.cu[i]) atomicMin(&s.prefix[j], s.len[i]);
+      if (s.cu[i + 1] > s.cu[i]) atomicMin(&s.shortest[j], s.len[i]);
     }
   __syncthreads();
-  for (int j = tid; j < NG; j += kHPlanThreads) {
-    const int want = min(max(a.prefix_lens[j], 0), s.prefix[j]);
-    const bool alone = !gp_ok || s.gp[j + 1] - s.gp[j] < 2;
-    s.prefix[j] = alone ? 0 : want;
-  }
-  __syncthreads();
-  for (int i = tid; i < B; i += kHPlanThreads)
-    if (s.seq_group[i] >= 0 && s.prefix[s.seq_group[i]] == 0) s.seq_group[i] = -1;
-  __syncthreads();
+  auto prefix_of = [&](int j) {  // 0: no prefix (also for the group number -1)
+    return j >= 0 && gp_ok && s.gp[j + 1] - s.gp[j] >= 2 ? min(max(s.want[j], 0), s.shortest[j]) : 0;
+  };
 
-  // jobs, and the whole cost as far as it is known without causal trimming
+  // A thread's jobs are consecutive, and its tiles below.
   const int njobs = B + NG, T2 = 2 * a.T;
+  const int jper = (njobs + kHPlanThreads - 1) / kHPlanThreads;
+  const int q0 = min(njobs, tid * jper), q1 = min(njobs, q0 + jper);
   long long cost = 0, total = 0;
-  for (int q = tid; q < njobs; q += kHPlanThreads) {
+  for (int q = q0; q < q1; ++q) {
     HJob j;
     if (q < B) {
       j.tok0 = s.cu[q];
       j.ntok = s.cu[q + 1] - s.cu[q];
       j.row = q;
-      j.lo = s.seq_group[q] >= 0 ? s.prefix[s.seq_group[q]] : 0;
+      j.lo = prefix_of(s.seq_group[q]);
       j.hi = s.len[q];
-      a.ws.seq_job[q] = s.seq_group[q] >= 0 ? B + s.seq_group[q] : -1;
     } else {
-      const int r = q - B;
-      const bool on = s.prefix[r] > 0;
-      j.row = on ? s.gp[r] : 0;
-      j.tok0 = on ? s.cu[s.gp[r]] : 0;
-      j.ntok = on ? s.cu[s.gp[r + 1]] - j.tok0 : 0;
+      const int r = q - B, P = prefix_of(r);
+      j.row = P > 0 ? s.gp[r] : 0;
+      j.tok0 = P > 0 ? s.cu[s.gp[r]] : 0;
+      j.ntok = P > 0 ? s.cu[s.gp[r + 1]] - j.tok0 : 0;
       j.lo = 0;
-      j.hi = s.prefix[r];
+      j.hi = P;
     }
     const int nb = j.ntok > 0 && j.hi > j.lo ? ((j.hi + 127) >> 7) - (j.lo >> 7) : 0;
     const int rem = j.ntok % T2;
     const int keys = rem > 0 && rem <= a.T;
     j.nrt = nb > 0 ? (j.ntok + T2 - 1) / T2 : 0;
-    j.chunk = j.nrt > keys ? kHCostRows : kHCostKeys;  // the cost of a block that sets the chunk, for now
+    j.chunk = j.nrt > keys;  // for now: whether tiles of two halves set the chunk
     j.nch = nb;
+    // (as far as it is known without causal trimming)
     if (nb > 0)
-      cost += (long long)a.Hkv * ((j.nrt - keys) * (nb * kHCostRows + kHCostTile) + keys * (nb * kHCostKeys + kHCostTile));
+      cost += (long long)a.Hkv *
+              ((j.nrt - keys) * (nb * kHCostRows + kHCostTile) + keys * (nb * kHCostKeys + kHCostTile));
     s.job[q] = j;
   }
-  block_scan(cost, s.scan, &total);
-  const long long goal = max((total + a.ctas - 1) / a.ctas, 1LL);
-  // a thread's jobs and tiles are consecutive from here on
-  const int jper = (njobs + kHPlanThreads - 1) / kHPlanThreads;
+  block_scan(cost, s.scan[0], &total);
+  const long long goal = max(ceil_div(total, a.ctas), 1LL);
   long long mine = 0, all = 0;
-  __syncthreads();
-  for (int q = tid * jper; q < min(njobs, (tid + 1) * jper); ++q) {
+  for (int q = q0; q < q1; ++q) {
     HJob& j = s.job[q];
     const int nb = j.nch;
-    j.chunk = (int)min((goal + j.chunk - 1) / j.chunk, (long long)max(nb, 1));
+    const long long chunk = j.chunk ? (goal + kHCostRows - 1) / kHCostRows : (goal + kHCostKeys - 1) / kHCostKeys;
+    j.chunk = (int)min(chunk, (long long)max(nb, 1));
     j.nch = (nb + j.chunk - 1) / j.chunk;
     mine += (long long)a.Hkv * j.nch * j.nrt;
   }
-  long long at = block_scan(mine, s.scan, &all);
-  for (int q = tid * jper; q < min(njobs, (tid + 1) * jper); ++q) {
+  long long at = block_scan(mine, s.scan[1], &all);
+  for (int q = q0; q < q1; ++q) {
     HJob& j = s.job[q];
     j.tile0 = (int)at;
     s.tile0[q] = (int)at;
     at += (long long)a.Hkv * j.nch * j.nrt;
-    a.ws.jobs[q] = j;
   }
   const int ntiles = (int)min(all, a.tile_cap);  // (all is within the cap: see shared_layout)
   __syncthreads();
 
-  auto tile_of = [&](int i, HTile* t) {
-    const int q = last_le(s.tile0, njobs, i);
-    const HJob& j = s.job[q];
-    int rel = i - j.tile0;
-    const int rt = rel % j.nrt;
-    rel /= j.nrt;
-    const int ch = rel % j.nch;
-    t->g = rel / j.nch;
-    t->tok0 = j.tok0 + rt * T2;
-    t->ntok = min(T2, j.ntok - rt * T2);
-    t->row = j.row;
-    t->lo = j.lo;
-    t->hi = j.hi;
-    int end = (j.hi + 127) >> 7;
-    if (a.causal && q < B)  // keys past the last token's position are nobody's
-      end = min(end, (max(j.hi - j.ntok + rt * T2 + t->ntok, 0) + 127) >> 7);
-    t->blk0 = (j.lo >> 7) + ch * j.chunk;
-    t->nblk = max(min(t->blk0 + j.chunk, end) - t->blk0, 0);
-    t->keys = t->ntok <= a.T;
-    t->pad = 0;
-    return t->nblk ? (long long)t->nblk * (t->keys ? kHCostKeys : kHCostRows) + kHCostTile : 0LL;
-  };
   const int tper = (ntiles + kHPlanThreads - 1) / kHPlanThreads;
-  const int i0 = min(ntiles, tid * tper), i1 = min(ntiles, (tid + 1) * tper);
-  HTile t;
-  cost = 0;
-  for (int i = i0; i < i1; ++i) cost += tile_of(i, &t);
-  const long long before = block_scan(cost, s.scan, &total);
-  const long long share = max((total + a.ctas - 1) / a.ctas, (long long)kHCostRows);
-  // a tile's ranges: those that hold the start of one of its steps
-  auto ranges = [&](HTile* x, long long c0) {
-    const int w = x->keys ? kHCostKeys : kHCostRows;
-    c0 += kHCostTile;
-    x->cost0 = c0;
-    x->cta0 = (int)(c0 / share);
-    x->nseg = x->nblk > 0 ? (int)((c0 + (long long)(x->nblk - 1) * w) / share) - x->cta0 + 1 : 0;
-    // a range may begin after the tile's first step and before its second:
-    // share >= the cost of a step, so each range in between holds one
-    return (long long)x->nseg * x->ntok * a.G * (x->keys ? 2 : 1);
-  };
-  long long run = before, rows = 0;
-  for (int i = i0; i < i1; ++i) {
-    const long long c = tile_of(i, &t);
-    rows += ranges(&t, run);
-    run += c;
+  const int i0 = min(ntiles, tid * tper), i1 = min(ntiles, i0 + tper);
+  HCursor c0{0, 0, 0, 0};
+  if (i0 < i1) {
+    c0.q = last_le(s.tile0, njobs, i0);
+    const HJob& j = s.job[c0.q];
+    const int rel = i0 - j.tile0, x = rel / j.nrt;
+    c0.rt = rel - x * j.nrt;
+    c0.g = x / j.nch;
+    c0.ch = x - c0.g * j.nch;
   }
-  long long part = block_scan(rows, s.scan, &all);
-  run = before;
-  for (int i = i0; i < i1; ++i) {
-    const long long c = tile_of(i, &t);
-    const long long n = ranges(&t, run);
-    run += c;
+  auto advance = [&](HCursor* c) {
+    const HJob* j = &s.job[c->q];
+    if (++c->rt < j->nrt) return;
+    c->rt = 0;
+    if (++c->ch < j->nch) return;
+    c->ch = 0;
+    if (++c->g < a.Hkv) return;
+    c->g = 0;
+    do ++c->q;
+    while (c->q < njobs && s.job[c->q].nrt == 0);
+  };
+  // blocks, tokens and cost of the tile at c
+  auto size_of = [&](const HCursor& c, int* blk0, int* nblk, int* ntok) -> long long {
+    const HJob& j = s.job[c.q];
+    *ntok = min(T2, j.ntok - c.rt * T2);
+    int end = (j.hi + 127) >> 7;
+    if (a.causal && c.q < B)  // keys past the last token's position are nobody's
+      end = min(end, (max(j.hi - j.ntok + c.rt * T2 + *ntok, 0) + 127) >> 7);
+    *blk0 = (j.lo >> 7) + c.ch * j.chunk;
+    *nblk = max(min(*blk0 + j.chunk, end) - *blk0, 0);
+    return *nblk ? (long long)*nblk * (*ntok <= a.T ? kHCostKeys : kHCostRows) + kHCostTile : 0LL;
+  };
+  cost = 0;
+  long long rows = 0;
+  int blk0, nblk, ntok;
+  HCursor c = c0;
+  for (int i = i0; i < i1; ++i, advance(&c)) {
+    cost += size_of(c, &blk0, &nblk, &ntok);
+    rows += nblk ? ntok * a.G * (ntok <= a.T ? 2 : 1) : 0;
+  }
+  long long run, part;
+  long long all_rows;
+  run = block_scan(cost, s.scan[2], &total);
+  part = block_scan(rows, s.scan[3], &all_rows);
+  const long long share = max(ceil_div(total, a.ctas), (long long)kHCostRows);
+  int rg = (int)(total < INT_MAX ? (uint32_t)run / (uint32_t)share : run / share);  // the range that holds `run`
+  long long rg_end = (rg + 1) * share;
+  c = c0;
+  for (int i = i0; i < i1; ++i, advance(&c)) {
+    const long long x = size_of(c, &blk0, &nblk, &ntok);
+    const HJob& j = s.job[c.q];
+    HTile t;
+    t.tok0 = j.tok0 + c.rt * T2;
+    t.ntok = ntok;
+    t.g = c.g;
+    t.row = j.row;
+    t.lo = j.lo;
+    t.hi = j.hi;
+    t.blk0 = blk0;
+    t.nblk = nblk;
+    t.cost0 = run + kHCostTile;
     t.part0 = part;
-    part += n;
-    a.ws.tiles[i] = t;
-    for (int k = 0; k < t.nseg; ++k) {
-      atomicMin(&s.first[t.cta0 + k], i);
-      atomicMax(&s.last[t.cta0 + k], i);
+    t.keys = ntok <= a.T;
+    t.pad = 0;
+    t.nseg = t.cta0 = 0;
+    if (nblk) {
+      // The ranges that hold the start of one of its steps.  (share is at
+      // least a step's cost, so each range between the first and the last
+      // holds one.)  The first tile to touch a range opens it.
+      const long long last = run + x - (t.keys ? kHCostKeys : kHCostRows);
+      if (run == rg_end - share) s.first[rg] = i;
+      int r = rg;
+      long long end = rg_end;
+      for (; t.cost0 >= end; end += share) s.first[++r] = i;
+      t.cta0 = r;
+      for (; last >= end; end += share) s.first[++r] = i;
+      t.nseg = r - t.cta0 + 1;
+      for (; run + x > end; end += share) s.first[++r] = i;
+      if (run + x == end) ++r, end += share;
+      rg = r;
+      rg_end = end;
+      part += ntok * a.G * (t.keys ? 2 : 1);
+      run += x;
     }
+    a.ws.tiles[i] = t;
   }
   for (int i = tid; i < a.total_q; i += kHPlanThreads) {
-    int2 v = make_int2(-1, 0);
+    HTok v{-1, 0, 0, 0, 0, 0, 0, 0};
     if (i >= s.cu[0] && i < s.cu[B]) {
-      const int q = last_le(s.cu, B, i);
-      const int L = s.len[q];
-      v.x = q;
-      v.y = a.causal ? min(max(L - (s.cu[q + 1] - i) + 1, 0), L) : L;
+      const int q = last_le(s.cu, B, i), L = s.len[q];
+      v.seq = q;
+      v.keys = a.causal ? min(max(L - (s.cu[q + 1] - i) + 1, 0), L) : L;
+      const HJob& own = s.job[q];
+      if (own.nrt > 0) {
+        v.own_base = own.tile0 + (i - own.tok0) / T2;
+        v.own_nch = own.nch;
+        v.own_nrt = own.nrt;
+      }
+      if (prefix_of(s.seq_group[q]) > 0) {
+        const HJob& pre = s.job[B + s.seq_group[q]];
+        v.pre_base = pre.tile0 + (i - pre.tok0) / T2;
+        v.pre_nch = pre.nch;
+        v.pre_nrt = pre.nrt;
+      }
     }
     a.ws.tok[i] = v;
   }
   __syncthreads();
-  for (int c = tid; c < a.ctas; c += kHPlanThreads) a.ws.hdr->range[c] = make_int2(s.first[c], s.last[c]);
+  // (a range's last tile may hold none of its steps: it is skipped there)
+  for (int k = tid; k < a.ctas; k += kHPlanThreads)
+    a.ws.hdr->range[k] = make_int2(s.first[k] < 0 ? 0 : s.first[k],
+                                   s.first[k] < 0 ? -1 : (s.first[k + 1] < 0 ? ntiles - 1 : s.first[k + 1]));
   if (tid == 0) {
     a.ws.hdr->share = share;
-    a.ws.hdr->tiles = ntiles;
+    a.ws.hdr->cuts = all_rows;
   }
 }
 
@@ -633,7 +690,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
   const int G = a.G, cta = blockIdx.x;
   pdl_wait();  // the plan
   const int2 range = a.ws.hdr->range[cta];
-  const long long share = a.ws.hdr->share;
+  const long long share = a.ws.hdr->share, cuts = a.ws.hdr->cuts;
 
   if (warp >= 8) {
     regs_dec<kHOtherRegs>();
@@ -797,19 +854,19 @@ __global__ void __launch_bounds__(kHThreads, 1)
           const uint32_t dv = uniform(desc_mn_major(sbase + kHOffKV + sv * kHTileBytes));
           const uint32_t dq = uniform(desc_k_major(sbase + (qp & 1) * kHTileBytes));
           const uint32_t dk = uniform(desc_k_major(sbase + kHOffKV + st * kHTileBytes));
+          if (owed >= 0) wait_v();
+          // P V alone when K (or a new tile's q) may not be there yet
+          const bool alone =
+              i == half || !hwarp_all(mbar_test(&c.kv_full[kp % (2 * kHStages)], (kp / (2 * kHStages)) & 1));
           // In a tile of two halves the groups take turns at the pipe: left
           // alone they can fall into step, both in their softmax at once and
           // then both waiting for each other's products.
           if (!keys) {
             if (h == 1 || nt > 0) wait(&c.turn[h], (nt + h + 1) & 1);
             ++nt;
-            if (!ok) break;
           }
+          if (!ok) break;
           if (owed >= 0) {
-            wait_v();
-            // P V alone when K (or a new tile's q) may not be there yet
-            const bool alone =
-                i == half || !hwarp_all(mbar_test(&c.kv_full[kp % (2 * kHStages)], (kp / (2 * kHStages)) & 1));
             start_pv(tS, dv);
             if (!ok) break;
             if (alone) {
@@ -830,12 +887,12 @@ __global__ void __launch_bounds__(kHThreads, 1)
             if (owed >= 0) rest_pv(tS, dv, &c.kv_empty[sv]);
             mma_qk(tS, dq, dk, id_qk);
             mma_commit(&c.s_full[h]);
+            if (!keys) mbar_arrive(&c.turn[h ^ 1]);
             // (two arrivals free a stage or a q buffer: one of each group, or both of the only one)
             mma_commit(&c.kv_empty[st]);
             if (keys) mma_commit(&c.kv_empty[st]);
             if (last) mma_commit(&c.q_empty[qp & 1]);
             if (last && !keys) mma_commit(&c.q_empty[qp & 1]);
-            if (!keys) mbar_arrive(&c.turn[h ^ 1]);
           }
           __syncwarp();
           if (owed >= 0) done_pv();
@@ -902,11 +959,10 @@ __global__ void __launch_bounds__(kHThreads, 1)
       const int tt = rt + (keys ? 0 : h * a.T);  // the row's token within the tile
       const bool live = rt < a.T && tt < s.t.ntok;
       const long long rows = (long long)s.t.ntok * G;
-      const long long pr =
-          s.t.part0 + (cta - s.t.cta0) * rows * stride + half * rows + tt * G + (r - rt * G);
+      const long long pr = part_row(s.t, cta, cuts) + half * rows + tt * G + (r - rt * G);
       const bool warp_live = __any_sync(0xffffffffu, live);
       int hi = key_end;  // the row sees the keys [lo, hi), all of the warp's rows [lo, warp_hi)
-      if (n > 0 && a.causal && live) hi = min(hi, a.ws.tok[s.t.tok0 + tt].y);
+      if (n > 0 && a.causal && live) hi = min(hi, a.ws.tok[s.t.tok0 + tt].keys);
       const int warp_hi = __reduce_min_sync(0xffffffffu, hi);
       float m = -INFINITY, l = 0.f;
       bool mine = false;  // this group has blocks of the segment
@@ -1043,103 +1099,141 @@ __global__ void __launch_bounds__(kHThreads, 1)
 
 // ------------------------------------------------------------------- join
 // out = sum w_k o_k / sum w_k, w_k = 2^(lse_k - max lse), over the partials of
-// a (token, query head) row: those of its sequence's own tile and of its
-// group's, a chunk and a range each.  One CTA per (token, kv head): its G
-// rows have the same list of partials, made once; a warp then takes a row.
-constexpr int kHJoinThreads = 128;
-// Partials of one row: its two jobs have a chunk each, plus at most `ctas`
-// further chunks (2 x where the job's chunk is counted at twice the tile's
-// cost) and `ctas` cuts, all of them possibly in two halves.
-constexpr int kHJoinMax = 2 * (2 + 3 * kHMaxCtas);
+// a (token, query head) row: those of its sequence's own tiles and of its
+// group's, a chunk and a range each.  One CTA per kv head and `tokens` tokens
+// (several when there are many: a row's chain of dependent loads, token,
+// tiles, log-sum-exps, partials, is what it waits for).  A warp lists a
+// token's partials, which its G rows share; then a warp takes a row at a
+// time, kHJoinDepth partials in flight.  With fewer rows than warps several
+// warps take a row's partials in turn and add up in shared memory.
+constexpr int kHJoinWarps = 8;
+constexpr int kHJoinDepth = 4;
+constexpr int kHJoinTokens = 8;
+// Partials of one row: its two jobs have a chunk each, plus at most
+// kHCostRatio x `ctas` further chunks and `ctas` cuts, all of them possibly in
+// two halves.
+constexpr int kHJoinMax = 2 * (2 + (kHCostRatio + 1) * kHMaxCtas);
 
 struct HJoinArgs {
   HPtrs ws;
   uint8_t* out;
   float* lse;  // may be null
-  int32_t Hkv, G, T, total_q, ctas;
+  int32_t Hkv, G, total_q;
+  int32_t tokens;  // of one CTA
+  int32_t slots;   // rows at once: a power of two, at most the warps
 };
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kHJoinThreads) k_shared_join(HJoinArgs a) {
-  __shared__ int32_t count;
-  __shared__ long long list[kHJoinMax];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t = blockIdx.x / a.Hkv, g = blockIdx.x - t * a.Hkv;
+__global__ void __launch_bounds__(kHJoinWarps * 32) k_shared_join(HJoinArgs a) {
+  extern __shared__ int32_t lists[];  // [tokens][kHJoinMax]
+  __shared__ int32_t count[kHJoinTokens];
+  __shared__ float4 sum[kHJoinWarps][32];
+  __shared__ float weight[kHJoinWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tg = blockIdx.x / a.Hkv, g = blockIdx.x - tg * a.Hkv;
+  const int t0 = tg * a.tokens, nt = min(a.tokens, a.total_q - t0);
   pdl_launch_dependents();
-  if (tid == 0) count = 0;
   pdl_wait();
-  __syncthreads();
-  const int2 tk = a.ws.tok[t];
-  if (tk.x < 0) return;  // outside every sequence: not written
-  if (warp == 0) {
+  if (warp < nt) {
+    const int t = t0 + warp;
+    int32_t* list = lists + warp * kHJoinMax;
+    const HTok tk = a.ws.tok[t];
+    const long long share = a.ws.hdr->share, cuts = a.ws.hdr->cuts;
     int n = 0;
-    const int pj = a.ws.seq_job[tk.x];
-    const long long share = a.ws.hdr->share;
-    for (int w = 0; w < 2; ++w) {
-      const int ji = w == 0 ? pj : tk.x;
-      if (ji < 0) continue;
-      const HJob j = a.ws.jobs[ji];
-      if (j.nrt == 0) continue;
-      const int base = j.tile0 + g * j.nch * j.nrt + (t - j.tok0) / (2 * a.T);
-      for (int c0 = 0; c0 < j.nch; c0 += 32) {
-        HSeg s;
-        s.t.nseg = 0;
-        int mine = 0;
-        if (c0 + lane < j.nch) {
-          s.t = load_tile(a.ws.tiles + base + (c0 + lane) * j.nrt);
-          for (int k = 0; k < s.t.nseg; ++k) {
-            cut(&s, share, s.t.cta0 + k);
-            mine += s.t.keys && s.n > 1 ? 2 : 1;
-          }
-        }
-        int x = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, x, o);
-          if (lane >= o) x += y;
-        }
-        int at = n + x - mine;
-        n += __shfl_sync(0xffffffffu, x, 31);
-        const long long rows = (long long)s.t.ntok * a.G;
+    for (int x0 = 0; x0 < tk.own_nch + tk.pre_nch; x0 += 32) {
+      const int x = x0 + lane;
+      HSeg s;
+      s.t.nseg = s.t.keys = s.t.ntok = s.t.tok0 = s.t.cta0 = 0;
+      s.t.part0 = 0;
+      int mine = 0;
+      if (x < tk.own_nch + tk.pre_nch) {
+        const bool p = x < tk.pre_nch;
+        s.t = load_tile(a.ws.tiles + (p ? tk.pre_base + (g * tk.pre_nch + x) * tk.pre_nrt
+                                        : tk.own_base + (g * tk.own_nch + x - tk.pre_nch) * tk.own_nrt));
         for (int k = 0; k < s.t.nseg; ++k) {
           cut(&s, share, s.t.cta0 + k);
-          const int nh = s.t.keys && s.n > 1 ? 2 : 1;
-          for (int hh = 0; hh < nh; ++hh, ++at)
-            if (at < kHJoinMax)
-              list[at] = s.t.part0 + (k * (s.t.keys ? 2 : 1) + hh) * rows + (long long)(t - s.t.tok0) * a.G;
+          mine += s.t.keys && s.n > 1 ? 2 : 1;
         }
       }
+      int y = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      int at = n + y - mine;
+      n += __shfl_sync(0xffffffffu, y, 31);
+      for (int k = 0; k < s.t.nseg; ++k) {
+        cut(&s, share, s.t.cta0 + k);
+        const int nh = s.t.keys && s.n > 1 ? 2 : 1;
+        for (int hh = 0; hh < nh; ++hh, ++at)
+          if (at < kHJoinMax)  // (rows fit 32 bits: see shared_rows_fit)
+            list[at] = (int)part_row(s.t, s.t.cta0 + k, cuts) + (hh * s.t.ntok + t - s.t.tok0) * a.G;
+      }
     }
-    if (lane == 0) count = min(n, kHJoinMax);
+    if (lane == 0) count[warp] = tk.seq < 0 ? -1 : min(n, kHJoinMax);  // -1: outside every sequence
   }
   __syncthreads();
-  const int n = count;
-  for (int hh = warp; hh < a.G; hh += kHJoinThreads / 32) {
-    float M = -INFINITY;
+  const int splits = kHJoinWarps / a.slots, slot = warp & (a.slots - 1), part = warp / a.slots;
+  for (int i0 = 0; i0 < nt * a.G; i0 += a.slots) {
+    const int row = i0 + slot, x = row / a.G, hh = row - x * a.G;
+    const int n = row < nt * a.G ? count[x] : -1;
+    const int32_t* list = lists + x * kHJoinMax;
+    float M = -INFINITY, W = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = lane; i < n; i += 32) M = hmax_nan(M, a.ws.part_lse[list[i] + hh]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = hmax_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float W = 0.f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const long long pr = list[i] + hh;
-        const float w = ex2_approx(a.ws.part_lse[pr] - M);
-        const float4 o = __ldcs(reinterpret_cast<const float4*>(a.ws.part_o + pr * 128) + lane);
-        acc.x = fmaf(w, o.x, acc.x);
-        acc.y = fmaf(w, o.y, acc.y);
-        acc.z = fmaf(w, o.z, acc.z);
-        acc.w = fmaf(w, o.w, acc.w);
-        W += w;
+    if (n > 0 && M != -INFINITY) {
+      const float4* po = reinterpret_cast<const float4*>(a.ws.part_o) + lane;
+      for (int j0 = part; j0 < n; j0 += kHJoinDepth * splits) {
+        float4 o[kHJoinDepth];
+        float w[kHJoinDepth];
+#pragma unroll
+        for (int u = 0; u < kHJoinDepth; ++u) {
+          const int j = j0 + u * splits;
+          w[u] = -INFINITY;
+          o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (j < n) {  // warp-uniform
+            const long long pr = list[j] + hh;
+            w[u] = a.ws.part_lse[pr];
+            o[u] = __ldcs(po + pr * 32);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kHJoinDepth; ++u) {
+          w[u] = ex2_approx(w[u] - M);
+          acc.x = fmaf(w[u], o[u].x, acc.x);
+          acc.y = fmaf(w[u], o[u].y, acc.y);
+          acc.z = fmaf(w[u], o[u].z, acc.z);
+          acc.w = fmaf(w[u], o[u].w, acc.w);
+          W += w[u];
+        }
       }
     }
-    const float inv = W == 0.f ? 0.f : 1.f / W;
-    const int h = g * a.G + hh;
-    reinterpret_cast<uint2*>(a.out + ((size_t)t * a.Hkv * a.G + h) * 256)[lane] =
-        make_uint2(hpack2<kBf16>(acc.x * inv, acc.y * inv), hpack2<kBf16>(acc.z * inv, acc.w * inv));
-    if (a.lse && lane == 0)
-      a.lse[(size_t)h * a.total_q + t] = W == 0.f ? -INFINITY : (M + lg2_approx(W)) * 0.69314718055994530942f;
+    if (splits > 1) {
+      __syncthreads();  // the previous rows' sums have been read
+      sum[warp][lane] = acc;
+      if (lane == 0) weight[warp] = W;
+      __syncthreads();
+      if (part == 0)
+        for (int k = 1; k < splits; ++k) {
+          const float4 y = sum[warp + k * a.slots][lane];
+          acc.x += y.x;
+          acc.y += y.y;
+          acc.z += y.z;
+          acc.w += y.w;
+          W += weight[warp + k * a.slots];
+        }
+    }
+    if (n >= 0 && part == 0) {
+      const float inv = W == 0.f ? 0.f : 1.f / W;
+      const int h = g * a.G + hh, t = t0 + x;
+      reinterpret_cast<uint2*>(a.out + ((size_t)t * a.Hkv * a.G + h) * 256)[lane] =
+          make_uint2(hpack2<kBf16>(acc.x * inv, acc.y * inv), hpack2<kBf16>(acc.z * inv, acc.w * inv));
+      if (a.lse && lane == 0)
+        a.lse[(size_t)h * a.total_q + t] = W == 0.f ? -INFINITY : (M + lg2_approx(W)) * 0.69314718055994530942f;
+    }
   }
 }
 
@@ -1160,6 +1254,9 @@ PFN_cuTensorMapEncodeTiled_v12000 shared_encode_fn() {
 }  // namespace
 
 size_t shared_workspace_bytes(const mxsa_problem& p) { return shared_layout(p).total; }
+
+// The join lists partial rows in 32 bits (2^31 rows would take 1.1 TB).
+bool shared_rows_fit(const mxsa_problem& p) { return shared_layout(p).row_cap < INT_MAX; }
 
 cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void* k_cache, const void* v_cache,
                                 const int32_t* block_tables, const int64_t* cu, const int32_t* lens, int num_groups,
@@ -1245,11 +1342,15 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
   ja.lse = lse;
   ja.Hkv = p.num_kv_heads;
   ja.G = G;
-  ja.T = T;
   ja.total_q = p.total_q;
-  ja.ctas = ctas;
-  return launch_pdl(bf16 ? k_shared_join<true> : k_shared_join<false>, dim3((unsigned)p.total_q * p.num_kv_heads),
-                    dim3(kHJoinThreads), 0, st, ja);
+  // several tokens to a CTA once there are four CTAs per SM
+  const long long pairs = (long long)p.total_q * p.num_kv_heads;
+  ja.tokens = (int)std::max(1LL, std::min<long long>(kHJoinTokens, pairs / (4LL * sms)));
+  ja.slots = 1;
+  while (ja.slots < G * ja.tokens && ja.slots < kHJoinWarps) ja.slots *= 2;
+  const long long blocks = (long long)((p.total_q + ja.tokens - 1) / ja.tokens) * p.num_kv_heads;
+  return launch_pdl(bf16 ? k_shared_join<true> : k_shared_join<false>, dim3((unsigned)blocks), dim3(kHJoinWarps * 32),
+                    (size_t)ja.tokens * kHJoinMax * 4, st, ja);
 }
 
 }  // namespace mxsa

@@ -268,7 +268,7 @@ mxsa_status mxsa_dense_fwd(const mxsa_problem* problem, const void* q, const voi
  *                and partial rows (FP32); needs no initialisation, keeps
  *                nothing between calls
  * The other arguments and limits are mxsa_dense_fwd's: kv_dtype = q_dtype,
- * num_seqs <= 1024, topk unused; also total_q * num_kv_heads < 2^31.  The
+ * num_seqs <= 1024, topk unused; also total_q * num_q_heads < 2^29 - 2^15.  The
  * softmax weights are rounded to q_dtype before they multiply V, everything
  * else is FP32.  A NaN or infinity at a key outside [0, used_kv_len) of a
  * sequence does not reach its rows; under causal masking the V rows of a

@@ -15,7 +15,7 @@ import pytest
 
 from tests.test_barrier_models import Bar
 
-MAXC, WR, WK, TILE, STAGES = 160, 4, 2, 2, 5
+MAXC, WR, WK, TILE, STAGES = 160, 8, 5, 10, 5
 
 
 def cdiv(a, b):
@@ -72,14 +72,34 @@ def plan(p):
         t["cost0"] = cost + TILE
         cost += t["n"] * t["w"] + TILE if t["n"] else 0
     share = max(cdiv(cost, p["ctas"]), WR)
-    part = 0
-    for t in tiles:
-        t["cta0"] = t["cost0"] // share
-        t["nseg"] = (t["cost0"] + (t["n"] - 1) * t["w"]) // share - t["cta0"] + 1 if t["n"] else 0
-        assert t["cta0"] + t["nseg"] <= p["ctas"] or t["n"] == 0
-        t["part0"] = part
-        part += t["nseg"] * t["ntok"] * G * (2 if t["keys"] else 1)
-    return jobs, tiles, share, part
+    part, run, first = 0, 0, {}
+    for i, t in enumerate(tiles):  # as the plan's threads walk them
+        t["part0"], t["nseg"], t["cta0"] = part, 0, 0
+        if not t["n"]:
+            continue
+        x = t["n"] * t["w"] + TILE
+        last = run + x - t["w"]
+        r = run // share
+        end = (r + 1) * share
+        if run == end - share:
+            first[r] = i
+        while t["cost0"] >= end:
+            r, end = r + 1, end + share
+            first[r] = i
+        t["cta0"] = r
+        while last >= end:
+            r, end = r + 1, end + share
+            first[r] = i
+        t["nseg"] = r - t["cta0"] + 1
+        while run + x > end:
+            r, end = r + 1, end + share
+            first[r] = i
+        part += t["ntok"] * G * (2 if t["keys"] else 1)
+        run += x
+        assert t["cta0"] == t["cost0"] // share and t["cta0"] + t["nseg"] - 1 == last // share < p["ctas"]
+    assert all(k < p["ctas"] for k in first)
+    ranges = {k: (first[k], first.get(k + 1, len(tiles) - 1)) for k in first}
+    return jobs, tiles, share, part, ranges
 
 
 def cut(t, share, c):
@@ -109,10 +129,11 @@ def test_plan_covers_every_key_once_within_its_bounds(seed):
     p = random_problem(random.Random(seed))
     G, B = p["hq"] // p["hkv"], len(p["lens"])
     T = 128 // G
-    jobs, tiles, share, part = plan(p)
+    jobs, tiles, share, part, ranges = plan(p)
     assert len(tiles) <= p["hkv"] * (2 * (p["total_q"] // (2 * T)) + 2 * B) + 2 * MAXC
-    assert part <= 4 * p["total_q"] * p["hq"] + 256 * 3 * MAXC
-    first, last = {}, {}
+    # rows of the tiles' first segments, then 256 for each range's cut
+    assert part + 256 * p["ctas"] <= 4 * p["total_q"] * p["hq"] + 256 * 3 * MAXC
+    assert all(t["ntok"] * G * (2 if t["keys"] else 1) <= 256 for t in tiles)
     for i, t in enumerate(tiles):
         got = 0
         for k in range(t["nseg"]):
@@ -120,8 +141,8 @@ def test_plan_covers_every_key_once_within_its_bounds(seed):
             i0, n = cut(t, share, c)
             assert n > 0 and i0 == got  # each range between the first and the last holds a step
             got += n
-            first[c] = min(first.get(c, i), i)
-            last[c] = max(last.get(c, i), i)
+            assert ranges[c][0] <= i <= ranges[c][1]
+            assert k == 0 or i == ranges[c][0]  # a range's cut is its first tile
         assert got == t["n"]
         for c in (t["cta0"] - 1, t["cta0"] + t["nseg"]):
             assert t["n"] == 0 or cut(t, share, c)[1] == 0
