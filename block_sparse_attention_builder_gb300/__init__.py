@@ -154,7 +154,7 @@ def _check(status: int, what: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # (the argument types make it a pointer)
 
 
 _ELEM_BYTES = {BF16: 2, FP16: 2, FP8_E4M3: 1}
@@ -166,13 +166,11 @@ def _need(what: str, name: str, t: Optional[torch.Tensor], nbytes: int):
     carries no size: a tensor smaller than that shape, or not contiguous,
     is refused here, before the C call (MXSA_ERR_INVALID_ARG).  Only bytes
     are compared, so raw views of a cache (uint8, int16) are accepted."""
-    if t is None:
+    if t is None or (t.is_contiguous() and t.nbytes >= nbytes):
         return
     if not t.is_contiguous():
         raise MxsaError(1, f"{what}: {name} is not contiguous")
-    have = t.numel() * t.element_size()
-    if have < nbytes:
-        raise MxsaError(1, f"{what}: {name} holds {have} bytes, the problem needs {nbytes}")
+    raise MxsaError(1, f"{what}: {name} holds {t.nbytes} bytes, the problem needs {nbytes}")
 
 
 def _need_attention(what: str, prob: Problem, q=None, k_cache=None, v_cache=None, block_tables=None,
@@ -192,10 +190,8 @@ def _need_attention(what: str, prob: Problem, q=None, k_cache=None, v_cache=None
     _need(what, "lse", lse, rows * 4)
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+def _stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def make_problem(num_seqs, total_q, num_q_heads, num_kv_heads, topk, page_size, num_pages, max_pages_per_seq,
@@ -371,13 +367,13 @@ def load_kv(prob, loc, k_cache, v_cache, k, v, idx_cache=None, idx_k=None, flags
 def _token_stride(what: str, name: str, t: torch.Tensor, n: int, heads: int, dim: int) -> int:
     """Elements between the tokens of t [n, heads, dim], a dense tensor or a
     view of a packed projection (a token's heads next to each other)."""
-    if tuple(t.shape) != (n, heads, dim) or t.element_size() != 2:
+    if t.shape != (n, heads, dim) or t.element_size() != 2:
         raise MxsaError(1, f"{what}: {name} is {tuple(t.shape)} of {t.dtype}, the problem needs "
                            f"{(n, heads, dim)} of a 16-bit type")
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != dim):
+    token, head, one = t.stride()
+    if one != 1 or (head != dim and heads > 1):
         raise MxsaError(1, f"{what}: the heads of {name} are not next to each other")
-    return st[0] if n > 1 else heads * dim
+    return token if n > 1 else heads * dim
 
 
 def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_cache, q_weight=None, k_weight=None,
@@ -396,45 +392,44 @@ def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_ca
     optional int32 device tensor (MXSA_FLAG_POS, MXSA_FLAG_PAGE)."""
     what = "mxsa_norm_rope_store"
     n, hq, hkv = loc.numel(), prob.num_q_heads, prob.num_kv_heads
-    kb = _ELEM_BYTES.get(prob.kv_dtype, 2)
-    cfg = NormRope()
-    cfg.q_stride = _token_stride(what, "q", q, n, hq, 128)
-    cfg.k_stride = _token_stride(what, "k", k, n, hkv, 128)
-    cfg.v_stride = _token_stride(what, "v", v, n, hkv, 128)
     if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
         raise MxsaError(1, f"{what}: cos_sin must be float32 [positions, rot_dim]")
-    cfg.num_positions, cfg.rot_dim = cos_sin.shape
+    q_stride = _token_stride(what, "q", q, n, hq, 128)
+    k_stride = _token_stride(what, "k", k, n, hkv, 128)
+    v_stride = _token_stride(what, "v", v, n, hkv, 128)
     _need(what, "cos_sin", cos_sin, 0)
     _need(what, "positions", positions, n * 8)
     _need(what, "loc", loc, n * 8)
     _need(what, "q_out", q_out, n * hq * 256)
     rows = max(prob.num_pages, 0) * max(hkv, 0) * max(prob.page_size, 0)
-    _need(what, "k_cache", k_cache, rows * _ROW_BYTES.get(prob.kv_dtype, 256))
-    _need(what, "v_cache", v_cache, rows * _ROW_BYTES.get(prob.kv_dtype, 256))
-    idx = 0
+    cache = rows * _ROW_BYTES.get(prob.kv_dtype, 256)
+    _need(what, "k_cache", k_cache, cache)
+    _need(what, "v_cache", v_cache, cache)
+    idx = iq_stride = ik_stride = 0
     if idx_q is not None or idx_k is not None:
         if idx_q is None or idx_k is None or idx_q_out is None or idx_cache is None:
             raise MxsaError(1, f"{what}: idx_q, idx_k, idx_q_out and idx_cache come together")
+        kb = _ELEM_BYTES.get(prob.kv_dtype, 2)
         idx = int(idx_q.shape[-1])
-        cfg.idx_q_stride = _token_stride(what, "idx_q", idx_q, n, hkv, idx)
-        cfg.idx_k_stride = _token_stride(what, "idx_k", idx_k, n, hkv, idx)
+        iq_stride = _token_stride(what, "idx_q", idx_q, n, hkv, idx)
+        ik_stride = _token_stride(what, "idx_k", idx_k, n, hkv, idx)
         _need(what, "idx_q_out", idx_q_out, n * hkv * idx * kb)
         _need(what, "idx_cache", idx_cache, rows * idx * kb)
-    cfg.idx_dim, cfg.interleaved, cfg.eps = idx, int(bool(interleaved)), eps
     per_head = None
     for name, w, heads, dim in (("q_weight", q_weight, hq, 128), ("k_weight", k_weight, hkv, 128),
                                 ("idx_q_weight", idx_q_weight, hkv, idx), ("idx_k_weight", idx_k_weight, hkv, idx)):
         if w is None:
             continue
         ph = w.dim() == 2
-        if per_head not in (None, ph) or tuple(w.shape) != ((heads, dim) if ph else (dim,)):
+        if per_head not in (None, ph) or w.shape != ((heads, dim) if ph else (dim,)):
             raise MxsaError(1, f"{what}: {name} is {tuple(w.shape)}: all weights are [dim], or all [heads, dim]")
         if w.element_size() != 2:
             raise MxsaError(1, f"{what}: {name} is {w.dtype}: the weights have the query's type")
         _need(what, name, w, 0)
         per_head = ph
-    cfg.weight_per_head = int(bool(per_head))
     _need(what, "flags", flags, 4)
+    cfg = NormRope(q_stride, k_stride, v_stride, iq_stride, ik_stride, cos_sin.shape[0], cos_sin.shape[1],
+                   bool(interleaved), bool(per_head), idx, eps)
     _check(_lib.mxsa_norm_rope_store(ctypes.byref(prob), ctypes.byref(cfg), n, _ptr(positions), _ptr(loc),
                                      _ptr(cos_sin), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight),
                                      _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _ptr(idx_q), _ptr(idx_k),

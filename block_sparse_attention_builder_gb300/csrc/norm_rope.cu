@@ -13,22 +13,32 @@
 //
 // Bound: HBM.  Each row is read once and written once; a token's cosines and
 // sines (up to 512 bytes) and the weight rows come from L1/L2.  Sixteen lanes
-// hold a row, 8 values (16 bytes) each, so a row's loads and stores are whole
-// lines, its sum of squares is four shuffles, and a partner half is one
-// shuffle of the raw 16 bytes away (4 registers, not 8 normed floats).  A
-// half-warp takes kRopeRows rows of one token: that many 16-byte loads are in
-// flight per lane, and the cosines, sines and weights are read once for them.
+// hold a row (eight an index row of 64), two pieces of 4 values each.  With
+// pairs (i, i + R / 2) a lane's pieces are the two halves of its pairs, so the
+// rotation needs no other lane; otherwise they are neighbours.  A half-warp
+// takes kRopeRows rows of one token: that many loads are in flight per lane,
+// and position, slot, cosines, sines and shared weights are read once.
+//
+// What held it back was instructions, 221 per 32 lanes of 8 values (68% of the
+// issue slots, DRAM at 42%), until the arithmetic was packed in pairs, the
+// row addresses became steps and each half-warp its own shuffle group.
+// 32768 tokens of 64 + 8 + 8 heads, bf16 (1.36 GB, 203 us at the copy rate):
+// 386 us with sixteen consecutive bytes to a lane and the partner's bytes by
+// shuffle, each value normed twice; 324 us with a lane's pieces as above (runs
+// of a token's rows with the next rows prefetched: 340 us); 240 us, 5.7 TB/s,
+// now.  2 or 8 rows at a time: 294 and 332 us.
 #include <algorithm>
 #include <climits>
 
 #include "cast.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace mxsa {
 
 namespace {
 
-constexpr int kRopeRows = 4;      // rows of a 16-lane group
+constexpr int kRopeRows = 4;      // rows of a task
 constexpr int kRopeThreads = 256;
 
 // what a part's rows become
@@ -39,7 +49,7 @@ struct RopePart {
   const uint16_t* w;   // null: no norm
   uint8_t* dst;
   long long stride;    // elements between tokens
-  int32_t heads, dim, tasks;  // tasks: 16-lane groups of one token
+  int32_t heads, dim, tasks;  // tasks: kRopeRows x 16 lanes of one token's rows
   int32_t dst_kind, rotate, w_stride;
 };
 
@@ -55,194 +65,224 @@ struct RopeArgs {
   float eps;
 };
 
+// four packed 16-bit values as two pairs
 template <bool kBf16>
-__device__ __forceinline__ void unpack8(const uint4& s, float* x) {
-  const uint32_t w[4] = {s.x, s.y, s.z, s.w};
+__device__ __forceinline__ void unpack4(const uint2& s, uint64_t* x) {
+  const uint32_t w[2] = {s.x, s.y};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
     if (kBf16) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      x[i] = pack_f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     } else {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
+      x[i] = pack_f2(f.x, f.y);
     }
   }
 }
 
 template <bool kBf16>
-__device__ __forceinline__ uint4 pack8(const float* y) {
-  uint32_t w[4];
+__device__ __forceinline__ uint2 pack4(const uint64_t* y) {
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 2; ++i) {
+    const float2 f = unpack_f2(y[i]);
     if (kBf16) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     } else {
-      const __half2 h = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+      const __half2 h = __floats2half2_rn(f.x, f.y);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ uint2 pack8_e4m3(const float* y) {
-  return make_uint2(e4m3_code2(y[0], y[1]) | (e4m3_code2(y[2], y[3]) << 16),
-                    e4m3_code2(y[4], y[5]) | (e4m3_code2(y[6], y[7]) << 16));
+__device__ __forceinline__ uint32_t pack4_e4m3(const uint64_t* y) {
+  const float2 f = unpack_f2(y[0]), g = unpack_f2(y[1]);
+  return e4m3_code2(f.x, f.y) | (e4m3_code2(g.x, g.y) << 16);
 }
 
 // kKind: the caches' kind.  kInter: rotated pairs side by side.
 template <int kKind, bool kBf16, bool kInter>
-__global__ void __launch_bounds__(kRopeThreads) k_norm_rope(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, kKind == kKindFp4 ? 4 : 5) k_norm_rope(const __grid_constant__ RopeArgs a) {
+  // a lane's pieces are the halves of its pairs; not for NVFP4, whose groups
+  // of 16 values are then two neighbouring lanes
+  constexpr bool kPair = !kInter && kKind != kKindFp4;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, hl = lane & 15;
-  uint32_t task = blockIdx.x * (kRopeThreads / 16) + (threadIdx.x >> 4);
-  bool live = task < a.total;
-  if (!live) task = 0;  // keeps its lanes for the warp's shuffles
+  const uint32_t hmask = 0xFFFFu << (lane & 16);  // the half-warp: all of it takes the same way below
+  const uint32_t task = blockIdx.x * (kRopeThreads / 16) + (threadIdx.x >> 4);
+  if (task >= a.total) return;
   const uint32_t t = task / (uint32_t)a.per_token;
   int r = (int)(task - t * (uint32_t)a.per_token), pi = 0;
   while (r >= a.part[pi].tasks) r -= a.part[pi++].tasks;
   const RopePart& p = a.part[pi];
-  const int lpr = p.dim >> 3;        // lanes of a row: 16 or 8
-  const int rpp = lpr == 16 ? 1 : 2; // rows side by side in 16 lanes
-  const int e = (hl & (lpr - 1)) * 8;
+  const int lpr = p.dim >> 3;         // lanes of a row: 16 or 8
+  const int rpp = lpr == 16 ? 1 : 2;  // rows side by side in 16 lanes
+  const int l = hl & (lpr - 1);
   const int h0 = r * (kRopeRows * rpp) + (lpr == 16 ? 0 : hl >> 3);
+  const int left = (p.heads - h0 + rpp - 1) / rpp;  // rows of the lane's column, at most kRopeRows of them here
+  // first columns of the lane's two pieces
+  const int half = a.rot >> 1;
+  int ea = 8 * l, eb = 8 * l + 4;
+  bool turn = p.rotate && ea < a.rot;
+  if (kPair && p.rotate) {
+    const int turning = half >> 2;  // lanes that hold pairs
+    turn = l < turning;
+    ea = turn ? 4 * l : a.rot + 8 * (l - turning);
+    eb = turn ? ea + half : ea + 4;
+  }
 
   // the rows first: nothing they need waits for the position
-  uint4 raw[kRopeRows];
-  const uint16_t* src = p.src + (long long)t * p.stride + e;
+  uint2 ra[kRopeRows], rb[kRopeRows];
+  const uint16_t* src = p.src + (long long)t * p.stride + h0 * p.dim;
+  const int step = rpp * p.dim;
 #pragma unroll
   for (int u = 0; u < kRopeRows; ++u) {
-    const int h = h0 + u * rpp;
-    raw[u] = live && h < p.heads ? *reinterpret_cast<const uint4*>(src + (long long)h * p.dim)
-                                 : make_uint4(0, 0, 0, 0);
+    ra[u] = rb[u] = make_uint2(0, 0);
+    if (u < left) {
+      ra[u] = *reinterpret_cast<const uint2*>(src + u * step + ea);
+      rb[u] = *reinterpret_cast<const uint2*>(src + u * step + eb);
+    }
   }
   const long long pos = a.positions[t];
-  if (pos < 0) live = false;  // padding: the token is left out
+  if (pos < 0) return;  // padding: the token is left out
   if (pos >= a.num_positions) {
-    if (live && a.flags && pi == 0 && r == 0 && hl == 0) atomicOr(a.flags, MXSA_FLAG_POS);
-    live = false;
+    if (a.flags && pi == 0 && r == 0 && hl == 0) atomicOr(a.flags, MXSA_FLAG_POS);
+    return;
   }
-  long long page = 0, off = 0;
+  // where the first row goes, and the bytes from one row to the next
+  const int es = kKind == kKindFp8 && p.dst_kind != kDstDense16 ? 1 : 2;
+  uint8_t* dst = p.dst + ((long long)t * p.heads + h0) * (p.dim * es);
+  long long dstep = step * es, off = 0;
   if (p.dst_kind == kDstCache) {
-    const long long l = a.loc[t];
-    if (l >= a.slots && live && a.flags && pi == 1 && r == 0 && hl == 0) atomicOr(a.flags, MXSA_FLAG_PAGE);
-    if (l < 0 || l >= a.slots) live = false;
-    page = l >> a.page_shift;
-    off = l & ((1LL << a.page_shift) - 1);
+    const long long slot = a.loc[t];
+    if (slot >= a.slots && a.flags && pi == 1 && r == 0 && hl == 0) atomicOr(a.flags, MXSA_FLAG_PAGE);
+    if (slot < 0 || slot >= a.slots) return;
+    off = slot & ((1LL << a.page_shift) - 1);
+    const long long slab = (slot >> a.page_shift) * p.heads + h0;
+    if (kKind == kKindFp4) {
+      dst = p.dst + slab * (72LL << a.page_shift);
+      dstep = (72LL * rpp) << a.page_shift;
+    } else {
+      dst = p.dst + (slab << a.page_shift | off) * (p.dim * es);
+      dstep <<= a.page_shift;
+    }
   }
 
-  const int half = a.rot >> 1;
-  const bool turn = p.rotate && e < a.rot;
-  float c[8], s[8];  // interleaved: the first four of each
-  if (turn && live) {
-    const float* cs = a.cos_sin + pos * a.rot;
-    const int j = kInter ? e >> 1 : (e < half ? e : e - half);
+  if (!p.rotate && kKind != kKindFp4) {  // V: the store's own cast
 #pragma unroll
-    for (int i = 0; i < (kInter ? 1 : 2); ++i) {
+    for (int u = 0; u < kRopeRows; ++u)
+      if (u < left)
+        put_chunk(make_uint4(ra[u].x, ra[u].y, rb[u].x, rb[u].y), dst + u * dstep, ea, kKind == kKindFp8, kBf16);
+    return;
+  }
+
+  // Cosines and sines of the lane's four pairs.  kPair: as pairs of
+  // neighbours.  Side by side: each twice, the sines' first copy negated.
+  // NVFP4 with pairs (i, i + R/2): of its eight columns, the sines signed for
+  // the partner's value.
+  constexpr int kAngles = kPair ? 2 : 4;
+  uint64_t c[kAngles], s[kAngles], w[4];
+  if (turn) {
+    const float* cs = a.cos_sin + pos * a.rot;
+    const int j = kPair ? ea : (kInter ? ea >> 1 : (ea < half ? ea : ea - half));
+    const float sign = !kPair && !kInter && ea < half ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < (kPair || kInter ? 1 : 2); ++i) {
       const float4 cv = reinterpret_cast<const float4*>(cs + j)[i];
       const float4 sv = reinterpret_cast<const float4*>(cs + half + j)[i];
-      c[4 * i] = cv.x, c[4 * i + 1] = cv.y, c[4 * i + 2] = cv.z, c[4 * i + 3] = cv.w;
-      s[4 * i] = sv.x, s[4 * i + 1] = sv.y, s[4 * i + 2] = sv.z, s[4 * i + 3] = sv.w;
+      if (kInter) {
+        c[0] = pack_f2(cv.x, cv.x), c[1] = pack_f2(cv.y, cv.y), c[2] = pack_f2(cv.z, cv.z), c[3] = pack_f2(cv.w, cv.w);
+        s[0] = pack_f2(-sv.x, sv.x), s[1] = pack_f2(-sv.y, sv.y);
+        s[2] = pack_f2(-sv.z, sv.z), s[3] = pack_f2(-sv.w, sv.w);
+      } else {
+        c[2 * i] = pack_f2(cv.x, cv.y), c[2 * i + 1] = pack_f2(cv.z, cv.w);
+        s[2 * i] = pack_f2(sign * sv.x, sign * sv.y), s[2 * i + 1] = pack_f2(sign * sv.z, sign * sv.w);
+      }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
   }
-  // half layout: the lane that holds the other value of this lane's pairs
-  const int step = half >> 3;
-  const int partner = turn ? (e < half ? lane + step : lane - step) : lane;
-  const int pe = turn ? (e < half ? e + half : e - half) : e;  // its first column
-  const float sign = e < half ? -1.f : 1.f;
+  const uint16_t* wr = p.w + h0 * p.w_stride;
+  auto load_weights = [&](int u) {
+    unpack4<kBf16>(*reinterpret_cast<const uint2*>(wr + u * rpp * p.w_stride + ea), w);
+    unpack4<kBf16>(*reinterpret_cast<const uint2*>(wr + u * rpp * p.w_stride + eb), w + 2);
+  };
+  if (p.w && p.w_stride == 0) load_weights(0);
 
 #pragma unroll
   for (int u = 0; u < kRopeRows; ++u) {
-    const int h = h0 + u * rpp;
-    const bool row = live && h < p.heads;
-    float x[8], y[8];
-    unpack8<kBf16>(raw[u], x);
-    // every lane of the warp takes part in the shuffles: its two halves may
-    // hold rows of different parts
-    float ss = 0.f;
+    // (rows past the last head hold zeros and are not written; the lanes keep
+    // to the half-warp's shuffles)
+    uint64_t y[4];
+    unpack4<kBf16>(ra[u], y);
+    unpack4<kBf16>(rb[u], y + 2);
+    if (p.w) {
+      const float2 s2 = unpack_f2(fma_f2(y[3], y[3], fma_f2(y[2], y[2], fma_f2(y[1], y[1], mul_f2(y[0], y[0])))));
+      float ss = s2.x + s2.y;
+      ss += __shfl_xor_sync(hmask, ss, 1);
+      ss += __shfl_xor_sync(hmask, ss, 2);
+      ss += __shfl_xor_sync(hmask, ss, 4);
+      if (lpr == 16) ss += __shfl_xor_sync(hmask, ss, 8);
+      const float rms = rsqrtf(fmaf(ss, lpr == 16 ? 1.f / 128 : 1.f / 64, a.eps));
+      if (p.w_stride && u < left) load_weights(u);
+      const uint64_t rms2 = pack_f2(rms, rms);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-    ss += __shfl_xor_sync(0xffffffffu, ss, 1);
-    ss += __shfl_xor_sync(0xffffffffu, ss, 2);
-    ss += __shfl_xor_sync(0xffffffffu, ss, 4);
-    const float side = __shfl_xor_sync(0xffffffffu, ss, 8);
-    if (lpr == 16) ss += side;
-    const float rms = __frsqrt_rn(ss / (float)p.dim + a.eps);
-    uint4 other = raw[u];
-    if (!kInter) {
-      other.x = __shfl_sync(0xffffffffu, raw[u].x, partner);
-      other.y = __shfl_sync(0xffffffffu, raw[u].y, partner);
-      other.z = __shfl_sync(0xffffffffu, raw[u].z, partner);
-      other.w = __shfl_sync(0xffffffffu, raw[u].w, partner);
+      for (int i = 0; i < 4; ++i) y[i] = mul_f2(mul_f2(y[i], rms2), w[i]);
     }
-    if (p.w && row) {
-      const uint16_t* wr = p.w + (long long)h * p.w_stride;
-      float w[8];
-      unpack8<kBf16>(*reinterpret_cast<const uint4*>(wr + e), w);
+    if (kPair) {
+      if (turn) {  // (columns past R keep infinities and NaN to themselves)
+        const uint64_t minus = pack_f2(-1.f, -1.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = x[i] * rms * w[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = x[i];
-    }
-    if (turn) {
-      if (kInter) {
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t ya = y[i], yb = y[i + 2];
+          y[i] = fma_f2(mul_f2(yb, s[i]), minus, mul_f2(ya, c[i]));
+          y[i + 2] = fma_f2(ya, s[i], mul_f2(yb, c[i]));
+        }
+      }
+    } else if (kInter) {
+      if (turn) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float ya = y[2 * i], yb = y[2 * i + 1];
-          y[2 * i] = ya * c[i] - yb * s[i];
-          y[2 * i + 1] = yb * c[i] + ya * s[i];
+          const float2 f = unpack_f2(y[i]);
+          y[i] = fma_f2(pack_f2(f.y, f.x), s[i & (kAngles - 1)], mul_f2(y[i], c[i & (kAngles - 1)]));
         }
+      }
+    } else {
+      const int partner = turn ? (ea < half ? lane + (half >> 3) : lane - (half >> 3)) : lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t o = __shfl_sync(hmask, y[i], partner);
+        if (turn) y[i] = fma_f2(o, s[i & (kAngles - 1)], mul_f2(y[i], c[i & (kAngles - 1)]));
+      }
+    }
+    uint8_t* to = dst + u * dstep;
+    if (kKind == kKindFp4 && p.dst_kind == kDstCache) {
+      float x[8], amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_f2(y[i]);
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));  // fmaxf drops a NaN operand
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(hmask, amax, 1));
+      float sd;
+      const uint32_t sc = nvfp4_scale(amax, &sd);
+      uint32_t codes = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) codes |= nvfp4_code(x[i], sd) << (4 * i);
+      if (u < left) {
+        *reinterpret_cast<uint32_t*>(to + off * 64 + (ea >> 1)) = codes;
+        if (!(lane & 1)) to[(64LL << a.page_shift) + off * 8 + (ea >> 4)] = (uint8_t)sc;
+      }
+    } else if (u < left) {
+      if (es == 1) {
+        *reinterpret_cast<uint32_t*>(to + ea) = pack4_e4m3(y);
+        *reinterpret_cast<uint32_t*>(to + eb) = pack4_e4m3(y + 2);
       } else {
-        float yo[8];
-        unpack8<kBf16>(other, yo);
-        if (p.w && row) {
-          float w[8];
-          unpack8<kBf16>(*reinterpret_cast<const uint4*>(p.w + (long long)h * p.w_stride + pe), w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) yo[i] = yo[i] * rms * w[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * c[i] + sign * yo[i] * s[i];
+        *reinterpret_cast<uint2*>(to + 2 * ea) = pack4<kBf16>(y);
+        *reinterpret_cast<uint2*>(to + 2 * eb) = pack4<kBf16>(y + 2);
       }
-    }
-    float amax = 0.f;
-    if (kKind == kKindFp4) {  // a group of 16 values is two lanes
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(y[i]));  // fmaxf drops a NaN operand
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    }
-    if (p.dst_kind == kDstCache) {
-      const long long at = page * p.heads + h;  // (page, head) slab
-      if (kKind == kKindFp4) {
-        if (row) {
-          float sd;
-          const uint32_t sc = nvfp4_scale(amax, &sd);
-          uint32_t codes = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) codes |= nvfp4_code(y[i], sd) << (4 * i);
-          uint8_t* slab = p.dst + at * (72LL << a.page_shift);
-          *reinterpret_cast<uint32_t*>(slab + off * 64 + (e >> 1)) = codes;
-          if (!(lane & 1)) slab[(64LL << a.page_shift) + off * 8 + (e >> 4)] = (uint8_t)sc;
-        }
-      } else if (row) {
-        const long long elem = (at << a.page_shift | off) * p.dim + e;
-        if (!p.rotate) put_chunk(raw[u], p.dst, elem, kKind == kKindFp8, kBf16);  // V: the store's own cast
-        else if (kKind == kKindFp8) *reinterpret_cast<uint2*>(p.dst + elem) = pack8_e4m3(y);
-        else *reinterpret_cast<uint4*>(p.dst + 2 * elem) = pack8<kBf16>(y);
-      }
-    } else if (row) {
-      const long long elem = ((long long)t * p.heads + h) * p.dim + e;
-      if (kKind == kKindFp8 && p.dst_kind == kDstDenseCast)
-        *reinterpret_cast<uint2*>(p.dst + elem) = pack8_e4m3(y);
-      else
-        *reinterpret_cast<uint4*>(p.dst + 2 * elem) = pack8<kBf16>(y);
     }
   }
 }

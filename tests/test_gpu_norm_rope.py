@@ -239,6 +239,20 @@ def test_in_place_empty_and_special_values():
     assert (e["q_out"] == 7).all()
 
 
+@pytest.mark.parametrize("kv,inter", [("bf16", False), ("fp8", True), ("nvfp4", False), ("nvfp4", True)])
+def test_infinities_past_the_rotated_columns_stay_in_their_column(kv, inter):
+    c = case(6, 4, 2, "bf16", kv, 64, 32, inter=inter, weights=False, packed=False, seed=31)
+    want = case(6, 4, 2, "bf16", kv, 64, 32, inter=inter, weights=False, packed=False, seed=31)
+    call(want)
+    c["q"][0, 0, 40], c["q"][1, 2, 100] = float("inf"), float("nan")
+    call(c)
+    torch.cuda.synchronize()
+    same = torch.ones(6, 4, 128, dtype=torch.bool, device="cuda")
+    same[0, 0, 40] = same[1, 2, 100] = False
+    assert torch.equal(c["q_out"][same], want["q_out"][same])
+    assert c["q_out"][0, 0, 40] == float("inf") and c["q_out"][1, 2, 100].isnan()
+
+
 def test_captured_and_replayed_on_another_stream():
     c = case(64, 16, 2, "bf16", "bf16", 64, 128, idx=128, seed=21)
     want = case(64, 16, 2, "bf16", "bf16", 64, 128, idx=128, seed=22)
