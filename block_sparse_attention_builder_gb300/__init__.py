@@ -190,8 +190,17 @@ def _need_attention(what: str, prob: Problem, q=None, k_cache=None, v_cache=None
     _need(what, "lse", lse, rows * 4)
 
 
+# the current stream's handle without a Stream object around it (a fifth of a
+# small call's host time), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def make_problem(num_seqs, total_q, num_q_heads, num_kv_heads, topk, page_size, num_pages, max_pages_per_seq,
@@ -416,10 +425,9 @@ def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_ca
         _need(what, "idx_q_out", idx_q_out, n * hkv * idx * kb)
         _need(what, "idx_cache", idx_cache, rows * idx * kb)
     per_head = None
-    for name, w, heads, dim in (("q_weight", q_weight, hq, 128), ("k_weight", k_weight, hkv, 128),
-                                ("idx_q_weight", idx_q_weight, hkv, idx), ("idx_k_weight", idx_k_weight, hkv, idx)):
-        if w is None:
-            continue
+
+    def weight(name, w, heads, dim):
+        nonlocal per_head
         ph = w.dim() == 2
         if per_head not in (None, ph) or w.shape != ((heads, dim) if ph else (dim,)):
             raise MxsaError(1, f"{what}: {name} is {tuple(w.shape)}: all weights are [dim], or all [heads, dim]")
@@ -427,6 +435,15 @@ def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_ca
             raise MxsaError(1, f"{what}: {name} is {w.dtype}: the weights have the query's type")
         _need(what, name, w, 0)
         per_head = ph
+
+    if q_weight is not None:
+        weight("q_weight", q_weight, hq, 128)
+    if k_weight is not None:
+        weight("k_weight", k_weight, hkv, 128)
+    if idx_q_weight is not None:
+        weight("idx_q_weight", idx_q_weight, hkv, idx)
+    if idx_k_weight is not None:
+        weight("idx_k_weight", idx_k_weight, hkv, idx)
     _need(what, "flags", flags, 4)
     cfg = NormRope(q_stride, k_stride, v_stride, iq_stride, ik_stride, cos_sin.shape[0], cos_sin.shape[1],
                    bool(interleaved), bool(per_head), idx, eps)

@@ -53,7 +53,8 @@ struct alignas(16) HTile {
   long long part0;                 // partial row of the tile's first segment
   int32_t cta0;                    // first range that holds a step of it
   int32_t nseg;                    // ranges that do
-  int32_t keys;                    // 1: one half of rows, the halves take alternate blocks
+  int32_t keys;                    // 0: two halves; else one half, the groups take alternate blocks, and its rows
+                                   // stand this often in the MMA's (see copies_of)
   int32_t pad;
 };
 
@@ -127,6 +128,15 @@ HPtrs shared_ptrs(const HLayout& L, void* ws) {
   x.part_o = reinterpret_cast<float*>(b + L.part_o);
   x.part_lse = reinterpret_cast<float*>(b + L.part_lse);
   return x;
+}
+
+// How often a one-half tile's q rows stand in its 128 MMA rows: few rows (of
+// few tokens, whose q is loaded token by token) stand there four times or
+// twice, 32 or 64 rows apart, and each copy's warps take a quarter or half of
+// every block's keys.
+constexpr int kHSmallQ = 8;
+__device__ __forceinline__ int copies_of(int ntok, int G) {
+  return ntok > kHSmallQ || ntok * G > 64 ? 1 : (ntok * G > 32 ? 2 : 4);
 }
 
 // First partial row of the part of tile t that range c holds.  A range begins
@@ -375,7 +385,7 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     t.nblk = nblk;
     t.cost0 = run + kHCostTile;
     t.part0 = part;
-    t.keys = ntok <= a.T;
+    t.keys = ntok <= a.T ? copies_of(ntok, a.G) : 0;
     t.pad = 0;
     t.nseg = t.cta0 = 0;
     if (nblk) {
@@ -458,7 +468,6 @@ constexpr uint32_t kHOffCtrl = kHOffKV + kHStages * kHTileBytes;
 // registers of a softmax thread and of the others: 256 x 216 + 128 x 72 is
 // the launch's 384 x 168
 constexpr int kHSoftmaxRegs = 216, kHOtherRegs = 72;
-constexpr int kHSmallQ = 4;              // halves of at most this many tokens load their q token by token
 
 // A role may pass over places and q slots of the other group without looking
 // at their barriers.  A parity only tells a phase from the one before, so a
@@ -623,6 +632,137 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
+// O of the thread's row times f, 16 columns at a time: the caller's scores
+// keep their registers
+__device__ __forceinline__ void scale_o(uint32_t tO, float f) {
+#pragma unroll
+  for (int cb = 0; cb < 8; ++cb) {
+    uint32_t w[16];
+    tmem_ld16(tO + cb * 16, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
+    tmem_st16(tO + cb * 16, w);
+  }
+}
+
+// One block of a tile whose rows stand 128 / kKeys times in the MMA's: copy
+// `copy` takes the keys kKeys x copy .. of the block, with a maximum and a sum
+// of its own, and writes zeros as the other keys' weights.  A decode tile's
+// 8 rows then cost a quarter of the time of one warp with 128 keys to a
+// thread.
+template <int kKeys, bool kBf16>
+__device__ __forceinline__ void few_rows(uint32_t tS, int copy, int k0, int lo, int hi, int warp_hi, bool live,
+                                         bool mine, float scale_log2, float* m, float* l) {
+  float sv[kKeys];
+#pragma unroll
+  for (int q = 0; q < kKeys / 32; ++q) tmem_ld32(tS + copy * kKeys + q * 32, sv + q * 32);
+  tmem_ld_wait();
+  const int first = k0 + copy * kKeys;
+  if (first < lo || first + kKeys > warp_hi) {
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) sv[k] = first + k >= lo && first + k < hi ? sv[k] : -INFINITY;
+  }
+  float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kKeys; k += 4) {
+    b0 = hmax3(b0, sv[k], sv[k + 1]);
+    b1 = hmax3(b1, sv[k + 2], sv[k + 3]);
+  }
+  const float bm = fmaxf(b0, b1) * scale_log2;
+  const bool raise = live && (bm > *m + kHRescale || (*m == -INFINITY && bm > -INFINITY));
+  if (__any_sync(0xffffffffu, raise)) {
+    const float f = raise ? (*m == -INFINITY ? 0.f : ex2_approx(*m - bm)) : 1.f;
+    if (mine) scale_o(tS + 128, f);
+    if (raise) {
+      *l *= f;
+      *m = bm;
+    }
+  }
+  const float mm = *m == -INFINITY ? 0.f : *m;
+  const uint64_t scale2 = pack_f2(scale_log2, scale_log2), off2 = pack_f2(-mm, -mm);
+  uint64_t l0 = pack_f2(0.f, 0.f);
+#pragma unroll
+  for (int q = 0; q < kKeys / 32; ++q) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 x = unpack_f2(fma_f2(pack_f2(sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]), scale2, off2));
+      const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+      l0 = add_f2(l0, pack_f2(p0, p1));
+      pk[k] = hpack2<kBf16>(p0, p1);
+    }
+    tmem_st16(tS + (copy * kKeys + q * 32) / 2, pk);
+  }
+  const uint32_t none[16] = {};
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (q / (kKeys / 32) != copy) tmem_st16(tS + 16 * q, none);
+  const float2 ls = unpack_f2(l0);
+  *l += ls.x + ls.y;
+}
+
+// barrier of one softmax group's 128 threads
+__device__ __forceinline__ void group_sync(int h) { asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory"); }
+
+// The partial rows of a tile with copies: the copies' sums join over shared
+// memory (32 KB at `mem`, the stage of the group's last V), 64 columns at a
+// time, 16-byte pieces of a row at places that change with the row.
+__device__ __forceinline__ void join_copies(uint32_t mem, uint32_t tO, int h, int r, int row, int copy, int copies,
+                                            int rows, bool live, float m, float l, float* part_o, float* part_lse) {
+  const int apart = 128 / copies;
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(mem + r * 8), "f"(m), "f"(l) : "memory");
+  group_sync(h);
+  float mq[4], lq[4], M = -INFINITY, L = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    mq[q] = -INFINITY;
+    lq[q] = 0.f;
+    if (q < copies) {
+      const uint2 v = ld_shared_v2(mem + (q * apart + row) * 8);
+      mq[q] = __uint_as_float(v.x);
+      lq[q] = __uint_as_float(v.y);
+    }
+    M = fmaxf(M, mq[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) L += lq[q] * (M == -INFINITY ? 1.f : ex2_approx(mq[q] - M));  // (a NaN stays one)
+  const float f = L == 0.f ? 0.f : (M == -INFINITY ? 1.f : ex2_approx(m - M)) / L;
+  if (live && copy == 0) part_lse[row] = L == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) + lg2_approx(L);
+  group_sync(h);
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+    for (int cb = 0; cb < 2; ++cb) {
+      float ov[32];
+      tmem_ld32(tO + pass * 64 + cb * 32, ov);  // every lane: the load is warp-collective
+      tmem_ld_wait();
+      if (live)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          st_shared_v4(mem + r * 256 + (((cb * 8 + k) ^ (r & 15)) << 4), __float_as_uint(ov[4 * k] * f),
+                       __float_as_uint(ov[4 * k + 1] * f), __float_as_uint(ov[4 * k + 2] * f),
+                       __float_as_uint(ov[4 * k + 3] * f));
+    }
+    group_sync(h);
+    for (int x = r; x < rows * 16; x += 128) {
+      const int rr = x >> 4, c4 = x & 15;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < copies; ++q) {
+        const int at = q * apart + rr;
+        const uint4 v = ld_shared_v4(mem + at * 256 + ((c4 ^ (at & 15)) << 4));
+        sum.x += __uint_as_float(v.x);
+        sum.y += __uint_as_float(v.y);
+        sum.z += __uint_as_float(v.z);
+        sum.w += __uint_as_float(v.w);
+      }
+      *reinterpret_cast<float4*>(part_o + rr * 128 + pass * 64 + c4 * 4) = sum;
+    }
+    fence_proxy_async_smem();  // the stage's next copy comes after what was done here
+    group_sync(h);
+  }
+}
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kHThreads, 1)
     k_shared(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmq1,
@@ -694,24 +834,26 @@ __global__ void __launch_bounds__(kHThreads, 1)
           ok = hwarp_all(
               mbar_wait(&c.q_empty[b], ((qn >> 1) & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
           if (!ok) break;
-          if (lane == 0) {
-            uint8_t* qd = sm + b * kHTileBytes;
-            uint64_t* full = &c.q_full[qn & 3];
-            const int t0 = s.t.tok0 + h * a.T, nt = min(a.T, s.t.ntok - h * a.T);
-            if (nt > kHSmallQ) {  // one box; rows past the tile's tokens are never used
+          uint8_t* qd = sm + b * kHTileBytes;
+          uint64_t* full = &c.q_full[qn & 3];
+          const int t0 = s.t.tok0 + h * a.T, nt = min(a.T, s.t.ntok - h * a.T);
+          if (nt > kHSmallQ) {  // one box; rows past the tile's tokens are never used
+            if (lane == 0) {
               mbar_arrive_expect_tx(full, (uint32_t)(G * a.T) * 256u);
               tma_load_3d(qd, &tmq, full, 0, s.t.g * G, t0);
               tma_load_3d(qd + 16384, &tmq, full, 64, s.t.g * G, t0);
-            } else {
-              mbar_arrive_expect_tx(full, (uint32_t)(G * nt) * 256u);
-              for (int x = 0; x < nt; ++x) {
-                tma_load_3d(qd + x * G * 128, &tmq1, full, 0, s.t.g * G, t0 + x);
-                tma_load_3d(qd + 16384 + x * G * 128, &tmq1, full, 64, s.t.g * G, t0 + x);
-              }
+            }
+          } else {  // token by token, each copy of the rows
+            const int copies = max(s.t.keys, 1), apart = 128 / copies;
+            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(G * nt * copies) * 256u);
+            __syncwarp();
+            for (int x = lane; x < nt * copies * 2; x += 32) {
+              const int col = x & 1, cp = (x >> 1) % copies, tk = (x >> 1) / copies;
+              tma_load_3d(qd + col * 16384 + (cp * apart + tk * G) * 128, &tmq1, full, col * 64, s.t.g * G, t0 + tk);
             }
           }
         }
-        // block i's pages come from a window of 32 blocks that the lanes hold;
+      // block i's pages come from a window of 32 blocks that the lanes hold;
       // the next window is loaded while this one is used
       const int32_t* row = a.block_tables + (size_t)s.t.row * a.max_pages;
       auto pages_at = [&](int i, int pg) -> int {  // lane's page pg of block i + lane, -1: none or not needed
@@ -787,7 +929,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
       int np = 0, no = 0;           // products P V issued, tiles finished
       int nt = 0;                   // turns taken
       int owed = -1, bits = 0;      // ring place of the V that the next P V takes; bit 0: first of its tile, 1: last,
-                                    // 2: no other group reads V
+                                    // 2: no other group reads V, 3: the softmax frees V
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) {
         ok = ok && hwarp_all(mbar_wait(bar, parity, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
@@ -808,8 +950,10 @@ __global__ void __launch_bounds__(kHThreads, 1)
       };
       auto rest_pv = [&](uint32_t tS, uint32_t dv, uint64_t* empty) {
         mma_pv_hi(tS + 128, tS, dv, id_pv);
-        mma_commit(empty);
-        if (bits & 4) mma_commit(empty);
+        if (!(bits & 8)) {
+          mma_commit(empty);
+          if (bits & 4) mma_commit(empty);
+        }
         if (bits & 2) mma_commit(&c.o_full[h]);
       };
       auto done_pv = [&] {
@@ -875,7 +1019,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
           __syncwarp();
           if (owed >= 0) done_pv();
           owed = at + place_v(i, n);
-          bits = (i == half ? 1 : 0) | (last ? 2 : 0) | (keys ? 4 : 0);
+          bits = (i == half ? 1 : 0) | (last ? 2 : 0) | (keys ? 4 : 0) | (last && keys > 1 ? 8 : 0);
         }
         if (half >= n && ok) {  // no block of this tile is the group's: nothing else would free what it owes
           if (owed >= 0) {
@@ -919,7 +1063,6 @@ __global__ void __launch_bounds__(kHThreads, 1)
     const int r = tid & 127;  // row of the half == TMEM lane
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + h * 256 + lane_addr, tO = tS + 128;
-    const int rt = r / G;
     int at = 0, qn = 0, n_s = 0, n_o = 0;
     bool ok = true;
     HTile next = range.x <= range.y ? load_tile(a.ws.tiles + range.x) : HTile{};
@@ -934,10 +1077,14 @@ __global__ void __launch_bounds__(kHThreads, 1)
       // buffer, so that short tiles keep both groups busy
       const int half = keys ? h ^ (qn & 1) : 0;
       if (n > 0) qn += keys ? 1 : 2;
-      const int tt = rt + (keys ? 0 : h * a.T);  // the row's token within the tile
+      // the thread's row of the tile's (copies of a one-half tile's rows stand
+      // `apart` rows apart) and its token within the tile
+      const int apart = keys > 1 ? 128 / keys : 128;
+      const int row = r & (apart - 1), copy = r / apart;
+      const int rt = row / G, tt = rt + (keys ? 0 : h * a.T);
       const bool live = rt < a.T && tt < s.t.ntok;
       const long long rows = (long long)s.t.ntok * G;
-      const long long pr = part_row(s.t, cta, cuts) + half * rows + tt * G + (r - rt * G);
+      const long long base = part_row(s.t, cta, cuts) + half * rows, pr = base + tt * G + (row - rt * G);
       const bool warp_live = __any_sync(0xffffffffu, live);
       int hi = key_end;  // the row sees the keys [lo, hi), all of the warp's rows [lo, warp_hi)
       if (n > 0 && a.causal && live) hi = min(hi, a.ws.tok[s.t.tok0 + tt].keys);
@@ -964,7 +1111,17 @@ __global__ void __launch_bounds__(kHThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        if (warp_live) {
+        if (keys > 1) {
+          tc_fence_after();
+          if (keys == 4)
+            few_rows<32, kBf16>(tS, copy, k0, lo, hi, warp_hi, live, mine, a.scale_log2, &m, &l);
+          else
+            few_rows<64, kBf16>(tS, copy, k0, lo, hi, warp_hi, live, mine, a.scale_log2, &m, &l);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.p_half[h]);
+        } else if (warp_live) {
           tc_fence_after();
           float sv[128];
 #pragma unroll
@@ -990,15 +1147,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
             if (mine) {
               // O holds the segment's blocks so far and is complete: S's
               // barrier follows every product issued before
-#pragma unroll
-              for (int cb = 0; cb < 8; ++cb) {  // 16 columns at a time: the scores keep their registers
-                uint32_t w[16];
-                tmem_ld16(tO + cb * 16, w);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
-                tmem_st16(tO + cb * 16, w);
-              }
+              scale_o(tO, f);
             }
             if (raise) {
               l *= f;
@@ -1046,7 +1195,16 @@ __global__ void __launch_bounds__(kHThreads, 1)
       ok = hwarp_all(mbar_wait(&c.o_full[h], n_o & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
       if (!ok) break;
       ++n_o;
-      if (warp_live) {
+      if (keys > 1) {
+        tc_fence_after();
+        const int pl = at - 2 * n + place_v(((n - 1 - half) & ~1) + half, n), st = pl % kHStages;  // its last block's V
+        join_copies(sbase + kHOffKV + st * kHTileBytes, tO, h, r, row, copy, keys, (int)rows, live, m, l,
+                    a.ws.part_o + base * 128, a.ws.part_lse + base);
+        if (r == 0) {
+          mbar_arrive(&c.kv_empty[st]);
+          mbar_arrive(&c.kv_empty[st]);
+        }
+      } else if (warp_live) {
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN stays one)
         float* po = a.ws.part_o + pr * 128;

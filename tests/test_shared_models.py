@@ -182,7 +182,7 @@ def test_ring_places_are_the_producers_order(n):
 
 
 def run_protocol(segs, seed):
-    """segs: (blocks, keys, edge) of the CTA's segments; edge: the groups wait for V to clear rows of it."""
+    """segs: (blocks, keys, edge) of the CTA's segments; keys: 0 two halves, 1 one half, 4 one half with copies; edge: the groups wait for V to clear rows of it."""
     rnd = random.Random(seed)
     B, pending = {}, {}
 
@@ -270,8 +270,11 @@ def run_protocol(segs, seed):
                 S[h] = ("used",)
                 O[h] = "done" if last else "acc"
                 reads[pl] -= 1
-                for _x in range(2 if alone else 1):
-                    B[f"kv_empty{pl % STAGES}"].arrive()
+                if not (alone > 1 and last):  # (with copies the softmax frees the tile's last V)
+                    for _x in range(2 if alone else 1):
+                        B[f"kv_empty{pl % STAGES}"].arrive()
+                else:
+                    reads[pl] += 1
                 if last:
                     B[f"o_full{h}"].arrive()
             later(f"mma{h}", done)
@@ -356,6 +359,13 @@ def run_protocol(segs, seed):
                 no += 1
                 assert O[h] == "done"
                 O[h] = "read"
+                if keys > 1:  # the copies joined in the last V's stage
+                    yield None
+                    pl = at - 2 * n + place_v(((n - 1 - half) & ~1) + half, n)
+                    assert stage[pl % STAGES] == pl
+                    reads[pl] -= 1
+                    for _x in range(2):
+                        B[f"kv_empty{pl % STAGES}"].arrive()
                 B[f"o_empty{h}"].arrive()
                 finished[h] += 1
 
@@ -389,6 +399,6 @@ def run_protocol(segs, seed):
 def test_forward_protocol(seed):
     r = random.Random(seed)
     for x in range(8):
-        segs = [(r.choice([1, 1, 2, 3, r.randint(1, 9)]), r.random() < 0.6, r.random() < 0.5)
+        segs = [(r.choice([1, 1, 2, 3, r.randint(1, 9)]), r.choice([0, 0, 1, 4, 4]), r.random() < 0.5)
                 for _ in range(r.randint(1, 7))]
         run_protocol(segs, seed * 100 + x)
