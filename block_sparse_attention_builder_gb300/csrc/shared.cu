@@ -9,15 +9,21 @@
 // the keys [P, L) of a sequence for its own tokens.  Per kv head a job's
 // tokens fall into *row tiles* of up to 2T tokens (T = 128 / G; two halves
 // of up to 128 (token, head) rows) and its 128-key blocks into chunks; a
-// *tile* is one chunk of one row tile.  Tiles are numbered row tile fastest,
-// then chunk, so the CTAs that run at the same time read the same keys and
-// meet in L2.  The tiles' blocks form one line of steps with a cost each,
-// and the line is cut into one equal range per CTA: a tile cut by a range's
-// end becomes two *segments*.  A chunk is about one range long, so the
-// number of pieces a row falls into stays near the number of CTAs that its
-// keys are worth, and the partial buffer is bounded by the shapes alone.
+// *tile* is one chunk of one row tile.  Every tile writes partial rows of its
+// own, so it does not matter which CTA takes it, nor when.
 //
-// Three launches: k_shared_plan (one CTA: jobs, tiles, ranges), k_shared
+// Tiles of two halves are bound by the tensor pipe and the softmax, tiles of
+// one half (decoding sequences' own keys) by memory.  They stand in two
+// queues; each CTA takes from the one until it is empty, then from the
+// other, and as many CTAs begin with each as it has of the work, so that
+// both kinds run at the same time and the CTAs end together.  (Equal shares
+// of the work fixed beforehand, tiles cut where a share ended: the slowest
+// CTAs took 540 us where the median took 490 us.)  A queue's tiles are in row
+// tile order within a chunk, so the CTAs that run at the same time read the
+// same keys and meet in L2.  A chunk is a quarter of a CTA's share of all
+// work, which bounds the partial buffer by the shapes alone.
+//
+// Three launches: k_shared_plan (one CTA: jobs, tiles, queues), k_shared
 // (persistent, one CTA per SM) and k_shared_join.
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -36,59 +42,69 @@ namespace mxsa {
 namespace {
 
 constexpr int kHMaxSeqs = 1024;
-constexpr int kHMaxCtas = 160;     // ranges; workspaces are sized for this many
+constexpr int kHMaxCtas = 160;     // workspaces are sized for this many
 // Costs, in units of about 0.2 us: one block of a tile of two halves, of one
 // half (whose halves then split the blocks), and a tile's own (its q, the
-// first block's latency, the epilogue).  From the times of CTAs with one
-// kind of work each, all kinds running at once (256 sequences over 65536
-// common keys): 1.5 us, 0.9 us and 1.9 us.
-constexpr int kHCostRows = 8, kHCostKeys = 5, kHCostTile = 10;
+// first block's latency, the epilogue).  They set the chunks and how many
+// CTAs begin with which queue.
+constexpr int kHCostRows = 8, kHCostKeys = 4, kHCostTile = 10;
 constexpr int kHCostRatio = (kHCostRows + kHCostKeys - 1) / kHCostKeys;
+// A CTA's share of all work is kHPerCta chunks; the end of a long column (four
+// chunks and more) is cut kHSmall times as fine, and these small tiles come
+// last in their queue.  A share of at most kHOneChunk blocks is one chunk.
+constexpr int kHPerCta = 2, kHSmall = 4, kHOneChunk = 24;
 
 // One tile: keys [128 blk0, 128 (blk0 + nblk)) of [lo, hi) for ntok tokens.
 struct alignas(16) HTile {
   int32_t tok0, ntok, g, row;      // first token, tokens, kv head, block table row
   int32_t lo, hi, blk0, nblk;
-  long long cost0;                 // cost before its first step
-  long long part0;                 // partial row of the tile's first segment
-  int32_t cta0;                    // first range that holds a step of it
-  int32_t nseg;                    // ranges that do
+  long long part0;                 // first partial row
   int32_t keys;                    // 0: two halves; else one half, the groups take alternate blocks, and its rows
                                    // stand this often in the MMA's (see copies_of)
   int32_t pad;
+};
+
+// What the join needs of a tile: its rows' partials and how many of each (two
+// where the groups took alternate blocks, the second `ntok` tokens on).
+struct alignas(16) HPieces {
+  int32_t part0, tok0, ntok, pieces;
 };
 
 struct HJob {
   int32_t tok0, ntok, row, lo, hi;
   int32_t tile0;                   // first tile
   int32_t nch, chunk, nrt;         // chunks, blocks of one, row tiles
+  int32_t nfull, small;            // chunks of `chunk` blocks, and the blocks of the others
 };
 
 // A token: its sequence (-1: none), the keys it sees, and the tiles of its
 // sequence's own keys and of its group's prefix: for kv head g and chunk c <
-// nch, tile base + (g * nch + c) * nrt.
+// nch, number base + (g * nch + c) * nrt.
 struct alignas(16) HTok {
   int32_t seq, keys, own_base, own_nch;
   int32_t own_nrt, pre_base, pre_nch, pre_nrt;
 };
 
+// The queues: 0 tiles of two halves, 1 of one half.
 struct HHeader {
-  long long share;                 // cost of one range
-  long long cuts;                  // partial row of range 0's cut (see part_row)
-  int2 range[kHMaxCtas];           // first and last tile of each CTA's range (first > last: none)
+  int32_t count[2];                // tiles
+  int32_t next[2];                 // places taken; the first `ctas` of a queue go to the CTAs that begin with it
+  int32_t ctas[2];
 };
 
 struct HPtrs {
   HHeader* hdr;
   HTok* tok;                       // [total_q]
-  HTile* tiles;
+  HPieces* pieces;                 // by tile number
+  HTile* queue[2];
   float* part_o;
   float* part_lse;                 // log2 units
 };
 
 struct HLayout {
-  size_t hdr, tok, tiles, part_o, part_lse, total;
+  size_t hdr, tok, pieces, queue, part_o, part_lse, total;
   long long tile_cap, row_cap;
+  int join_cap;  // partials of one row
 };
 
 HLayout shared_layout(const mxsa_problem& p) {
@@ -96,14 +112,21 @@ HLayout shared_layout(const mxsa_problem& p) {
   // (job, kv head, row tile) triples: each token lies in at most two jobs, a
   // job's last row tile may be short, and there are at most B + B / 2 jobs
   const long long triples = p.num_kv_heads * (2 * (p.total_q / (2 * T)) + 2LL * p.num_seqs);
-  // chunks beyond the first: at most the CTAs' ranges, kHCostRatio times as
-  // many where a tile of one half takes its job's chunk of two
-  const long long extra = kHCostRatio * kHMaxCtas;
+  // Chunks beyond the first.  A job's chunk is at least 1 / kHPerCta of a
+  // CTA's share of the whole cost, in blocks of two halves' cost where the
+  // job has such tiles; a tile of one half then costs kHCostRatio less.  With
+  // small tiles a column of x >= 4 chunks has at most x + 2 kHSmall - 1, without
+  // x + 1/2.  And no more than there are blocks.  A kv head has its share.
+  const long long blocks = max_blocks_per_seq(p);
+  const long long by_cost = (long long)kHPerCta * kHCostRatio * kHMaxCtas * (4 + 2 * kHSmall - 1) / 4;
+  const long long extra = std::min(by_cost, triples * (blocks - 1));
   HLayout L;
   L.tile_cap = triples + extra;
-  // a row and its twin (halves that split the blocks) in two jobs, and the
-  // cuts, each of at most 256 rows
-  L.row_cap = 4LL * p.total_q * p.num_q_heads + 256LL * (extra + kHMaxCtas);
+  // A row and its twin (halves that split the blocks) in two jobs; a further
+  // chunk's tile has at most 256 rows, twins counted.
+  const long long rows = (long long)p.total_q * G;
+  L.row_cap = 4LL * p.total_q * p.num_q_heads + std::min(256LL, 2 * rows) * extra;
+  L.join_cap = (int)(2 * std::min(2 + by_cost / p.num_kv_heads, 2 * blocks + 2));
   size_t o = 0;
   auto take = [&o](size_t n) {
     const size_t at = o;
@@ -112,7 +135,8 @@ HLayout shared_layout(const mxsa_problem& p) {
   };
   L.hdr = take(sizeof(HHeader));
   L.tok = take(sizeof(HTok) * (size_t)p.total_q);
-  L.tiles = take(sizeof(HTile) * L.tile_cap);
+  L.pieces = take(sizeof(HPieces) * L.tile_cap);
+  L.queue = take(2 * sizeof(HTile) * L.tile_cap);
   L.part_o = take(512ull * L.row_cap);
   L.part_lse = take(4ull * L.row_cap);
   L.total = o;
@@ -124,7 +148,9 @@ HPtrs shared_ptrs(const HLayout& L, void* ws) {
   HPtrs x;
   x.hdr = reinterpret_cast<HHeader*>(b + L.hdr);
   x.tok = reinterpret_cast<HTok*>(b + L.tok);
-  x.tiles = reinterpret_cast<HTile*>(b + L.tiles);
+  x.pieces = reinterpret_cast<HPieces*>(b + L.pieces);
+  x.queue[0] = reinterpret_cast<HTile*>(b + L.queue);
+  x.queue[1] = x.queue[0] + L.tile_cap;
   x.part_o = reinterpret_cast<float*>(b + L.part_o);
   x.part_lse = reinterpret_cast<float*>(b + L.part_lse);
   return x;
@@ -137,14 +163,6 @@ HPtrs shared_ptrs(const HLayout& L, void* ws) {
 constexpr int kHSmallQ = 8;
 __device__ __forceinline__ int copies_of(int ntok, int G) {
   return ntok > kHSmallQ || ntok * G > 64 ? 1 : (ntok * G > 32 ? 2 : 4);
-}
-
-// First partial row of the part of tile t that range c holds.  A range begins
-// with at most one tile that an earlier range began, so the cuts' rows lie at
-// a fixed distance, behind those of the tiles' first segments.
-constexpr int kHCutRows = 256;
-__device__ __forceinline__ long long part_row(const HTile& t, int c, long long cuts) {
-  return c == t.cta0 ? t.part0 : cuts + (long long)c * kHCutRows;
 }
 
 __device__ __forceinline__ long long ceil_div(long long x, int y) {
@@ -173,8 +191,7 @@ struct HPlanSmem {
   int32_t gp[kHMaxSeqs + 1], want[kHMaxSeqs], shortest[kHMaxSeqs];
   int32_t tile0[2 * kHMaxSeqs];
   HJob job[2 * kHMaxSeqs];
-  long long scan[4][kHPlanThreads / 32];
-  int32_t first[kHMaxCtas + 1];
+  long long scan[6][kHPlanThreads / 32];
 };
 
 // exclusive sum over the block; *total gets the whole.  `s`: one word per
@@ -245,13 +262,11 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
       s.shortest[i] = a.max_len;
     }
   }
-  for (int i = tid; i <= a.ctas; i += kHPlanThreads) s.first[i] = -1;
   const bool cu_ok = !__syncthreads_or(bad & MXSA_FLAG_CU), gp_ok = !__syncthreads_or(bad & MXSA_FLAG_GROUP);
   if (bad && a.flags) atomicOr(a.flags, bad);
   if (!cu_ok) {  // no sequence has tokens: no tile, no row
     for (int t = tid; t < a.total_q; t += kHPlanThreads) a.ws.tok[t] = HTok{-1, 0, 0, 0, 0, 0, 0, 0};
-    for (int c = tid; c < a.ctas; c += kHPlanThreads) a.ws.hdr->range[c] = make_int2(0, -1);
-    if (tid == 0) a.ws.hdr->share = 1, a.ws.hdr->cuts = 0;
+    if (tid == 0) *a.ws.hdr = HHeader{{0, 0}, {0, 0}, {a.ctas, 0}};
     return;
   }
   // a group's prefix is at most its shortest sequence with tokens
@@ -272,7 +287,7 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
   const int njobs = B + NG, T2 = 2 * a.T;
   const int jper = (njobs + kHPlanThreads - 1) / kHPlanThreads;
   const int q0 = min(njobs, tid * jper), q1 = min(njobs, q0 + jper);
-  long long cost = 0, total = 0;
+  long long cost[2] = {0, 0}, total[2];  // of the two kinds of tiles
   for (int q = q0; q < q1; ++q) {
     HJob j;
     if (q < B) {
@@ -296,23 +311,35 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     j.chunk = j.nrt > keys;  // for now: whether tiles of two halves set the chunk
     j.nch = nb;
     // (as far as it is known without causal trimming)
-    if (nb > 0)
-      cost += (long long)a.Hkv *
-              ((j.nrt - keys) * (nb * kHCostRows + kHCostTile) + keys * (nb * kHCostKeys + kHCostTile));
+    if (nb > 0) {
+      cost[0] += (long long)a.Hkv * (j.nrt - keys) * (nb * kHCostRows + kHCostTile);
+      cost[1] += (long long)a.Hkv * keys * (nb * kHCostKeys + kHCostTile);
+    }
     s.job[q] = j;
   }
-  block_scan(cost, s.scan[0], &total);
-  const long long goal = max(ceil_div(total, a.ctas), 1LL);
+  block_scan(cost[0], s.scan[0], &total[0]);
+  block_scan(cost[1], s.scan[1], &total[1]);
+  const long long share = max(ceil_div(total[0] + total[1], a.ctas), 1LL);
   long long mine = 0, all = 0;
   for (int q = q0; q < q1; ++q) {
     HJob& j = s.job[q];
     const int nb = j.nch;
-    const long long chunk = j.chunk ? (goal + kHCostRows - 1) / kHCostRows : (goal + kHCostKeys - 1) / kHCostKeys;
-    j.chunk = (int)min(chunk, (long long)max(nb, 1));
-    j.nch = (nb + j.chunk - 1) / j.chunk;
+    const int w = j.chunk ? kHCostRows : kHCostKeys;
+    const long long whole = (share + w - 1) / w;
+    const int want = (int)min(whole <= kHOneChunk ? whole : (whole + kHPerCta - 1) / kHPerCta, (long long)max(nb, 1));
+    if (whole <= kHOneChunk || nb < 4 * want) {  // chunks of one size, the nearest number of them
+      j.nfull = j.nch = nb > 0 ? max((nb + want / 2) / want, 1) : 0;
+      j.chunk = nb > 0 ? (nb + j.nch - 1) / j.nch : 1;
+      j.small = 1;
+    } else {
+      j.chunk = want;
+      j.nfull = nb / want - 1;
+      j.small = (want + kHSmall - 1) / kHSmall;
+      j.nch = j.nfull + (nb - j.nfull * want + j.small - 1) / j.small;
+    }
     mine += (long long)a.Hkv * j.nch * j.nrt;
   }
-  long long at = block_scan(mine, s.scan[1], &all);
+  long long at = block_scan(mine, s.scan[2], &all);
   for (int q = q0; q < q1; ++q) {
     HJob& j = s.job[q];
     j.tile0 = (int)at;
@@ -344,36 +371,39 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     do ++c->q;
     while (c->q < njobs && s.job[c->q].nrt == 0);
   };
-  // blocks, tokens and cost of the tile at c
-  auto size_of = [&](const HCursor& c, int* blk0, int* nblk, int* ntok) -> long long {
+  // blocks and tokens of the tile at c
+  auto size_of = [&](const HCursor& c, int* blk0, int* nblk, int* ntok) {
     const HJob& j = s.job[c.q];
     *ntok = min(T2, j.ntok - c.rt * T2);
     int end = (j.hi + 127) >> 7;
     if (a.causal && c.q < B)  // keys past the last token's position are nobody's
       end = min(end, (max(j.hi - j.ntok + c.rt * T2 + *ntok, 0) + 127) >> 7);
-    *blk0 = (j.lo >> 7) + c.ch * j.chunk;
-    *nblk = max(min(*blk0 + j.chunk, end) - *blk0, 0);
-    return *nblk ? (long long)*nblk * (*ntok <= a.T ? kHCostKeys : kHCostRows) + kHCostTile : 0LL;
+    const int fine = max(c.ch - j.nfull, 0);
+    *blk0 = (j.lo >> 7) + (c.ch - fine) * j.chunk + fine * j.small;
+    *nblk = max(min(*blk0 + (c.ch < j.nfull ? j.chunk : j.small), end) - *blk0, 0);
   };
-  cost = 0;
-  long long rows = 0;
+  // tiles of each queue (in one word; full and small ones) and partial rows
+  // before the thread's own
+  long long full = 0, small = 0, rows = 0;
   int blk0, nblk, ntok;
   HCursor c = c0;
   for (int i = i0; i < i1; ++i, advance(&c)) {
-    cost += size_of(c, &blk0, &nblk, &ntok);
-    rows += nblk ? ntok * a.G * (ntok <= a.T ? 2 : 1) : 0;
+    size_of(c, &blk0, &nblk, &ntok);
+    const bool keys = ntok <= a.T;
+    if (nblk) {
+      (c.ch < s.job[c.q].nfull ? full : small) += keys ? 1LL << 32 : 1LL;
+      rows += ntok * a.G * (keys ? 2 : 1);
+    }
   }
-  long long run, part;
-  long long all_rows;
-  run = block_scan(cost, s.scan[2], &total);
-  part = block_scan(rows, s.scan[3], &all_rows);
-  const long long share = max(ceil_div(total, a.ctas), (long long)kHCostRows);
-  int rg = (int)(total < INT_MAX ? (uint32_t)run / (uint32_t)share : run / share);  // the range that holds `run`
-  long long rg_end = (rg + 1) * share;
+  long long all_full, all_small, all_rows;
+  full = block_scan(full, s.scan[3], &all_full);
+  small = block_scan(small, s.scan[4], &all_small) + all_full;  // (behind the queue's full ones)
+  long long part = block_scan(rows, s.scan[5], &all_rows);
   c = c0;
   for (int i = i0; i < i1; ++i, advance(&c)) {
-    const long long x = size_of(c, &blk0, &nblk, &ntok);
+    size_of(c, &blk0, &nblk, &ntok);
     const HJob& j = s.job[c.q];
+    const bool keys = ntok <= a.T;
     HTile t;
     t.tok0 = j.tok0 + c.rt * T2;
     t.ntok = ntok;
@@ -383,31 +413,16 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     t.hi = j.hi;
     t.blk0 = blk0;
     t.nblk = nblk;
-    t.cost0 = run + kHCostTile;
     t.part0 = part;
-    t.keys = ntok <= a.T ? copies_of(ntok, a.G) : 0;
+    t.keys = keys ? copies_of(ntok, a.G) : 0;
     t.pad = 0;
-    t.nseg = t.cta0 = 0;
+    a.ws.pieces[i] = HPieces{(int)part, t.tok0, ntok, keys ? min(nblk, 2) : min(nblk, 1)};  // (rows fit 32 bits)
     if (nblk) {
-      // The ranges that hold the start of one of its steps.  (share is at
-      // least a step's cost, so each range between the first and the last
-      // holds one.)  The first tile to touch a range opens it.
-      const long long last = run + x - (t.keys ? kHCostKeys : kHCostRows);
-      if (run == rg_end - share) s.first[rg] = i;
-      int r = rg;
-      long long end = rg_end;
-      for (; t.cost0 >= end; end += share) s.first[++r] = i;
-      t.cta0 = r;
-      for (; last >= end; end += share) s.first[++r] = i;
-      t.nseg = r - t.cta0 + 1;
-      for (; run + x > end; end += share) s.first[++r] = i;
-      if (run + x == end) ++r, end += share;
-      rg = r;
-      rg_end = end;
-      part += ntok * a.G * (t.keys ? 2 : 1);
-      run += x;
+      part += ntok * a.G * (keys ? 2 : 1);
+      long long& place = c.ch < j.nfull ? full : small;
+      a.ws.queue[keys][keys ? place >> 32 : (int)place] = t;
+      place += keys ? 1LL << 32 : 1LL;
     }
-    a.ws.tiles[i] = t;
   }
   for (int i = tid; i < a.total_q; i += kHPlanThreads) {
     HTok v{-1, 0, 0, 0, 0, 0, 0, 0};
@@ -430,14 +445,13 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     }
     a.ws.tok[i] = v;
   }
-  __syncthreads();
-  // (a range's last tile may hold none of its steps: it is skipped there)
-  for (int k = tid; k < a.ctas; k += kHPlanThreads)
-    a.ws.hdr->range[k] = make_int2(s.first[k] < 0 ? 0 : s.first[k],
-                                   s.first[k] < 0 ? -1 : (s.first[k + 1] < 0 ? ntiles - 1 : s.first[k + 1]));
   if (tid == 0) {
-    a.ws.hdr->share = share;
-    a.ws.hdr->cuts = all_rows;
+    const long long all_queued = all_full + all_small;
+    const int n0 = (int)all_queued, n1 = (int)(all_queued >> 32);
+    // (half of the share: the second kind's smaller tiles fill up the end)
+    int with1 = (int)(total[1] * a.ctas / 2 / max(total[0] + total[1], 1LL));
+    with1 = n1 == 0 ? 0 : (n0 == 0 ? a.ctas : min(max(with1, 1), a.ctas - 1));
+    *a.ws.hdr = HHeader{{n0, n1}, {a.ctas - with1, with1}, {a.ctas - with1, with1}};
   }
 }
 
@@ -462,12 +476,13 @@ constexpr int kHThreads = 384;
 constexpr int kHProducer = 8, kHMma = 9;
 constexpr uint32_t kHTileBytes = 32768;  // 128 rows x 128 x 16-bit
 constexpr int kHStages = 5;
+constexpr int kHWork = 4;
 constexpr float kHRescale = 8.f;         // log2 units
 constexpr uint32_t kHOffKV = 2 * kHTileBytes;
 constexpr uint32_t kHOffCtrl = kHOffKV + kHStages * kHTileBytes;
-// registers of a softmax thread and of the others: 256 x 216 + 128 x 72 is
+// registers of a softmax thread and of the others: 256 x 208 + 128 x 88 is
 // the launch's 384 x 168
-constexpr int kHSoftmaxRegs = 216, kHOtherRegs = 72;
+constexpr int kHSoftmaxRegs = 208, kHOtherRegs = 88;
 
 // A role may pass over places and q slots of the other group without looking
 // at their barriers.  A parity only tells a phase from the one before, so a
@@ -477,6 +492,8 @@ constexpr int kHSoftmaxRegs = 216, kHOtherRegs = 72;
 struct HCtrl {
   uint64_t q_full[4], q_empty[2], kv_full[2 * kHStages], kv_empty[kHStages];
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2], turn[2], done;
+  uint64_t work_full[kHWork], work_empty[kHWork];
+  HTile work[kHWork];  // the CTA's tiles, from the producer to the other roles; no blocks: the end
   uint32_t tmem_base;
   int32_t abort_flag, local_flags;
 };
@@ -489,12 +506,6 @@ struct HArgs {
   float scale_log2;
 };
 
-// The part of a tile that range c holds: blocks [b0, b0 + n) of the keys.
-struct HSeg {
-  HTile t;
-  int b0, n;
-};
-
 __device__ __forceinline__ HTile load_tile(const HTile* p) {
   HTile t;
   const int4* s = reinterpret_cast<const int4*>(p);
@@ -504,21 +515,7 @@ __device__ __forceinline__ HTile load_tile(const HTile* p) {
   return t;
 }
 
-// first step of the tile that costs at least `cost` from the line's start
-__device__ __forceinline__ int step_at(const HTile& t, long long cost) {
-  const long long d = cost - t.cost0;
-  if (d <= 0) return 0;
-  const int w = t.keys ? kHCostKeys : kHCostRows;
-  return (int)min((d + w - 1) / w, (long long)t.nblk);
-}
-
-__device__ __forceinline__ void cut(HSeg* s, long long share, int c) {
-  const int i0 = step_at(s->t, c * share), i1 = step_at(s->t, (c + 1) * share);
-  s->b0 = s->t.blk0 + i0;
-  s->n = i1 - i0;
-}
-
-// ring places of a segment's blocks, relative to the segment's first: K0, K1,
+// ring places of a tile's blocks, relative to the tile's first: K0, K1,
 // V0, K2, V1, ..., K(n-1), V(n-2), V(n-1)
 __device__ __forceinline__ int place_k(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int place_v(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
@@ -789,6 +786,10 @@ __global__ void __launch_bounds__(kHThreads, 1)
       mbar_init(&c.kv_full[i + kHStages], 1);
       mbar_init(&c.kv_empty[i], 2);
     }
+    for (int i = 0; i < kHWork; ++i) {
+      mbar_init(&c.work_full[i], 1);
+      mbar_init(&c.work_empty[i], 10);  // the issuers' and the softmax groups' warps
+    }
     mbar_init(&c.done, 2);
     c.abort_flag = 0;
     c.local_flags = 0;
@@ -807,8 +808,19 @@ __global__ void __launch_bounds__(kHThreads, 1)
   const uint32_t sbase = smem_u32(sm);
   const int G = a.G, cta = blockIdx.x;
   pdl_wait();  // the plan
-  const int2 range = a.ws.hdr->range[cta];
-  const long long share = a.ws.hdr->share, cuts = a.ws.hdr->cuts;
+  // The next tile of a role that is not the producer; false at the end (or
+  // when a wait gave up).
+  int taken = 0;
+  auto next_tile = [&](HTile* t) {
+    const int w = taken % kHWork;
+    if (!hwarp_all(mbar_wait(&c.work_full[w], (taken / kHWork) & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs)))
+      return false;
+    *t = c.work[w];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c.work_empty[w]);
+    ++taken;
+    return t->nblk > 0;
+  };
 
   if (warp >= 8) {
     regs_dec<kHOtherRegs>();
@@ -823,67 +835,103 @@ __global__ void __launch_bounds__(kHThreads, 1)
       const int ps = 1 << a.page_shift, npg = ps == 128 ? 1 : 2;
       int at = 0, qn = 0;  // ring places taken so far
       bool ok = true;
-      HSeg s;
-      for (int ti = range.x; ti <= range.y && ok; ++ti) {
-        s.t = load_tile(a.ws.tiles + ti);  // (the ring holds loads for longer than this takes)
-        cut(&s, share, cta);
-        if (s.n <= 0) continue;
-        const int nh = s.t.keys ? 1 : 2;
-        for (int h = 0; h < nh && ok; ++h, ++qn) {
-          const int b = qn & 1;
-          ok = hwarp_all(
-              mbar_wait(&c.q_empty[b], ((qn >> 1) & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
-          if (!ok) break;
-          uint8_t* qd = sm + b * kHTileBytes;
-          uint64_t* full = &c.q_full[qn & 3];
-          const int t0 = s.t.tok0 + h * a.T, nt = min(a.T, s.t.ntok - h * a.T);
-          if (nt > kHSmallQ) {  // one box; rows past the tile's tokens are never used
-            if (lane == 0) {
-              mbar_arrive_expect_tx(full, (uint32_t)(G * a.T) * 256u);
-              tma_load_3d(qd, &tmq, full, 0, s.t.g * G, t0);
-              tma_load_3d(qd + 16384, &tmq, full, 64, s.t.g * G, t0);
-            }
-          } else {  // token by token, each copy of the rows
-            const int copies = max(s.t.keys, 1), apart = 128 / copies;
-            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(G * nt * copies) * 256u);
-            __syncwarp();
-            for (int x = lane; x < nt * copies * 2; x += 32) {
-              const int col = x & 1, cp = (x >> 1) % copies, tk = (x >> 1) / copies;
-              tma_load_3d(qd + col * 16384 + (cp * apart + tk * G) * 128, &tmq1, full, col * 64, s.t.g * G, t0 + tk);
-            }
-          }
+      // The CTA's queue: the second kind's CTAs are spread over the grid.
+      const int with1 = a.ws.hdr->ctas[1], count[2] = {a.ws.hdr->count[0], a.ws.hdr->count[1]};
+      const int before1 = (int)((long long)cta * with1 / gridDim.x);
+      int q = (int)((long long)(cta + 1) * with1 / gridDim.x) - before1;
+      bool other = false, end = false;  // the queue it began with is empty; both are
+      auto resolve = [&](int place) {   // the tile at a place of queue q, or of the other queue
+        place = __shfl_sync(0xffffffffu, place, 0);
+        if (place >= (q ? count[1] : count[0]) && !other) {
+          other = true;
+          q ^= 1;
+          if (lane == 0) place = atomicAdd(&a.ws.hdr->next[q], 1);
+          place = __shfl_sync(0xffffffffu, place, 0);
         }
-      // block i's pages come from a window of 32 blocks that the lanes hold;
-      // the next window is loaded while this one is used
-      const int32_t* row = a.block_tables + (size_t)s.t.row * a.max_pages;
-      auto pages_at = [&](int i, int pg) -> int {  // lane's page pg of block i + lane, -1: none or not needed
-        const int b = s.b0 + i + lane;
+        end = place >= (q ? count[1] : count[0]);
+        return end ? HTile{} : load_tile((q ? a.ws.queue[1] : a.ws.queue[0]) + place);
+      };
+      // block i's pages come from a window of 32 blocks that the lanes hold
+      auto pages_at = [&](const HTile& t, int i, int pg) -> int {  // page pg of block i + lane, -1: none needed
+        const int b = t.blk0 + i + lane;
         const int p0 = b * 128 + pg * 64;  // its first key
-        if (pg >= npg || i + lane >= s.n || p0 >= s.t.hi || p0 + ps <= s.t.lo) return -1;
-        const int phys = row[p0 >> a.page_shift];
+        if (pg >= npg || i + lane >= t.nblk || p0 >= t.hi || p0 + ps <= t.lo) return -1;
+        const int phys = a.block_tables[(size_t)t.row * a.max_pages + (p0 >> a.page_shift)];
         if (phys >= 0 && phys < a.num_pages) return phys;
         atomicOr(fl, MXSA_FLAG_PAGE);
         return -1;
       };
-      int win[2] = {pages_at(0, 0), pages_at(0, 1)}, ahead[2] = {pages_at(32, 0), pages_at(32, 1)};
-      int prev[2] = {-1, -1};
-      for (int i = 0; i <= s.n && ok; ++i) {
-        int cur[2] = {-1, -1};
-        if (i < s.n) {
-          if ((i & 31) == 0 && i > 0) {
-#pragma unroll
-            for (int pg = 0; pg < 2; ++pg) {
-              win[pg] = ahead[pg];
-              ahead[pg] = pages_at(i + 32, pg);
+      HTile next = resolve(q ? before1 : cta - before1);  // the first place is the CTA's own
+      int win[2] = {pages_at(next, 0, 0), pages_at(next, 0, 1)};
+      for (int n = 0; ok; ++n) {
+        const int w = n % kHWork;
+        ok = hwarp_all(
+            mbar_wait(&c.work_empty[w], ((n / kHWork) & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
+        if (!ok) break;
+        const HTile t = next;
+        if (lane == 0) {
+          c.work[w] = t;
+          mbar_arrive(&c.work_full[w]);
+        }
+        if (end) break;
+        auto load_q = [&] {
+          const int nh = t.keys ? 1 : 2;
+          for (int h = 0; h < nh && ok; ++h, ++qn) {
+            const int b = qn & 1;
+            ok = hwarp_all(
+                mbar_wait(&c.q_empty[b], ((qn >> 1) & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
+            if (!ok) break;
+            uint8_t* qd = sm + b * kHTileBytes;
+            uint64_t* full = &c.q_full[qn & 3];
+            const int t0 = t.tok0 + h * a.T, nt = min(a.T, t.ntok - h * a.T);
+            if (nt > kHSmallQ) {  // one box; rows past the tile's tokens are never used
+              if (lane == 0) {
+                mbar_arrive_expect_tx(full, (uint32_t)(G * a.T) * 256u);
+                tma_load_3d(qd, &tmq, full, 0, t.g * G, t0);
+                tma_load_3d(qd + 16384, &tmq, full, 64, t.g * G, t0);
+              }
+            } else {  // token by token, each copy of the rows
+              const int copies = max(t.keys, 1), apart = 128 / copies;
+              if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(G * nt * copies) * 256u);
+              __syncwarp();
+              for (int x = lane; x < nt * copies * 2; x += 32) {
+                const int col = x & 1, cp = (x >> 1) % copies, tk = (x >> 1) / copies;
+                tma_load_3d(qd + col * 16384 + (cp * apart + tk * G) * 128, &tmq1, full, col * 64, t.g * G, t0 + tk);
+              }
             }
           }
-          cur[0] = __shfl_sync(0xffffffffu, win[0], i & 31);
-          cur[1] = __shfl_sync(0xffffffffu, win[1], i & 31);
-        }
-        // K of block i, then V of block i - 1: the ring's order
+        };
+        // The next tile is claimed six blocks before the end, not sooner: a
+        // claimed tile waits for this CTA.  Its record and pages are there by
+        // the time its first K can be loaded.
+        const int claim_at = max(t.nblk - 6, 0), resolve_at = min(claim_at + 2, t.nblk);
+        int place = 0;
+        int ahead[2] = {pages_at(t, 32, 0), pages_at(t, 32, 1)};  // the next window
+        int prev[2] = {-1, -1};
+        for (int i = 0; i <= t.nblk && ok; ++i) {
+          // (the first K is on its way before the q buffers are waited for)
+          if (i == 1) load_q();
+          if (i == claim_at && lane == 0) place = atomicAdd(&a.ws.hdr->next[q], 1);
+          if (i == resolve_at) next = resolve(place);
+          int cur[2] = {-1, -1};
+          if (i < t.nblk) {
+            if ((i & 31) == 0 && i > 0) {
+#pragma unroll
+              for (int pg = 0; pg < 2; ++pg) {
+                win[pg] = ahead[pg];
+                ahead[pg] = pages_at(t, i + 32, pg);
+              }
+            }
+            cur[0] = __shfl_sync(0xffffffffu, win[0], i & 31);
+            cur[1] = __shfl_sync(0xffffffffu, win[1], i & 31);
+          } else {
+            win[0] = pages_at(next, 0, 0);
+            win[1] = pages_at(next, 0, 1);
+          }
+          // K of block i, then V of block i - 1: the ring's order
 #pragma unroll
           for (int kv = 0; kv < 2 && ok; ++kv) {
-            if (kv == 0 ? i >= s.n : i == 0) continue;
+            if (kv == 0 ? i >= t.nblk : i == 0) continue;
             const int* pg = kv == 0 ? cur : prev;
             const int st = at % kHStages, use = at / kHStages;
             ok = hwarp_all(mbar_wait(&c.kv_empty[st], (use & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
@@ -897,7 +945,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
               mbar_arrive_expect_tx(full, (uint32_t)present * (uint32_t)ps * 256u);
               for (int x = 0; x < npg; ++x) {
                 if (pg[x] < 0) continue;
-                const int z = pg[x] * a.Hkv + s.t.g;
+                const int z = pg[x] * a.Hkv + t.g;
                 tma_load_3d(dst + x * 8192, tm, full, 0, 0, z);
                 tma_load_3d(dst + 16384 + x * 8192, tm, full, 64, 0, z);
               }
@@ -962,12 +1010,9 @@ __global__ void __launch_bounds__(kHThreads, 1)
         owed = -1;
       };
       const uint32_t tS = uniform(tmem + h * 256);
-      for (int ti = range.x; ti <= range.y && ok; ++ti) {
-        HSeg s;
-        s.t = load_tile(a.ws.tiles + ti);  // (the last blocks' softmax takes longer than this)
-        cut(&s, share, cta);
-        if (s.n <= 0) continue;
-        const int n = s.n, keys = s.t.keys, stride = keys ? 2 : 1;
+      HTile t;
+      while (ok && next_tile(&t)) {
+        const int n = t.nblk, keys = t.keys, stride = keys ? 2 : 1;
         const int half = keys ? h ^ (qn & 1) : 0;  // (see the softmax)
         const int qp = keys ? qn : qn + h;
         for (int i = half; i < n && ok; i += stride) {
@@ -1065,32 +1110,29 @@ __global__ void __launch_bounds__(kHThreads, 1)
     const uint32_t tS = tmem + h * 256 + lane_addr, tO = tS + 128;
     int at = 0, qn = 0, n_s = 0, n_o = 0;
     bool ok = true;
-    HTile next = range.x <= range.y ? load_tile(a.ws.tiles + range.x) : HTile{};
-    for (int ti = range.x; ti <= range.y && ok; ++ti) {
-      // what the block loop and the epilogue need of the tile, and no more:
-      // a row's 128 scores leave few registers
-      HSeg s;
-      s.t = next;
-      cut(&s, share, cta);
-      const int n = s.n, b0 = s.b0, lo = s.t.lo, key_end = s.t.hi, keys = s.t.keys, stride = keys ? 2 : 1;
+    HTile t;
+    while (ok && next_tile(&t)) {
+      // (what the block loop and the epilogue need of the tile, and no more: a
+      // row's 128 scores leave few registers)
+      const int n = t.nblk, b0 = t.blk0, lo = t.lo, key_end = t.hi, keys = t.keys, stride = keys ? 2 : 1;
       // the group that takes a one-half tile's first block changes with the q
       // buffer, so that short tiles keep both groups busy
       const int half = keys ? h ^ (qn & 1) : 0;
-      if (n > 0) qn += keys ? 1 : 2;
+      qn += keys ? 1 : 2;
       // the thread's row of the tile's (copies of a one-half tile's rows stand
       // `apart` rows apart) and its token within the tile
       const int apart = keys > 1 ? 128 / keys : 128;
       const int row = r & (apart - 1), copy = r / apart;
       const int rt = row / G, tt = rt + (keys ? 0 : h * a.T);
-      const bool live = rt < a.T && tt < s.t.ntok;
-      const long long rows = (long long)s.t.ntok * G;
-      const long long base = part_row(s.t, cta, cuts) + half * rows, pr = base + tt * G + (row - rt * G);
+      const bool live = rt < a.T && tt < t.ntok;
+      const long long rows = (long long)t.ntok * G;
+      const long long base = t.part0 + half * rows, pr = base + tt * G + (row - rt * G);
       const bool warp_live = __any_sync(0xffffffffu, live);
       int hi = key_end;  // the row sees the keys [lo, hi), all of the warp's rows [lo, warp_hi)
-      if (n > 0 && a.causal && live) hi = min(hi, a.ws.tok[s.t.tok0 + tt].keys);
+      if (a.causal && live) hi = min(hi, a.ws.tok[t.tok0 + tt].keys);
       const int warp_hi = __reduce_min_sync(0xffffffffu, hi);
       float m = -INFINITY, l = 0.f;
-      bool mine = false;  // this group has blocks of the segment
+      bool mine = false;  // this group has blocks of the tile
       for (int i = half; i < n && ok; i += stride, ++n_s) {
         const int k0 = (b0 + i) << 7;  // the block's first key
         ok = hwarp_all(mbar_wait(&c.s_full[h], n_s & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
@@ -1145,7 +1187,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
           if (__any_sync(0xffffffffu, raise)) {
             const float f = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - bm)) : 1.f;
             if (mine) {
-              // O holds the segment's blocks so far and is complete: S's
+              // O holds the tile's blocks so far and is complete: S's
               // barrier follows every product issued before
               scale_o(tO, f);
             }
@@ -1188,10 +1230,9 @@ __global__ void __launch_bounds__(kHThreads, 1)
         if (lane == 0) mbar_arrive(&c.p_full[h]);
         mine = true;
       }
-      at += 2 * max(n, 0);
-      if (ti < range.y) next = load_tile(a.ws.tiles + ti + 1);
+      at += 2 * n;
       if (!ok || !mine) continue;
-      // ---- the segment's partial rows
+      // ---- the tile's partial rows
       ok = hwarp_all(mbar_wait(&c.o_full[h], n_o & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
       if (!ok) break;
       ++n_o;
@@ -1236,7 +1277,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
 // ------------------------------------------------------------------- join
 // out = sum w_k o_k / sum w_k, w_k = 2^(lse_k - max lse), over the partials of
 // a (token, query head) row: those of its sequence's own tiles and of its
-// group's, a chunk and a range each.  One CTA per kv head and `tokens` tokens
+// group's, one or two for each chunk.  One CTA per kv head and `tokens` tokens
 // (several when there are many: a row's chain of dependent loads, token,
 // tiles, log-sum-exps, partials, is what it waits for).  A warp lists a
 // token's partials, which its G rows share; then a warp takes a row at a
@@ -1245,11 +1286,6 @@ __global__ void __launch_bounds__(kHThreads, 1)
 constexpr int kHJoinWarps = 8;
 constexpr int kHJoinDepth = 4;
 constexpr int kHJoinTokens = 8;
-// Partials of one row: its two jobs have a chunk each, plus at most
-// kHCostRatio x `ctas` further chunks and `ctas` cuts, all of them possibly in
-// two halves.
-constexpr int kHJoinMax = 2 * (2 + (kHCostRatio + 1) * kHMaxCtas);
-
 struct HJoinArgs {
   HPtrs ws;
   uint8_t* out;
@@ -1257,11 +1293,12 @@ struct HJoinArgs {
   int32_t Hkv, G, total_q;
   int32_t tokens;  // of one CTA
   int32_t slots;   // rows at once: a power of two, at most the warps
+  int32_t cap;     // partials of one row, at most
 };
 
 template <bool kBf16>
 __global__ void __launch_bounds__(kHJoinWarps * 32) k_shared_join(HJoinArgs a) {
-  extern __shared__ int32_t lists[];  // [tokens][kHJoinMax]
+  extern __shared__ int32_t lists[];  // [tokens][cap]
   __shared__ int32_t count[kHJoinTokens];
   __shared__ float4 sum[kHJoinWarps][32];
   __shared__ float weight[kHJoinWarps];
@@ -1272,49 +1309,34 @@ __global__ void __launch_bounds__(kHJoinWarps * 32) k_shared_join(HJoinArgs a) {
   pdl_wait();
   if (warp < nt) {
     const int t = t0 + warp;
-    int32_t* list = lists + warp * kHJoinMax;
+    int32_t* list = lists + warp * a.cap;
     const HTok tk = a.ws.tok[t];
-    const long long share = a.ws.hdr->share, cuts = a.ws.hdr->cuts;
     int n = 0;
     for (int x0 = 0; x0 < tk.own_nch + tk.pre_nch; x0 += 32) {
       const int x = x0 + lane;
-      HSeg s;
-      s.t.nseg = s.t.keys = s.t.ntok = s.t.tok0 = s.t.cta0 = 0;
-      s.t.part0 = 0;
-      int mine = 0;
-      if (x < tk.own_nch + tk.pre_nch) {
-        const bool p = x < tk.pre_nch;
-        s.t = load_tile(a.ws.tiles + (p ? tk.pre_base + (g * tk.pre_nch + x) * tk.pre_nrt
-                                        : tk.own_base + (g * tk.own_nch + x - tk.pre_nch) * tk.own_nrt));
-        for (int k = 0; k < s.t.nseg; ++k) {
-          cut(&s, share, s.t.cta0 + k);
-          mine += s.t.keys && s.n > 1 ? 2 : 1;
-        }
-      }
-      int y = mine;
+      HPieces p{0, 0, 0, 0};
+      if (x < tk.own_nch + tk.pre_nch)
+        p = a.ws.pieces[x < tk.pre_nch ? tk.pre_base + (g * tk.pre_nch + x) * tk.pre_nrt
+                                       : tk.own_base + (g * tk.own_nch + x - tk.pre_nch) * tk.own_nrt];
+      int y = p.pieces;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int z = __shfl_up_sync(0xffffffffu, y, o);
         if (lane >= o) y += z;
       }
-      int at = n + y - mine;
+      int at = n + y - p.pieces;
       n += __shfl_sync(0xffffffffu, y, 31);
-      for (int k = 0; k < s.t.nseg; ++k) {
-        cut(&s, share, s.t.cta0 + k);
-        const int nh = s.t.keys && s.n > 1 ? 2 : 1;
-        for (int hh = 0; hh < nh; ++hh, ++at)
-          if (at < kHJoinMax)  // (rows fit 32 bits: see shared_rows_fit)
-            list[at] = (int)part_row(s.t, s.t.cta0 + k, cuts) + (hh * s.t.ntok + t - s.t.tok0) * a.G;
-      }
+      for (int k = 0; k < p.pieces; ++k, ++at)
+        if (at < a.cap) list[at] = p.part0 + (k * p.ntok + t - p.tok0) * a.G;  // (within the cap: see shared_layout)
     }
-    if (lane == 0) count[warp] = tk.seq < 0 ? -1 : min(n, kHJoinMax);  // -1: outside every sequence
+    if (lane == 0) count[warp] = tk.seq < 0 ? -1 : min(n, a.cap);  // -1: outside every sequence
   }
   __syncthreads();
   const int splits = kHJoinWarps / a.slots, slot = warp & (a.slots - 1), part = warp / a.slots;
   for (int i0 = 0; i0 < nt * a.G; i0 += a.slots) {
     const int row = i0 + slot, x = row / a.G, hh = row - x * a.G;
     const int n = row < nt * a.G ? count[x] : -1;
-    const int32_t* list = lists + x * kHJoinMax;
+    const int32_t* list = lists + x * a.cap;
     float M = -INFINITY, W = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i = lane; i < n; i += 32) M = hmax_nan(M, a.ws.part_lse[list[i] + hh]);
@@ -1481,12 +1503,13 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
   ja.total_q = p.total_q;
   // several tokens to a CTA once there are four CTAs per SM
   const long long pairs = (long long)p.total_q * p.num_kv_heads;
-  ja.tokens = (int)std::max(1LL, std::min<long long>(kHJoinTokens, pairs / (4LL * sms)));
+  ja.cap = L.join_cap;
+  ja.tokens = (int)std::max(1LL, std::min<long long>({kHJoinTokens, pairs / (4LL * sms), 40960 / (4LL * ja.cap)}));
   ja.slots = 1;
   while (ja.slots < G * ja.tokens && ja.slots < kHJoinWarps) ja.slots *= 2;
   const long long blocks = (long long)((p.total_q + ja.tokens - 1) / ja.tokens) * p.num_kv_heads;
   return launch_pdl(bf16 ? k_shared_join<true> : k_shared_join<false>, dim3((unsigned)blocks), dim3(kHJoinWarps * 32),
-                    (size_t)ja.tokens * kHJoinMax * 4, st, ja);
+                    (size_t)ja.tokens * ja.cap * 4, st, ja);
 }
 
 }  // namespace mxsa

@@ -1,13 +1,14 @@
 """CPU models of the dense path over shared prefixes (mxsa_dense_shared_fwd).
 
-The plan: jobs, tiles, the line of steps and its cut into ranges, restated in
-Python; random problems check that every visible (token, key) pair lies in
-exactly one segment, that a row's partials are distinct and that the tile and
-partial-row bounds that size the workspace hold.
+The plan: jobs, tiles and their chunks restated in Python; random problems
+check that every visible (token, key) pair lies in exactly one tile, that a
+row's partials are distinct and that the bounds on tiles, partial rows and
+partials of one row that size the workspace hold.
 
-The forward's mbarrier protocol (producer, two MMA issuers, two softmax groups,
-five K/V stages, two q buffers) under random interleavings: no deadlock, and
-no buffer is refilled or overwritten before its readers are done.
+The forward's protocol (producer, two MMA issuers, two softmax groups, five
+K/V stages, two q buffers, the ring of tiles) under random interleavings: no
+deadlock, and no buffer is refilled or overwritten before its readers are
+done.
 """
 import random
 
@@ -15,7 +16,8 @@ import pytest
 
 from tests.test_barrier_models import Bar
 
-MAXC, WR, WK, TILE, STAGES = 160, 8, 5, 10, 5
+MAXC, WR, WK, TILE, STAGES, WORK = 160, 8, 4, 10, 5, 4
+PER_CTA, SMALL, ONE_CHUNK = 2, 4, 24
 
 
 def cdiv(a, b):
@@ -23,7 +25,7 @@ def cdiv(a, b):
 
 
 def plan(p):
-    """p: cu, lens, gp, prefix, hkv, hq, causal, ctas.  Returns (jobs, tiles, share)."""
+    """p: cu, lens, gp, prefix, hkv, hq, causal, ctas.  Returns (tiles, partial rows)."""
     G = p["hq"] // p["hkv"]
     T, B, cu = 128 // G, len(p["lens"]), p["cu"]
     seq_group, prefix = [-1] * B, []
@@ -50,11 +52,19 @@ def plan(p):
         j["w"] = WR if j["nrt"] > keys else WK
         if j["nb"]:
             total += p["hkv"] * ((j["nrt"] - keys) * (j["nb"] * WR + TILE) + keys * (j["nb"] * WK + TILE))
-    goal = max(cdiv(total, p["ctas"]), 1)
+    share = max(cdiv(total, p["ctas"]), 1)
     tiles = []
     for j in jobs:
-        j["chunk"] = min(cdiv(goal, j["w"]), max(j["nb"], 1))
-        j["nch"] = cdiv(j["nb"], j["chunk"])
+        whole = cdiv(share, j["w"])
+        nb = j["nb"]
+        c = min(whole if whole <= ONE_CHUNK else cdiv(whole, PER_CTA), max(nb, 1))
+        if whole <= ONE_CHUNK or nb < 4 * c:
+            nfull = nch = max((nb + c // 2) // c, 1) if nb else 0
+            c, small = cdiv(nb, nch) if nch else 1, 1
+        else:
+            nfull, small = nb // c - 1, cdiv(c, SMALL)
+            nch = nfull + cdiv(nb - nfull * c, small)
+        j["chunk"], j["nch"] = c, nch
         j["tile0"] = len(tiles)
         for g in range(p["hkv"]):
             for ch in range(j["nch"]):
@@ -63,49 +73,16 @@ def plan(p):
                     end = cdiv(j["hi"], 128)
                     if p["causal"] and j["own"]:
                         end = min(end, cdiv(max(j["hi"] - j["ntok"] + rt * 2 * T + ntok, 0), 128))
-                    b0 = j["lo"] // 128 + ch * j["chunk"]
+                    fine = max(ch - nfull, 0)
+                    b0 = j["lo"] // 128 + (ch - fine) * c + fine * small
                     tiles.append(dict(tok0=j["tok0"] + rt * 2 * T, ntok=ntok, g=g, lo=j["lo"], hi=j["hi"], b0=b0,
-                                      n=max(min(b0 + j["chunk"], end) - b0, 0), keys=ntok <= T, job=j))
-    cost = 0
+                                      n=max(min(b0 + (c if ch < nfull else small), end) - b0, 0), keys=ntok <= T, job=j))
+    part = 0
     for t in tiles:
-        t["w"] = WK if t["keys"] else WR
-        t["cost0"] = cost + TILE
-        cost += t["n"] * t["w"] + TILE if t["n"] else 0
-    share = max(cdiv(cost, p["ctas"]), WR)
-    part, run, first = 0, 0, {}
-    for i, t in enumerate(tiles):  # as the plan's threads walk them
-        t["part0"], t["nseg"], t["cta0"] = part, 0, 0
-        if not t["n"]:
-            continue
-        x = t["n"] * t["w"] + TILE
-        last = run + x - t["w"]
-        r = run // share
-        end = (r + 1) * share
-        if run == end - share:
-            first[r] = i
-        while t["cost0"] >= end:
-            r, end = r + 1, end + share
-            first[r] = i
-        t["cta0"] = r
-        while last >= end:
-            r, end = r + 1, end + share
-            first[r] = i
-        t["nseg"] = r - t["cta0"] + 1
-        while run + x > end:
-            r, end = r + 1, end + share
-            first[r] = i
-        part += t["ntok"] * G * (2 if t["keys"] else 1)
-        run += x
-        assert t["cta0"] == t["cost0"] // share and t["cta0"] + t["nseg"] - 1 == last // share < p["ctas"]
-    assert all(k < p["ctas"] for k in first)
-    ranges = {k: (first[k], first.get(k + 1, len(tiles) - 1)) for k in first}
-    return jobs, tiles, share, part, ranges
-
-
-def cut(t, share, c):
-    at = lambda x: 0 if x <= t["cost0"] else min(cdiv(x - t["cost0"], t["w"]), t["n"])
-    i0, i1 = at(c * share), at((c + 1) * share)
-    return i0, i1 - i0
+        t["part0"] = part
+        if t["n"]:
+            part += t["ntok"] * G * (2 if t["keys"] else 1)
+    return tiles, part
 
 
 def random_problem(r):
@@ -129,23 +106,14 @@ def test_plan_covers_every_key_once_within_its_bounds(seed):
     p = random_problem(random.Random(seed))
     G, B = p["hq"] // p["hkv"], len(p["lens"])
     T = 128 // G
-    jobs, tiles, share, part, ranges = plan(p)
-    assert len(tiles) <= p["hkv"] * (2 * (p["total_q"] // (2 * T)) + 2 * B) + 2 * MAXC
-    # rows of the tiles' first segments, then 256 for each range's cut
-    assert part + 256 * p["ctas"] <= 4 * p["total_q"] * p["hq"] + 256 * 3 * MAXC
+    tiles, part = plan(p)
+    triples = p["hkv"] * (2 * (p["total_q"] // (2 * T)) + 2 * B)
+    blocks = max(1, cdiv(max(p["lens"]), 128))
+    by_cost = PER_CTA * 2 * MAXC * (4 + 2 * SMALL - 1) // 4
+    extra = min(by_cost, triples * (blocks - 1))
+    assert len(tiles) <= triples + extra
+    assert part <= 4 * p["total_q"] * p["hq"] + min(256, 2 * p["total_q"] * G) * extra
     assert all(t["ntok"] * G * (2 if t["keys"] else 1) <= 256 for t in tiles)
-    for i, t in enumerate(tiles):
-        got = 0
-        for k in range(t["nseg"]):
-            c = t["cta0"] + k
-            i0, n = cut(t, share, c)
-            assert n > 0 and i0 == got  # each range between the first and the last holds a step
-            got += n
-            assert ranges[c][0] <= i <= ranges[c][1]
-            assert k == 0 or i == ranges[c][0]  # a range's cut is its first tile
-        assert got == t["n"]
-        for c in (t["cta0"] - 1, t["cta0"] + t["nseg"]):
-            assert t["n"] == 0 or cut(t, share, c)[1] == 0
     # tokens: the key blocks of its tiles, masked, make up its visible keys
     for s in range(B):
         for tok in range(p["cu"][s], p["cu"][s + 1]):
@@ -156,8 +124,8 @@ def test_plan_covers_every_key_once_within_its_bounds(seed):
                 for t in tiles:
                     if t["g"] == g and t["tok0"] <= tok < t["tok0"] + t["ntok"] and t["n"]:
                         got.append((max(t["b0"] * 128, t["lo"]), min((t["b0"] + t["n"]) * 128, t["hi"], see)))
-                        parts += t["nseg"] * (2 if t["keys"] else 1)
-                assert parts <= 2 * (2 + 3 * MAXC)
+                        parts += min(t["n"], 2) if t["keys"] else 1
+                assert parts <= 2 * min(2 + by_cost // p["hkv"], 2 * blocks + 2)
                 got = sorted(x for x in got if x[1] > x[0])
                 at = 0
                 for lo, hi in got:
@@ -182,7 +150,7 @@ def test_ring_places_are_the_producers_order(n):
 
 
 def run_protocol(segs, seed):
-    """segs: (blocks, keys, edge) of the CTA's segments; keys: 0 two halves, 1 one half, 4 one half with copies; edge: the groups wait for V to clear rows of it."""
+    """segs: (blocks, keys, edge) of the CTA's tiles; keys: 0 two halves, 1 one half, 4 one half with copies; edge: the groups wait for V to clear rows of it."""
     rnd = random.Random(seed)
     B, pending = {}, {}
 
@@ -195,6 +163,23 @@ def run_protocol(segs, seed):
         bar(f"q_empty{i}", 2)
     for i in range(4):
         bar(f"q_full{i}")
+    for i in range(WORK):
+        bar(f"work_full{i}")
+        bar(f"work_empty{i}", 4)
+    work = [None] * WORK
+
+    def tiles_of():
+        """The tiles as a role sees them, through the ring."""
+        k = 0
+        while True:
+            yield ("wait", B[f"work_full{k % WORK}"], (k // WORK) & 1)
+            got = work[k % WORK]
+            B[f"work_empty{k % WORK}"].arrive()
+            k += 1
+            assert got[0] == k - 1, "another tile's record"
+            yield ("tile", got[1])
+            if got[1] is None:
+                return
     for i in range(STAGES):
         bar(f"kv_full{i}")
         bar(f"kv_full{i + STAGES}")
@@ -217,18 +202,25 @@ def run_protocol(segs, seed):
 
     def producer():
         at = qn = 0
-        for n, keys, _ in segs:
-            for _h in range(1 if keys else 2):
-                b = qn & 1
-                yield ("wait", B[f"q_empty{b}"], ((qn >> 1) & 1) ^ 1)
-                assert qn < 2 or qreads[qn - 2] == 0, "q refilled early"
-
-                def land(b=b, qn=qn):
-                    qbuf[b] = qn
-                    B[f"q_full{qn & 3}"].arrive()
-                later(f"q{b}", land)
-                qn += 1
+        for k, tile in enumerate(segs + [None]):
+            yield ("wait", B[f"work_empty{k % WORK}"], ((k // WORK) & 1) ^ 1)
+            work[k % WORK] = (k, tile)
+            B[f"work_full{k % WORK}"].arrive()
+            if tile is None:
+                return
+            n, keys, _ = tile
             for x in range(2 * n):
+                if x == 1:  # the q buffers after the first K
+                    for _h in range(1 if keys else 2):
+                        b = qn & 1
+                        yield ("wait", B[f"q_empty{b}"], ((qn >> 1) & 1) ^ 1)
+                        assert qn < 2 or qreads[qn - 2] == 0, "q refilled early"
+
+                        def land(b=b, qn=qn):
+                            qbuf[b] = qn
+                            B[f"q_full{qn & 3}"].arrive()
+                        later(f"q{b}", land)
+                        qn += 1
                 st = at % STAGES
                 yield ("wait", B[f"kv_empty{st}"], ((at // STAGES) & 1) ^ 1)
                 assert at < STAGES or reads[at - STAGES] == 0, "stage refilled early"
@@ -279,7 +271,13 @@ def run_protocol(segs, seed):
                     B[f"o_full{h}"].arrive()
             later(f"mma{h}", done)
 
-        for n, keys, _ in segs:
+        for got in tiles_of():
+            if got[0] == "wait":
+                yield got
+                continue
+            if got[1] is None:
+                break
+            n, keys, _ = got[1]
             half = h ^ (qn & 1) if keys else 0
             qp = qn if keys else qn + h
             for i in range(half, n, 2 if keys else 1):
@@ -333,7 +331,13 @@ def run_protocol(segs, seed):
 
     def softmax(h):
         at = ns = no = qn = 0
-        for n, keys, edge in segs:
+        for got in tiles_of():
+            if got[0] == "wait":
+                yield got
+                continue
+            if got[1] is None:
+                break
+            n, keys, edge = got[1]
             mine = False
             half = h ^ (qn & 1) if keys else 0
             qn += 1 if keys else 2
