@@ -182,9 +182,9 @@ struct HPlanArgs {
 };
 
 // One CTA that the forward waits for: few barriers, and what a thread does
-// per tile kept short (256, 512 and 1024 threads take the same time within
-// 2 us).
-constexpr int kHPlanThreads = 512;
+// per tile kept short.  256 threads: 512 and 1024 take up to 2 us longer with
+// few sequences and are not faster with 256.
+constexpr int kHPlanThreads = 256;
 
 struct HPlanSmem {
   int32_t cu[kHMaxSeqs + 1], len[kHMaxSeqs], seq_group[kHMaxSeqs];
@@ -194,28 +194,41 @@ struct HPlanSmem {
   long long scan[6][kHPlanThreads / 32];
 };
 
-// exclusive sum over the block; *total gets the whole.  `s`: one word per
-// warp, not used by another call of the launch.
-__device__ __forceinline__ long long block_scan(long long v, long long* s, long long* total) {
+// Exclusive sums over the block of kN values at once; total gets the wholes.
+// `s`: kN words per warp, not used by another call of the launch.
+template <int kN>
+__device__ __forceinline__ void block_scan(long long (&v)[kN], long long* s, long long (&total)[kN]) {
   constexpr int kWarps = kHPlanThreads / 32;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  long long x = v;
+  long long x[kN], y[kN];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s[w] = x;
+  for (int i = 0; i < kN; ++i) x[i] = v[i];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const long long z = __shfl_up_sync(0xffffffffu, x[i], o);
+      if (lane >= o) x[i] += z;
+    }
+  if (lane == 31)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) s[i * kWarps + w] = x[i];
   __syncthreads();
-  long long y = s[lane & (kWarps - 1)];
 #pragma unroll
-  for (int o = 1; o < kWarps; o <<= 1) {
-    const long long z = __shfl_up_sync(0xffffffffu, y, o);
-    if ((lane & (kWarps - 1)) >= o) y += z;
+  for (int i = 0; i < kN; ++i) y[i] = s[i * kWarps + (lane & (kWarps - 1))];
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const long long z = __shfl_up_sync(0xffffffffu, y[i], o);
+      if ((lane & (kWarps - 1)) >= o) y[i] += z;
+    }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const long long before = __shfl_sync(0xffffffffu, y[i], max(w - 1, 0));
+    total[i] = __shfl_sync(0xffffffffu, y[i], kWarps - 1);
+    v[i] = x[i] - v[i] + (w ? before : 0);
   }
-  const long long before = __shfl_sync(0xffffffffu, y, max(w - 1, 0));
-  *total = __shfl_sync(0xffffffffu, y, kWarps - 1);
-  return x - v + (w ? before : 0);
 }
 
 // the last index i of a[0 .. n) (non-decreasing, a[0] <= x) with a[i] <= x
@@ -283,26 +296,29 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     return j >= 0 && gp_ok && s.gp[j + 1] - s.gp[j] >= 2 ? min(max(s.want[j], 0), s.shortest[j]) : 0;
   };
 
-  // A thread's jobs are consecutive, and its tiles below.
+  // Jobs: the groups' prefixes, whose tiles are the longest and go first, then
+  // the sequences' own keys.  A thread's jobs are consecutive, and its tiles
+  // below.
   const int njobs = B + NG, T2 = 2 * a.T;
   const int jper = (njobs + kHPlanThreads - 1) / kHPlanThreads;
   const int q0 = min(njobs, tid * jper), q1 = min(njobs, q0 + jper);
   long long cost[2] = {0, 0}, total[2];  // of the two kinds of tiles
   for (int q = q0; q < q1; ++q) {
     HJob j;
-    if (q < B) {
-      j.tok0 = s.cu[q];
-      j.ntok = s.cu[q + 1] - s.cu[q];
-      j.row = q;
-      j.lo = prefix_of(s.seq_group[q]);
-      j.hi = s.len[q];
-    } else {
-      const int r = q - B, P = prefix_of(r);
-      j.row = P > 0 ? s.gp[r] : 0;
-      j.tok0 = P > 0 ? s.cu[s.gp[r]] : 0;
-      j.ntok = P > 0 ? s.cu[s.gp[r + 1]] - j.tok0 : 0;
+    if (q < NG) {
+      const int P = prefix_of(q);
+      j.row = P > 0 ? s.gp[q] : 0;
+      j.tok0 = P > 0 ? s.cu[s.gp[q]] : 0;
+      j.ntok = P > 0 ? s.cu[s.gp[q + 1]] - j.tok0 : 0;
       j.lo = 0;
       j.hi = P;
+    } else {
+      const int r = q - NG;
+      j.tok0 = s.cu[r];
+      j.ntok = s.cu[r + 1] - s.cu[r];
+      j.row = r;
+      j.lo = prefix_of(s.seq_group[r]);
+      j.hi = s.len[r];
     }
     const int nb = j.ntok > 0 && j.hi > j.lo ? ((j.hi + 127) >> 7) - (j.lo >> 7) : 0;
     const int rem = j.ntok % T2;
@@ -317,10 +333,9 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     }
     s.job[q] = j;
   }
-  block_scan(cost[0], s.scan[0], &total[0]);
-  block_scan(cost[1], s.scan[1], &total[1]);
+  block_scan<2>(cost, s.scan[0], total);
   const long long share = max(ceil_div(total[0] + total[1], a.ctas), 1LL);
-  long long mine = 0, all = 0;
+  long long tiles[1] = {0}, all[1];
   for (int q = q0; q < q1; ++q) {
     HJob& j = s.job[q];
     const int nb = j.nch;
@@ -337,16 +352,17 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
       j.small = (want + kHSmall - 1) / kHSmall;
       j.nch = j.nfull + (nb - j.nfull * want + j.small - 1) / j.small;
     }
-    mine += (long long)a.Hkv * j.nch * j.nrt;
+    tiles[0] += (long long)a.Hkv * j.nch * j.nrt;
   }
-  long long at = block_scan(mine, s.scan[2], &all);
+  block_scan<1>(tiles, s.scan[2], all);
+  long long at = tiles[0];
   for (int q = q0; q < q1; ++q) {
     HJob& j = s.job[q];
     j.tile0 = (int)at;
     s.tile0[q] = (int)at;
     at += (long long)a.Hkv * j.nch * j.nrt;
   }
-  const int ntiles = (int)min(all, a.tile_cap);  // (all is within the cap: see shared_layout)
+  const int ntiles = (int)min(all[0], a.tile_cap);  // (all is within the cap: see shared_layout)
   __syncthreads();
 
   const int tper = (ntiles + kHPlanThreads - 1) / kHPlanThreads;
@@ -376,7 +392,7 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     const HJob& j = s.job[c.q];
     *ntok = min(T2, j.ntok - c.rt * T2);
     int end = (j.hi + 127) >> 7;
-    if (a.causal && c.q < B)  // keys past the last token's position are nobody's
+    if (a.causal && c.q >= NG)  // keys past the last token's position are nobody's
       end = min(end, (max(j.hi - j.ntok + c.rt * T2 + *ntok, 0) + 127) >> 7);
     const int fine = max(c.ch - j.nfull, 0);
     *blk0 = (j.lo >> 7) + (c.ch - fine) * j.chunk + fine * j.small;
@@ -384,21 +400,22 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
   };
   // tiles of each queue (in one word; full and small ones) and partial rows
   // before the thread's own
-  long long full = 0, small = 0, rows = 0;
+  long long sums[3] = {0, 0, 0}, wholes[3];  // full, small, rows
   int blk0, nblk, ntok;
   HCursor c = c0;
   for (int i = i0; i < i1; ++i, advance(&c)) {
     size_of(c, &blk0, &nblk, &ntok);
     const bool keys = ntok <= a.T;
     if (nblk) {
-      (c.ch < s.job[c.q].nfull ? full : small) += keys ? 1LL << 32 : 1LL;
-      rows += ntok * a.G * (keys ? 2 : 1);
+      const long long one = keys ? 1LL << 32 : 1LL;
+      if (c.ch < s.job[c.q].nfull) sums[0] += one;
+      else sums[1] += one;
+      sums[2] += ntok * a.G * (keys ? 2 : 1);
     }
   }
-  long long all_full, all_small, all_rows;
-  full = block_scan(full, s.scan[3], &all_full);
-  small = block_scan(small, s.scan[4], &all_small) + all_full;  // (behind the queue's full ones)
-  long long part = block_scan(rows, s.scan[5], &all_rows);
+  block_scan<3>(sums, s.scan[3], wholes);
+  long long full = sums[0], small = sums[1] + wholes[0];  // (behind the queue's full ones)
+  long long part = sums[2];
   c = c0;
   for (int i = i0; i < i1; ++i, advance(&c)) {
     size_of(c, &blk0, &nblk, &ntok);
@@ -430,14 +447,14 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
       const int q = last_le(s.cu, B, i), L = s.len[q];
       v.seq = q;
       v.keys = a.causal ? min(max(L - (s.cu[q + 1] - i) + 1, 0), L) : L;
-      const HJob& own = s.job[q];
+      const HJob& own = s.job[NG + q];
       if (own.nrt > 0) {
         v.own_base = own.tile0 + (i - own.tok0) / T2;
         v.own_nch = own.nch;
         v.own_nrt = own.nrt;
       }
       if (prefix_of(s.seq_group[q]) > 0) {
-        const HJob& pre = s.job[B + s.seq_group[q]];
+        const HJob& pre = s.job[s.seq_group[q]];
         v.pre_base = pre.tile0 + (i - pre.tok0) / T2;
         v.pre_nch = pre.nch;
         v.pre_nrt = pre.nrt;
@@ -446,7 +463,7 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     a.ws.tok[i] = v;
   }
   if (tid == 0) {
-    const long long all_queued = all_full + all_small;
+    const long long all_queued = wholes[0] + wholes[1];
     const int n0 = (int)all_queued, n1 = (int)(all_queued >> 32);
     // (half of the share: the second kind's smaller tiles fill up the end)
     int with1 = (int)(total[1] * a.ctas / 2 / max(total[0] + total[1], 1LL));
@@ -840,12 +857,16 @@ __global__ void __launch_bounds__(kHThreads, 1)
       const int before1 = (int)((long long)cta * with1 / gridDim.x);
       int q = (int)((long long)(cta + 1) * with1 / gridDim.x) - before1;
       bool other = false, end = false;  // the queue it began with is empty; both are
+      auto claim = [&]() -> int {       // lane 0: a place of queue q (none is left behind the CTAs' own: no atomic)
+        return (q ? count[1] <= with1 : count[0] <= (int)gridDim.x - with1) ? INT_MAX
+                                                                            : atomicAdd(&a.ws.hdr->next[q], 1);
+      };
       auto resolve = [&](int place) {   // the tile at a place of queue q, or of the other queue
         place = __shfl_sync(0xffffffffu, place, 0);
         if (place >= (q ? count[1] : count[0]) && !other) {
           other = true;
           q ^= 1;
-          if (lane == 0) place = atomicAdd(&a.ws.hdr->next[q], 1);
+          if (lane == 0) place = claim();
           place = __shfl_sync(0xffffffffu, place, 0);
         }
         end = place >= (q ? count[1] : count[0]);
@@ -903,16 +924,22 @@ __global__ void __launch_bounds__(kHThreads, 1)
         };
         // The next tile is claimed six blocks before the end, not sooner: a
         // claimed tile waits for this CTA.  Its record and pages are there by
-        // the time its first K can be loaded.
-        const int claim_at = max(t.nblk - 6, 0), resolve_at = min(claim_at + 2, t.nblk);
+        // the time its first K can be loaded.  (In a short tile nothing waits
+        // for them before all its own loads are on their way.)
+        const int claim_at = max(t.nblk - 6, 0), resolve_at = claim_at + 2, pages_at_block = claim_at + 4;
         int place = 0;
         int ahead[2] = {pages_at(t, 32, 0), pages_at(t, 32, 1)};  // the next window
+        int first[2] = {-1, -1};                                  // the next tile's first one
         int prev[2] = {-1, -1};
         for (int i = 0; i <= t.nblk && ok; ++i) {
           // (the first K is on its way before the q buffers are waited for)
           if (i == 1) load_q();
-          if (i == claim_at && lane == 0) place = atomicAdd(&a.ws.hdr->next[q], 1);
-          if (i == resolve_at) next = resolve(place);
+          if (i == claim_at && lane == 0) place = claim();
+          if (i == resolve_at && i < t.nblk) next = resolve(place);
+          if (i == pages_at_block && i < t.nblk) {
+            first[0] = pages_at(next, 0, 0);
+            first[1] = pages_at(next, 0, 1);
+          }
           int cur[2] = {-1, -1};
           if (i < t.nblk) {
             if ((i & 31) == 0 && i > 0) {
@@ -924,9 +951,6 @@ __global__ void __launch_bounds__(kHThreads, 1)
             }
             cur[0] = __shfl_sync(0xffffffffu, win[0], i & 31);
             cur[1] = __shfl_sync(0xffffffffu, win[1], i & 31);
-          } else {
-            win[0] = pages_at(next, 0, 0);
-            win[1] = pages_at(next, 0, 1);
           }
           // K of block i, then V of block i - 1: the ring's order
 #pragma unroll
@@ -954,6 +978,13 @@ __global__ void __launch_bounds__(kHThreads, 1)
           prev[0] = cur[0];
           prev[1] = cur[1];
         }
+        if (resolve_at >= t.nblk) next = resolve(place);
+        if (pages_at_block >= t.nblk) {
+          first[0] = pages_at(next, 0, 0);
+          first[1] = pages_at(next, 0, 1);
+        }
+        win[0] = first[0];
+        win[1] = first[1];
       }
       // drain: the copies in flight land before the CTA may exit
       if (lane == 0) {
@@ -1284,7 +1315,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
 // time, kHJoinDepth partials in flight.  With fewer rows than warps several
 // warps take a row's partials in turn and add up in shared memory.
 constexpr int kHJoinWarps = 8;
-constexpr int kHJoinDepth = 4;
+constexpr int kHJoinDepth = 8;
 constexpr int kHJoinTokens = 8;
 struct HJoinArgs {
   HPtrs ws;
@@ -1339,25 +1370,29 @@ __global__ void __launch_bounds__(kHJoinWarps * 32) k_shared_join(HJoinArgs a) {
     const int32_t* list = lists + x * a.cap;
     float M = -INFINITY, W = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* po = reinterpret_cast<const float4*>(a.ws.part_o) + lane;
+    float4 o[kHJoinDepth];
+    float w[kHJoinDepth];
+    auto fetch = [&](int j0) {
+#pragma unroll
+      for (int u = 0; u < kHJoinDepth; ++u) {
+        const int j = j0 + u * splits;
+        w[u] = -INFINITY;
+        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < n) {  // warp-uniform
+          const long long pr = list[j] + hh;
+          w[u] = a.ws.part_lse[pr];
+          o[u] = __ldcs(po + pr * 32);
+        }
+      }
+    };
+    fetch(part);  // on their way before the log-sum-exps are known
     for (int i = lane; i < n; i += 32) M = hmax_nan(M, a.ws.part_lse[list[i] + hh]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = hmax_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int x = 16; x > 0; x >>= 1) M = hmax_nan(M, __shfl_xor_sync(0xffffffffu, M, x));
     if (n > 0 && M != -INFINITY) {
-      const float4* po = reinterpret_cast<const float4*>(a.ws.part_o) + lane;
       for (int j0 = part; j0 < n; j0 += kHJoinDepth * splits) {
-        float4 o[kHJoinDepth];
-        float w[kHJoinDepth];
-#pragma unroll
-        for (int u = 0; u < kHJoinDepth; ++u) {
-          const int j = j0 + u * splits;
-          w[u] = -INFINITY;
-          o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (j < n) {  // warp-uniform
-            const long long pr = list[j] + hh;
-            w[u] = a.ws.part_lse[pr];
-            o[u] = __ldcs(po + pr * 32);
-          }
-        }
+        if (j0 > part) fetch(j0);
 #pragma unroll
         for (int u = 0; u < kHJoinDepth; ++u) {
           w[u] = ex2_approx(w[u] - M);

@@ -36,13 +36,13 @@ def plan(p):
         for s in members:
             seq_group[s] = j if prefix[j] > 0 else -1
     jobs = []
-    for s in range(B):
-        jobs.append(dict(tok0=cu[s], ntok=cu[s + 1] - cu[s], lo=prefix[seq_group[s]] if seq_group[s] >= 0 else 0,
-                         hi=p["lens"][s], own=True))
     for j, P in enumerate(prefix):
         on = P > 0
         jobs.append(dict(tok0=cu[p["gp"][j]] if on else 0, ntok=cu[p["gp"][j + 1]] - cu[p["gp"][j]] if on else 0, lo=0,
                          hi=P, own=False))
+    for s in range(B):
+        jobs.append(dict(tok0=cu[s], ntok=cu[s + 1] - cu[s], lo=prefix[seq_group[s]] if seq_group[s] >= 0 else 0,
+                         hi=p["lens"][s], own=True))
     total = 0
     for j in jobs:
         j["nb"] = cdiv(j["hi"], 128) - j["lo"] // 128 if j["ntok"] > 0 and j["hi"] > j["lo"] else 0
