@@ -268,12 +268,14 @@ mxsa_status mxsa_dense_fwd(const mxsa_problem* problem, const void* q, const voi
  *                and partial rows (FP32); needs no initialisation, keeps
  *                nothing between calls
  * The other arguments and limits are mxsa_dense_fwd's: kv_dtype = q_dtype,
- * num_seqs <= 1024, topk unused; also total_q * num_q_heads < 2^29 - 2^15.  The
- * softmax weights are rounded to q_dtype before they multiply V, everything
- * else is FP32.  A NaN or infinity at a key outside [0, used_kv_len) of a
- * sequence does not reach its rows; under causal masking the V rows of a
- * sequence's own later tokens have to be finite.  Results do not depend on
- * timing: the same call gives the same bits.
+ * num_seqs <= 1024, topk unused; total_q * num_q_heads < 2^29 - 2^17 always
+ * fits.  The softmax weights are rounded to q_dtype before they multiply V,
+ * everything else is FP32.  A NaN or infinity at a key outside
+ * [0, used_kv_len) of a sequence does not reach its rows; under causal masking
+ * the V rows of keys that come after a token but that others of its group see
+ * have to be finite.  Results do not depend on timing: the same call gives the
+ * same bits.  Two calls that may run at the same time, captured graphs
+ * included, need a ws each.
  * cu_seqlens_q must be non-decreasing within [0, total_q], else MXSA_FLAG_CU
  * and nothing is written; tokens before cu_seqlens_q[0] and from
  * cu_seqlens_q[B] on are not written.  device_flags (may be NULL) also gets

@@ -323,6 +323,28 @@ def test_load_is_exact(q, kv, n, hkv, ps, idx):
             assert torch.equal(torch.nan_to_num(got, nan=0.0), torch.nan_to_num(ref, nan=0.0))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "nvfp4"])
+def test_slots_past_two_to_the_31_elements(kv):
+    """Written by norm_rope_store into the last slots of a cache of more than 2^31 elements, and read back."""
+    c = case(70, 8, 2, "bf16", kv, 64, 64, seed=41)
+    per = 2 * 64 * (72 if kv == "nvfp4" else 128)
+    pages = (1 << 31) // per + 3
+    kvt = "nvfp4" if kv == "nvfp4" else TDT[kv]
+    shape = (pages, 2, 64 * 72) if kv == "nvfp4" else (pages, 2, 64, 128)
+    big = [torch.empty(shape, dtype=c["kc"].dtype, device="cuda") for _ in range(2)]
+    prob = mx.make_problem(1, 70, 8, 2, 1, 64, pages, pages, False, q_dtype=torch.bfloat16, kv_dtype=kvt)
+    want = [torch.zeros_like(c["kc"]) for _ in range(2)]
+    call(dict(c, kc=want[0], vc=want[1]))
+    shift = (pages - c["pages"]) * 64
+    call(dict(c, prob=prob, kc=big[0], vc=big[1], loc=c["loc"] + shift))
+    back = [[torch.empty(70, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)] for _ in range(2)]
+    mx.load_kv(c["prob"], c["loc"], *want, *back[0])
+    mx.load_kv(prob, c["loc"] + shift, *big, *back[1])
+    torch.cuda.synchronize()
+    for x, y in zip(*back):
+        assert torch.equal(x, y) and x.abs().sum() > 0
+
+
 @pytest.mark.parametrize("q", ["bf16", "fp16"])
 def test_load_of_what_the_store_wrote(q):
     """A 16-bit row, stored in e4m3 and read back, is its cast."""

@@ -310,6 +310,46 @@ def test_large_scores_raise_the_running_maximum():
     c.run().check()
 
 
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches(seed):
+    r = np.random.RandomState(seed)
+    hq, hkv = [(8, 1), (16, 2), (12, 4), (4, 4), (128, 1), (10, 2), (64, 8), (96, 1)][r.randint(8)]
+    causal = bool(r.randint(2))
+
+    def members(n, lo):
+        return [(int(r.choice([0, 1, 1, 1, 2, r.randint(1, 70)])), int(r.choice([lo, lo + r.randint(0, 900)])))
+                for _ in range(n)]
+
+    groups = [(int(r.choice([0, 1, 127, 128, 129, r.randint(1, 5000)])), members(r.randint(1, 30), 0))
+              for _ in range(r.randint(0, 4))]
+    groups += [(None, members(r.randint(1, 9), 1))]
+    Case(groups, hq=hq, hkv=hkv, q=["bf16", "fp16"][r.randint(2)], ps=[64, 128][r.randint(2)], causal=causal, seed=seed,
+         lead=int(r.randint(3)), tail=int(r.randint(3))).run().check()
+
+
+@pytest.mark.parametrize("ps", [64, 128])
+def test_long_columns(ps):
+    """Tiles of more blocks than a page window holds, columns that end in small tiles, both queues."""
+    Case([(100000, [(40, 37 + 300 * i) for i in range(7)]), (None, [(1, 9000), (3, 50)])], hq=16, ps=ps, seed=5).run().check()
+    Case([(None, [(1, 200000), (0, 10), (2, 513)])], hq=32, hkv=4, ps=ps, seed=6, tail=2).run().check()
+
+
+def test_pages_past_two_to_the_31_elements():
+    """A cache of 2^31 elements and more: the sequences' pages are its last ones."""
+    c = Case([(300, [(1, 90), (2, 70)])], seed=3, poison=False, hkv=2)
+    used, per = c.k.shape[0], c.k[0].numel()
+    pages = (1 << 31) // per + used + 5
+    big = [torch.empty(pages, *c.k.shape[1:], dtype=c.k.dtype, device="cuda") for _ in range(2)]
+    for b, x in zip(big, (c.k, c.v)):
+        b[pages - used:] = x
+    c.k, c.v = big
+    shift = pages - used
+    c.dt = torch.where(c.dt >= 0, c.dt + shift, c.dt)
+    c.slots = [(p + shift, o) for p, o in c.slots]
+    c.prob.num_pages = pages
+    c.run().check()
+
+
 # --------------------------------------------------- the calls of a serving step
 @pytest.mark.parametrize("kv", ["bf16", "fp8", "nvfp4"])
 def test_a_step_of_all_three(kv):
