@@ -255,24 +255,26 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
   pdl_wait();
 
   int bad = 0;  // status bits
-  for (int i = tid; i <= B; i += kHPlanThreads) {
+  for (int i = tid; i <= B; i += kHPlanThreads) {  // (NG <= B; no groups: the pointers may be null)
+    // everything is on its way before anything is looked at
     const long long v = a.cu[i], nx = i < B ? a.cu[i + 1] : a.total_q;
+    const int L = i < B ? a.lens[i] : 0;
+    const int gv = NG > 0 && i <= NG ? a.group_ptr[i] : 0, gn = i < NG ? a.group_ptr[i + 1] : B;
+    const int want = i < NG ? a.prefix_lens[i] : 0;
     if (v < 0 || v > nx) bad |= MXSA_FLAG_CU;
     s.cu[i] = (int)v;
-  }
-  for (int i = tid; i < B; i += kHPlanThreads) {
-    const int L = a.lens[i];
-    if (L < 0 || L > a.max_len) bad |= MXSA_FLAG_LEN;
-    s.len[i] = min(max(L, 0), a.max_len);
-    s.seq_group[i] = -1;
-  }
-  for (int i = tid; i <= NG && NG > 0; i += kHPlanThreads) {  // (no groups: the pointer may be null)
-    const int v = a.group_ptr[i], nx = i < NG ? a.group_ptr[i + 1] : B;
-    if (v < 0 || v > nx) bad |= MXSA_FLAG_GROUP;
-    s.gp[i] = v;
-    if (i < NG) {
-      s.want[i] = a.prefix_lens[i];
-      s.shortest[i] = a.max_len;
+    if (i < B) {
+      if (L < 0 || L > a.max_len) bad |= MXSA_FLAG_LEN;
+      s.len[i] = min(max(L, 0), a.max_len);
+      s.seq_group[i] = -1;
+    }
+    if (NG > 0 && i <= NG) {
+      if (gv < 0 || gv > gn) bad |= MXSA_FLAG_GROUP;
+      s.gp[i] = gv;
+      if (i < NG) {
+        s.want[i] = want;
+        s.shortest[i] = a.max_len;
+      }
     }
   }
   const bool cu_ok = !__syncthreads_or(bad & MXSA_FLAG_CU), gp_ok = !__syncthreads_or(bad & MXSA_FLAG_GROUP);
@@ -339,8 +341,8 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
   for (int q = q0; q < q1; ++q) {
     HJob& j = s.job[q];
     const int nb = j.nch;
-    const int w = j.chunk ? kHCostRows : kHCostKeys;
-    const long long whole = (share + w - 1) / w;
+    const long long whole =
+        j.chunk ? (share + kHCostRows - 1) / kHCostRows : (share + kHCostKeys - 1) / kHCostKeys;
     const int want = (int)min(whole <= kHOneChunk ? whole : (whole + kHPerCta - 1) / kHPerCta, (long long)max(nb, 1));
     if (whole <= kHOneChunk || nb < 4 * want) {  // chunks of one size, the nearest number of them
       j.nfull = j.nch = nb > 0 ? max((nb + want / 2) / want, 1) : 0;
@@ -474,9 +476,8 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
 
 // ---------------------------------------------------------------- forward
 // 384 threads: two softmax groups (warps 0-3 and 4-7; thread = TMEM lane =
-// row), a producer warp, two MMA issuers, and a warp that only makes the last
-// warpgroup whole: it gives registers to the softmax groups, whose
-// threads hold a row's 128 scores.  A tile of two halves gives each
+// row), a producer, two MMA issuers and a scheduler (a warp each; they give
+// registers to the softmax groups, whose threads hold a row's 128 scores).  A tile of two halves gives each
 // group its own 128 rows over the same blocks; a tile of one half gives both
 // groups the same rows and alternate blocks (each then makes a partial of
 // its own).  Per block: S = q k^T (TMEM), a lazily raised running maximum
@@ -490,10 +491,10 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
 // order in which the issuer takes them (K0 K1 V0 K2 V1 ... ), so 160 KB of
 // loads are in flight when the CTA waits for memory.
 constexpr int kHThreads = 384;
-constexpr int kHProducer = 8, kHMma = 9;
+constexpr int kHProducer = 8, kHMma = 9, kHSched = 11;
 constexpr uint32_t kHTileBytes = 32768;  // 128 rows x 128 x 16-bit
 constexpr int kHStages = 5;
-constexpr int kHWork = 4;
+constexpr int kHWork = 4, kHWindows = 2, kHWindow = 3;
 constexpr float kHRescale = 8.f;         // log2 units
 constexpr uint32_t kHOffKV = 2 * kHTileBytes;
 constexpr uint32_t kHOffCtrl = kHOffKV + kHStages * kHTileBytes;
@@ -506,11 +507,20 @@ constexpr int kHSoftmaxRegs = 208, kHOtherRegs = 88;
 // stage's (and a q buffer's) uses alternate between two "full" barriers: to
 // mistake a phase a role would have to be two uses ahead of the copies, and
 // each wait comes after one for a copy that was issued later than that.
+// Some blocks of a tile, from the scheduler to the producer: the pages' third
+// coordinates (two a block; -1: none).  No blocks: the end.
+struct alignas(16) HWindow {
+  int2 z[kHWindow];
+  int32_t n, first, last;  // blocks; whether they are their tile's first and last ones
+};
+
 struct HCtrl {
   uint64_t q_full[4], q_empty[2], kv_full[2 * kHStages], kv_empty[kHStages];
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2], turn[2], done;
   uint64_t work_full[kHWork], work_empty[kHWork];
-  HTile work[kHWork];  // the CTA's tiles, from the producer to the other roles; no blocks: the end
+  uint64_t win_full[kHWindows], win_empty[kHWindows];
+  HTile work[kHWork];  // the CTA's tiles, from the scheduler to the issuers and the softmax; no blocks: the end
+  HWindow win[kHWindows];
   uint32_t tmem_base;
   int32_t abort_flag, local_flags;
 };
@@ -649,7 +659,7 @@ __device__ __forceinline__ void regs_dec() {
 // O of the thread's row times f, 16 columns at a time: the caller's scores
 // keep their registers
 __device__ __forceinline__ void scale_o(uint32_t tO, float f) {
-#pragma unroll
+#pragma unroll 1
   for (int cb = 0; cb < 8; ++cb) {
     uint32_t w[16];
     tmem_ld16(tO + cb * 16, w);
@@ -658,6 +668,22 @@ __device__ __forceinline__ void scale_o(uint32_t tO, float f) {
     for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
     tmem_st16(tO + cb * 16, w);
   }
+}
+
+// S of the thread's row outside columns [lo, hi) to -infinity.  A pass of its
+// own over S, in a loop: edges are few, and unrolled beside the block's other
+// code they cost a launch 3 us of instruction fetches at its first edge.
+__device__ __forceinline__ void mask_s(uint32_t tS, int lo, int hi) {
+#pragma unroll 1
+  for (int cb = 0; cb < 128; cb += 16) {
+    uint32_t w[16];
+    tmem_ld16(tS + cb, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w[k] = cb + k >= lo && cb + k < hi ? w[k] : 0xFF800000u;
+    tmem_st16(tS + cb, w);
+  }
+  tmem_st_wait();
 }
 
 // One block of a tile whose rows stand 128 / kKeys times in the MMA's: copy
@@ -807,6 +833,10 @@ __global__ void __launch_bounds__(kHThreads, 1)
       mbar_init(&c.work_full[i], 1);
       mbar_init(&c.work_empty[i], 10);  // the issuers' and the softmax groups' warps
     }
+    for (int i = 0; i < kHWindows; ++i) {
+      mbar_init(&c.win_full[i], 1);
+      mbar_init(&c.win_empty[i], 1);
+    }
     mbar_init(&c.done, 2);
     c.abort_flag = 0;
     c.local_flags = 0;
@@ -843,25 +873,76 @@ __global__ void __launch_bounds__(kHThreads, 1)
     regs_dec<kHOtherRegs>();
     if (warp == kHProducer) {
       // -------------------------------------------------------------- producer
+      // One lane that only waits for stages and issues copies: a block takes
+      // it less than the copies take to land, so the ring stays full.
+      if (lane == 0) {
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+        const uint32_t page_bytes = 256u << a.page_shift;
+        int at = 0, st = 0, full = 0;  // ring places taken; the next one's stage and full barrier
+        uint32_t parity = 1;
+        auto load = [&](const CUtensorMap* tm, int2 z) {
+          if (!mbar_wait(&c.kv_empty[st], parity, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs)) return false;
+          uint64_t* bar = &c.kv_full[full];
+          uint8_t* dst = sm + kHOffKV + st * kHTileBytes;
+          mbar_arrive_expect_tx(bar, (uint32_t)((z.x >= 0) + (z.y >= 0)) * page_bytes);
+          if (z.x >= 0) {
+            tma_load_3d(dst, tm, bar, 0, 0, z.x);
+            tma_load_3d(dst + 16384, tm, bar, 64, 0, z.x);
+          }
+          if (z.y >= 0) {
+            tma_load_3d(dst + 8192, tm, bar, 0, 0, z.y);
+            tma_load_3d(dst + 16384 + 8192, tm, bar, 64, 0, z.y);
+          }
+          ++at;
+          if (++st == kHStages) st = 0, parity ^= 1;
+          if (++full == 2 * kHStages) full = 0;
+          return true;
+        };
+        int2 prev = make_int2(-1, -1);
+        bool ok = true;
+        for (int w = 0; ok; ++w) {
+          const int x = w % kHWindows;
+          if (!mbar_wait(&c.win_full[x], (w / kHWindows) & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs)) break;
+          const int n = c.win[x].n, first = c.win[x].first, last = c.win[x].last;
+          if (n == 0) break;
+#pragma unroll 1
+          for (int i = 0; i < n && ok; ++i) {  // K of a block, then V of the one before: the ring's order
+            const int2 z = c.win[x].z[i];
+            if (i == n - 1) mbar_arrive(&c.win_empty[x]);
+            ok = load(&tmk, z);
+            if (ok && (i > 0 || !first)) ok = load(&tmv, prev);
+            prev = z;
+          }
+          if (ok && last) ok = load(&tmv, prev);
+        }
+        // drain: the copies in flight land before the CTA may exit
+        for (int k = max(0, at - kHStages); k < at; ++k)
+          mbar_drain(&c.kv_full[k % (2 * kHStages)], (k / (2 * kHStages)) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
+      }
+      __syncwarp();
+    } else if (warp == kHSched) {
+      // ------------------------------------------------------------- scheduler
+      // Claims tiles, hands them to the other roles, looks up their pages and
+      // loads q: what waits for global memory, and would keep the producer
+      // from its copies.
       if (lane == 0) {
         tma_prefetch_desc(&tmq);
         tma_prefetch_desc(&tmq1);
-        tma_prefetch_desc(&tmk);
-        tma_prefetch_desc(&tmv);
       }
       const int ps = 1 << a.page_shift, npg = ps == 128 ? 1 : 2;
-      int at = 0, qn = 0;  // ring places taken so far
+      int qn = 0;  // q buffers filled
       bool ok = true;
       // The CTA's queue: the second kind's CTAs are spread over the grid.
       const int with1 = a.ws.hdr->ctas[1], count[2] = {a.ws.hdr->count[0], a.ws.hdr->count[1]};
       const int before1 = (int)((long long)cta * with1 / gridDim.x);
       int q = (int)((long long)(cta + 1) * with1 / gridDim.x) - before1;
-      bool other = false, end = false;  // the queue it began with is empty; both are
-      auto claim = [&]() -> int {       // lane 0: a place of queue q (none is left behind the CTAs' own: no atomic)
+      bool other = false;          // the queue it began with is empty
+      auto claim = [&]() -> int {  // lane 0: a place of queue q (none is left behind the CTAs' own: no atomic)
         return (q ? count[1] <= with1 : count[0] <= (int)gridDim.x - with1) ? INT_MAX
                                                                             : atomicAdd(&a.ws.hdr->next[q], 1);
       };
-      auto resolve = [&](int place) {   // the tile at a place of queue q, or of the other queue
+      auto resolve = [&](int place) {  // the tile at a place of queue q, or of the other queue; no blocks: none left
         place = __shfl_sync(0xffffffffu, place, 0);
         if (place >= (q ? count[1] : count[0]) && !other) {
           other = true;
@@ -869,130 +950,100 @@ __global__ void __launch_bounds__(kHThreads, 1)
           if (lane == 0) place = claim();
           place = __shfl_sync(0xffffffffu, place, 0);
         }
-        end = place >= (q ? count[1] : count[0]);
-        return end ? HTile{} : load_tile((q ? a.ws.queue[1] : a.ws.queue[0]) + place);
+        return place >= (q ? count[1] : count[0]) ? HTile{} : load_tile((q ? a.ws.queue[1] : a.ws.queue[0]) + place);
       };
-      // block i's pages come from a window of 32 blocks that the lanes hold
-      auto pages_at = [&](const HTile& t, int i, int pg) -> int {  // page pg of block i + lane, -1: none needed
-        const int b = t.blk0 + i + lane;
-        const int p0 = b * 128 + pg * 64;  // its first key
-        if (pg >= npg || i + lane >= t.nblk || p0 >= t.hi || p0 + ps <= t.lo) return -1;
-        const int phys = a.block_tables[(size_t)t.row * a.max_pages + (p0 >> a.page_shift)];
-        if (phys >= 0 && phys < a.num_pages) return phys;
-        atomicOr(fl, MXSA_FLAG_PAGE);
-        return -1;
+      // A window's pages, one to a lane: page lane % 2 of block i + lane / 2,
+      // where the window holds it and it has keys of the tile.
+      auto needed = [&](const HTile& t, int i, int n) {
+        const int k = i + (lane >> 1), p0 = (t.blk0 + k) * 128 + (lane & 1) * 64;
+        return (lane >> 1) < n && k < t.nblk && (lane & 1) < npg && p0 < t.hi && p0 + ps > t.lo;
       };
-      HTile next = resolve(q ? before1 : cta - before1);  // the first place is the CTA's own
-      int win[2] = {pages_at(next, 0, 0), pages_at(next, 0, 1)};
+      auto page_of = [&](const HTile& t, int i, int n) {
+        const int p0 = (t.blk0 + i + (lane >> 1)) * 128 + (lane & 1) * 64;
+        return needed(t, i, n) ? a.block_tables[(size_t)t.row * a.max_pages + (p0 >> a.page_shift)] : -1;
+      };
+      auto load_q = [&](const HTile& t) {
+        const int nh = t.keys ? 1 : 2;
+        for (int h = 0; h < nh && ok; ++h, ++qn) {
+          const int b = qn & 1;
+          ok = hwarp_all(
+              mbar_wait(&c.q_empty[b], ((qn >> 1) & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
+          if (!ok) break;
+          uint8_t* qd = sm + b * kHTileBytes;
+          uint64_t* full = &c.q_full[qn & 3];
+          const int t0 = t.tok0 + h * a.T, nt = min(a.T, t.ntok - h * a.T);
+          if (nt > kHSmallQ) {  // one box; rows past the tile's tokens are never used
+            if (lane == 0) {
+              mbar_arrive_expect_tx(full, (uint32_t)(G * a.T) * 256u);
+              tma_load_3d(qd, &tmq, full, 0, t.g * G, t0);
+              tma_load_3d(qd + 16384, &tmq, full, 64, t.g * G, t0);
+            }
+          } else {  // token by token, each copy of the rows
+            const int copies = max(t.keys, 1), apart = 128 / copies;
+            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(G * nt * copies) * 256u);
+            __syncwarp();
+            for (int x = lane; x < nt * copies * 2; x += 32) {
+              const int col = x & 1, cp = (x >> 1) % copies, tk = (x >> 1) / copies;
+              tma_load_3d(qd + col * 16384 + (cp * apart + tk * G) * 128, &tmq1, full, col * 64, t.g * G, t0 + tk);
+            }
+          }
+        }
+      };
+      int wn = 0;  // windows handed over
+      auto window_free = [&] {
+        ok = ok && hwarp_all(mbar_wait(&c.win_empty[wn % kHWindows], ((wn / kHWindows) & 1) ^ 1, abort_flag, fl,
+                                       MXSA_FLAG_TIMEOUT, kWaitLimitNs));
+      };
+      HTile t = resolve(q ? before1 : cta - before1);  // the first place is the CTA's own
       for (int n = 0; ok; ++n) {
+        // windows: a short one first, so that the last one gives the next
+        // tile's claim and look-ups time
+        int k = 0, size = t.nblk ? (t.nblk - 1) % kHWindow + 1 : 0;
+        int page = page_of(t, 0, size), ahead = page_of(t, size, kHWindow);  // of this window, of the next
         const int w = n % kHWork;
         ok = hwarp_all(
             mbar_wait(&c.work_empty[w], ((n / kHWork) & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
         if (!ok) break;
-        const HTile t = next;
         if (lane == 0) {
           c.work[w] = t;
           mbar_arrive(&c.work_full[w]);
         }
-        if (end) break;
-        auto load_q = [&] {
-          const int nh = t.keys ? 1 : 2;
-          for (int h = 0; h < nh && ok; ++h, ++qn) {
-            const int b = qn & 1;
-            ok = hwarp_all(
-                mbar_wait(&c.q_empty[b], ((qn >> 1) & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
-            if (!ok) break;
-            uint8_t* qd = sm + b * kHTileBytes;
-            uint64_t* full = &c.q_full[qn & 3];
-            const int t0 = t.tok0 + h * a.T, nt = min(a.T, t.ntok - h * a.T);
-            if (nt > kHSmallQ) {  // one box; rows past the tile's tokens are never used
-              if (lane == 0) {
-                mbar_arrive_expect_tx(full, (uint32_t)(G * a.T) * 256u);
-                tma_load_3d(qd, &tmq, full, 0, t.g * G, t0);
-                tma_load_3d(qd + 16384, &tmq, full, 64, t.g * G, t0);
-              }
-            } else {  // token by token, each copy of the rows
-              const int copies = max(t.keys, 1), apart = 128 / copies;
-              if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(G * nt * copies) * 256u);
-              __syncwarp();
-              for (int x = lane; x < nt * copies * 2; x += 32) {
-                const int col = x & 1, cp = (x >> 1) % copies, tk = (x >> 1) / copies;
-                tma_load_3d(qd + col * 16384 + (cp * apart + tk * G) * 128, &tmq1, full, col * 64, t.g * G, t0 + tk);
-              }
-            }
+        do {
+          window_free();
+          if (!ok) break;
+          HWindow& x = c.win[wn % kHWindows];
+          if (lane < 2 * kHWindow) {
+            const bool want = needed(t, k, size), there = page >= 0 && page < a.num_pages;
+            if (want && !there) atomicOr(fl, MXSA_FLAG_PAGE);
+            reinterpret_cast<int32_t*>(x.z)[lane] = want && there ? page * a.Hkv + t.g : -1;
           }
-        };
-        // The next tile is claimed six blocks before the end, not sooner: a
-        // claimed tile waits for this CTA.  Its record and pages are there by
-        // the time its first K can be loaded.  (In a short tile nothing waits
-        // for them before all its own loads are on their way.)
-        const int claim_at = max(t.nblk - 6, 0), resolve_at = claim_at + 2, pages_at_block = claim_at + 4;
+          if (lane == 0) {
+            x.n = size;
+            x.first = k == 0;
+            x.last = k + size >= t.nblk;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&c.win_full[wn % kHWindows]);
+          ++wn;
+          k += size;
+          page = ahead;
+          if (k + kHWindow < t.nblk) ahead = page_of(t, k + kHWindow, kHWindow);
+          // (the first keys are on their way before the q buffers are waited for)
+          if (k == size && size) load_q(t);
+          size = kHWindow;
+        } while (k < t.nblk && ok);
+        if (t.nblk == 0 || !ok) break;
+        // The next tile is claimed when the producer comes to this one's last
+        // window, not sooner: a claimed tile waits for this CTA.
+        window_free();
+        if (!ok) break;
         int place = 0;
-        int ahead[2] = {pages_at(t, 32, 0), pages_at(t, 32, 1)};  // the next window
-        int first[2] = {-1, -1};                                  // the next tile's first one
-        int prev[2] = {-1, -1};
-        for (int i = 0; i <= t.nblk && ok; ++i) {
-          // (the first K is on its way before the q buffers are waited for)
-          if (i == 1) load_q();
-          if (i == claim_at && lane == 0) place = claim();
-          if (i == resolve_at && i < t.nblk) next = resolve(place);
-          if (i == pages_at_block && i < t.nblk) {
-            first[0] = pages_at(next, 0, 0);
-            first[1] = pages_at(next, 0, 1);
-          }
-          int cur[2] = {-1, -1};
-          if (i < t.nblk) {
-            if ((i & 31) == 0 && i > 0) {
-#pragma unroll
-              for (int pg = 0; pg < 2; ++pg) {
-                win[pg] = ahead[pg];
-                ahead[pg] = pages_at(t, i + 32, pg);
-              }
-            }
-            cur[0] = __shfl_sync(0xffffffffu, win[0], i & 31);
-            cur[1] = __shfl_sync(0xffffffffu, win[1], i & 31);
-          }
-          // K of block i, then V of block i - 1: the ring's order
-#pragma unroll
-          for (int kv = 0; kv < 2 && ok; ++kv) {
-            if (kv == 0 ? i >= t.nblk : i == 0) continue;
-            const int* pg = kv == 0 ? cur : prev;
-            const int st = at % kHStages, use = at / kHStages;
-            ok = hwarp_all(mbar_wait(&c.kv_empty[st], (use & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
-            if (!ok) break;
-            ++at;
-            if (lane == 0) {
-              uint64_t* full = &c.kv_full[(at - 1) % (2 * kHStages)];
-              uint8_t* dst = sm + kHOffKV + st * kHTileBytes;
-              const int present = (pg[0] >= 0) + (pg[1] >= 0);
-              const CUtensorMap* tm = kv == 0 ? &tmk : &tmv;
-              mbar_arrive_expect_tx(full, (uint32_t)present * (uint32_t)ps * 256u);
-              for (int x = 0; x < npg; ++x) {
-                if (pg[x] < 0) continue;
-                const int z = pg[x] * a.Hkv + t.g;
-                tma_load_3d(dst + x * 8192, tm, full, 0, 0, z);
-                tma_load_3d(dst + 16384 + x * 8192, tm, full, 64, 0, z);
-              }
-            }
-          }
-          prev[0] = cur[0];
-          prev[1] = cur[1];
-        }
-        if (resolve_at >= t.nblk) next = resolve(place);
-        if (pages_at_block >= t.nblk) {
-          first[0] = pages_at(next, 0, 0);
-          first[1] = pages_at(next, 0, 1);
-        }
-        win[0] = first[0];
-        win[1] = first[1];
+        if (lane == 0) place = claim();
+        t = resolve(place);
       }
-      // drain: the copies in flight land before the CTA may exit
-      if (lane == 0) {
-        for (int k = max(0, at - kHStages); k < at; ++k)
-          mbar_drain(&c.kv_full[k % (2 * kHStages)], (k / (2 * kHStages)) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
+      if (lane == 0)  // drain
         for (int k = max(0, qn - 2); k < qn; ++k)
           mbar_drain(&c.q_full[k & 3], (k >> 2) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
-      }
       __syncwarp();
     } else if (warp == kHMma || warp == kHMma + 1) {
       // --------------------------------------------------------- MMA issuers
@@ -1196,15 +1247,11 @@ __global__ void __launch_bounds__(kHThreads, 1)
           if (lane == 0) mbar_arrive(&c.p_half[h]);
         } else if (warp_live) {
           tc_fence_after();
+          if (k0 < lo || k0 + 128 > warp_hi) mask_s(tS, lo - k0, hi - k0);
           float sv[128];
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sv + q * 32);
           tmem_ld_wait();
-          if (k0 < lo || k0 + 128 > warp_hi) {
-            const int rlo = lo - k0, rhi = hi - k0;
-#pragma unroll
-            for (int k = 0; k < 128; ++k) sv[k] = k >= rlo && k < rhi ? sv[k] : -INFINITY;
-          }
           float b0 = -INFINITY, b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 128; k += 8) {
@@ -1280,7 +1327,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN stays one)
         float* po = a.ws.part_o + pr * 128;
-#pragma unroll
+#pragma unroll 1
         for (int cb = 0; cb < 4; ++cb) {
           float ov[32];
           tmem_ld32(tO + cb * 32, ov);  // every lane: the load is warp-collective

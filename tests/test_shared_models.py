@@ -17,6 +17,7 @@ import pytest
 from tests.test_barrier_models import Bar
 
 MAXC, WR, WK, TILE, STAGES, WORK = 160, 8, 4, 10, 5, 4
+WINDOWS, WINDOW = 2, 3
 PER_CTA, SMALL, ONE_CHUNK = 2, 4, 24
 
 
@@ -200,36 +201,83 @@ def run_protocol(segs, seed):
     S, O = [None, None], [None, None]
     finished = [0, 0]
 
-    def producer():
-        at = qn = 0
+    for i in range(WINDOWS):
+        bar(f"win_full{i}")
+        bar(f"win_empty{i}")
+    win = [None] * WINDOWS
+
+    def scheduler():
+        wn = qn = 0
         for k, tile in enumerate(segs + [None]):
             yield ("wait", B[f"work_empty{k % WORK}"], ((k // WORK) & 1) ^ 1)
             work[k % WORK] = (k, tile)
             B[f"work_full{k % WORK}"].arrive()
+            n, keys = tile[:2] if tile else (0, 0)
+            i, size = 0, (n - 1) % WINDOW + 1 if n else 0
+            while True:
+                yield ("wait", B[f"win_empty{wn % WINDOWS}"], ((wn // WINDOWS) & 1) ^ 1)
+                win[wn % WINDOWS] = (wn, size, i == 0, i + size >= n)
+                B[f"win_full{wn % WINDOWS}"].arrive()
+                wn += 1
+                for _h in range((1 if keys else 2) if i == 0 and n else 0):
+                    b = qn & 1
+                    yield ("wait", B[f"q_empty{b}"], ((qn >> 1) & 1) ^ 1)
+                    assert qn < 2 or qreads[qn - 2] == 0, "q refilled early"
+
+                    def land(b=b, qn=qn):
+                        qbuf[b] = qn
+                        B[f"q_full{qn & 3}"].arrive()
+                    later(f"q{b}", land)
+                    qn += 1
+                i, size = i + size, WINDOW
+                if i >= n:
+                    break
             if tile is None:
                 return
-            n, keys, _ = tile
-            for x in range(2 * n):
-                if x == 1:  # the q buffers after the first K
-                    for _h in range(1 if keys else 2):
-                        b = qn & 1
-                        yield ("wait", B[f"q_empty{b}"], ((qn >> 1) & 1) ^ 1)
-                        assert qn < 2 or qreads[qn - 2] == 0, "q refilled early"
+            yield ("wait", B[f"win_empty{wn % WINDOWS}"], ((wn // WINDOWS) & 1) ^ 1)
 
-                        def land(b=b, qn=qn):
-                            qbuf[b] = qn
-                            B[f"q_full{qn & 3}"].arrive()
-                        later(f"q{b}", land)
-                        qn += 1
-                st = at % STAGES
-                yield ("wait", B[f"kv_empty{st}"], ((at // STAGES) & 1) ^ 1)
-                assert at < STAGES or reads[at - STAGES] == 0, "stage refilled early"
+    def producer():
+        at = w = 0
+        order = [(k, x) for k, (n, _, _) in enumerate(segs) for x in range(2 * n)]
+        block = 0  # of the windows so far
 
-                def land(st=st, at=at):
-                    stage[st] = at
-                    B[f"kv_full{at % (2 * STAGES)}"].arrive()
-                later(f"kv{st}", land)
-                at += 1
+        def load(kv):
+            nonlocal at
+            st = at % STAGES
+            yield ("wait", B[f"kv_empty{st}"], ((at // STAGES) & 1) ^ 1)
+            assert at < STAGES or reads[at - STAGES] == 0, "stage refilled early"
+            k, x = order[at]
+            n, b = segs[k][0], block - sum(t[0] for t in segs[:k])
+            assert x == (place_k(b) if kv == "k" else place_v(b, n)), "another block's place"
+
+            def land(st=st, at=at):
+                stage[st] = at
+                B[f"kv_full{at % (2 * STAGES)}"].arrive()
+            later(f"kv{st}", land)
+            at += 1
+
+        while True:
+            yield ("wait", B[f"win_full{w % WINDOWS}"], (w // WINDOWS) & 1)
+            num, n, first, last = win[w % WINDOWS]
+            assert num == w, "another window"
+            if n == 0:
+                assert at == len(order)
+                return
+            for i in range(n):
+                if i == n - 1:
+                    win[w % WINDOWS] = None
+                    B[f"win_empty{w % WINDOWS}"].arrive()
+                yield from load("k")
+                if i or not first:
+                    block -= 1
+                    yield from load("v")
+                    block += 1
+                block += 1
+            if last:
+                block -= 1
+                yield from load("v")
+                block += 1
+            w += 1
 
     def issuer(h):
         at = qn = npv = no = 0
@@ -382,7 +430,7 @@ def run_protocol(segs, seed):
             qreads[qn + x] = n
         at += 2 * n
         qn += 1 if keys else 2
-    roles = {"p": producer(), "m0": issuer(0), "m1": issuer(1), "s0": softmax(0), "s1": softmax(1)}
+    roles = {"c": scheduler(), "p": producer(), "m0": issuer(0), "m1": issuer(1), "s0": softmax(0), "s1": softmax(1)}
     blocked = dict.fromkeys(roles)
     while roles or any(pending.values()):
         ready = [k for k in roles if blocked[k] is None or blocked[k][1].ready(blocked[k][2])]
@@ -403,6 +451,6 @@ def run_protocol(segs, seed):
 def test_forward_protocol(seed):
     r = random.Random(seed)
     for x in range(8):
-        segs = [(r.choice([1, 1, 2, 3, r.randint(1, 9)]), r.choice([0, 0, 1, 4, 4]), r.random() < 0.5)
+        segs = [(r.choice([1, 1, 2, 3, r.randint(1, 9), r.randint(8, 26)]), r.choice([0, 0, 1, 4, 4]), r.random() < 0.5)
                 for _ in range(r.randint(1, 7))]
-        run_protocol(segs, seed * 100 + x)
+        run_protocol([(1, 0, True), (1, 2, True), (1, 4, True)] + segs, seed * 100 + x)  # (the tiles before the plan)
