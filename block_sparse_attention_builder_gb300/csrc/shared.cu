@@ -476,20 +476,31 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
 
 // ---------------------------------------------------------------- forward
 // 384 threads: two softmax groups (warps 0-3 and 4-7; thread = TMEM lane =
-// row), a producer, two MMA issuers and a scheduler (a warp each; they give
-// registers to the softmax groups, whose threads hold a row's 128 scores).  A tile of two halves gives each
-// group its own 128 rows over the same blocks; a tile of one half gives both
-// groups the same rows and alternate blocks (each then makes a partial of
-// its own).  Per block: S = q k^T (TMEM), a lazily raised running maximum
-// (raised when a score passes it by 2^8, O in TMEM is then rescaled),
-// P = exp2(S - m) rounded to the 16-bit type over S, l += sum P, O += P V.
-// Each group has an issuer: P V of a block, then q k^T of the group's next
-// one, so that while one group runs its softmax the tensor pipe has the
-// other's two products.  S is overwritten by the MMA after the one that reads
-// P from it; both are issued by one thread, which the pipe keeps in
+// row), a producer, two MMA issuers and a scheduler (a warp each).  A tile of
+// two halves gives each group its own 128 rows over the same blocks; a tile of
+// one half gives both groups the same rows and alternate blocks (each then
+// makes a partial of its own).  Per block: S = q k^T (TMEM), a lazily raised
+// running maximum (raised when a score passes it by 2^8, O in TMEM is then
+// rescaled), P = exp2(S - m) rounded to the 16-bit type over S, l += sum P,
+// O += P V.  Each group has an issuer: P V of a block, then q k^T of the
+// group's next one, so that while one group runs its softmax the tensor pipe
+// has the other's two products.  S is overwritten by the MMA after the one
+// that reads P from it; both are issued by one thread, which the pipe keeps in
 // order.  K and V blocks have a stage of 32 KB each in a ring of five, in the
 // order in which the issuer takes them (K0 K1 V0 K2 V1 ... ), so 160 KB of
-// loads are in flight when the CTA waits for memory.
+// loads are in flight when the CTA waits for memory.  What waits for global
+// memory otherwise (claims, records, pages) is the scheduler's: in the
+// producer's way it cost 1900 cycles a block of a decode tile.
+//
+// Bound.  Tiles of two halves: a group's chain of softmax (1650 cycles a
+// block: 500 for the maximum, 16 a pair of exponentials), two hand-overs
+// (250 and 300) and its products; the tensor pipe's own 2176 cycles of both
+// groups' four products are 0.7 of it.  256 decoding sequences of 64 + 8
+// heads on a shared prefix of 65536 keys and 64 to 2048 of their own (558
+// GFLOP, 1.36 GB): 515 us in all, 1.08 PFLOP/s.  Tiles of one half: memory;
+// 256 sequences with 2048 keys of their own and no prefix (2.16 GB): 351 us,
+// 6.1 TB/s.  Code that is run once or rarely is kept in loops: unrolled, its
+// first use in a launch costs 3 to 4 us of instruction fetches.
 constexpr int kHThreads = 384;
 constexpr int kHProducer = 8, kHMma = 9, kHSched = 11;
 constexpr uint32_t kHTileBytes = 32768;  // 128 rows x 128 x 16-bit
@@ -498,9 +509,6 @@ constexpr int kHWork = 4, kHWindows = 2, kHWindow = 3;
 constexpr float kHRescale = 8.f;         // log2 units
 constexpr uint32_t kHOffKV = 2 * kHTileBytes;
 constexpr uint32_t kHOffCtrl = kHOffKV + kHStages * kHTileBytes;
-// registers of a softmax thread and of the others: 256 x 208 + 128 x 88 is
-// the launch's 384 x 168
-constexpr int kHSoftmaxRegs = 208, kHOtherRegs = 88;
 
 // A role may pass over places and q slots of the other group without looking
 // at their barriers.  A parity only tells a phase from the one before, so a
@@ -646,18 +654,7 @@ __device__ __forceinline__ void mma_pv_hi(uint32_t d, uint32_t tp, uint32_t v, u
   mma_pv_step<7>(d, tp, v, idesc, 1u);
 }
 
-// a warpgroup's registers per thread, from or to the launch's pool
-template <int kRegs>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
-// O of the thread's row times f, 16 columns at a time: the caller's scores
-// keep their registers
+// O of the thread's row times f, 16 columns at a time
 __device__ __forceinline__ void scale_o(uint32_t tO, float f) {
 #pragma unroll 1
   for (int cb = 0; cb < 8; ++cb) {
@@ -870,7 +867,6 @@ __global__ void __launch_bounds__(kHThreads, 1)
   };
 
   if (warp >= 8) {
-    regs_dec<kHOtherRegs>();
     if (warp == kHProducer) {
       // -------------------------------------------------------------- producer
       // One lane that only waits for stages and issues copies: a block takes
@@ -1184,7 +1180,6 @@ __global__ void __launch_bounds__(kHThreads, 1)
       __syncwarp();
     }
   } else {
-    regs_inc<kHSoftmaxRegs>();
     // --------------------------------------------------------------- softmax
     const int h = warp >> 2;
     const int r = tid & 127;  // row of the half == TMEM lane
@@ -1194,8 +1189,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
     bool ok = true;
     HTile t;
     while (ok && next_tile(&t)) {
-      // (what the block loop and the epilogue need of the tile, and no more: a
-      // row's 128 scores leave few registers)
+      // (what the block loop and the epilogue need of the tile, and no more)
       const int n = t.nblk, b0 = t.blk0, lo = t.lo, key_end = t.hi, keys = t.keys, stride = keys ? 2 : 1;
       // the group that takes a one-half tile's first block changes with the q
       // buffer, so that short tiles keep both groups busy
@@ -1248,17 +1242,24 @@ __global__ void __launch_bounds__(kHThreads, 1)
         } else if (warp_live) {
           tc_fence_after();
           if (k0 < lo || k0 + 128 > warp_hi) mask_s(tS, lo - k0, hi - k0);
-          float sv[128];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sv + q * 32);
-          tmem_ld_wait();
+          // S 64 keys at a time, twice: the second ones and the first ones for
+          // the maximum, then again the second ones for their exponentials.
+          // A row's 128 scores at once would need registers that the other
+          // warps then lack.
+          float sv[64];
           float b0 = -INFINITY, b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 128; k += 8) {
-            b0 = hmax3(b0, sv[k], sv[k + 1]);
-            b1 = hmax3(b1, sv[k + 2], sv[k + 3]);
-            b2 = hmax3(b2, sv[k + 4], sv[k + 5]);
-            b3 = hmax3(b3, sv[k + 6], sv[k + 7]);
+          for (int hf = 1; hf >= 0; --hf) {
+            tmem_ld32(tS + 64 * hf, sv);
+            tmem_ld32(tS + 64 * hf + 32, sv + 32);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 64; k += 8) {
+              b0 = hmax3(b0, sv[k], sv[k + 1]);
+              b1 = hmax3(b1, sv[k + 2], sv[k + 3]);
+              b2 = hmax3(b2, sv[k + 4], sv[k + 5]);
+              b3 = hmax3(b3, sv[k + 6], sv[k + 7]);
+            }
           }
           const float bm = fmaxf(fmaxf(b0, b1), fmaxf(b2, b3)) * a.scale_log2;
           const bool raise = live && (bm > m + kHRescale || (m == -INFINITY && bm > -INFINITY));
@@ -1277,23 +1278,32 @@ __global__ void __launch_bounds__(kHThreads, 1)
           const float mm = m == -INFINITY ? 0.f : m;
           const uint64_t scale2 = pack_f2(a.scale_log2, a.scale_log2), off2 = pack_f2(-mm, -mm);
           uint64_t l0 = pack_f2(0.f, 0.f), l1 = l0;
+          // (a loop: its code is fetched once for both halves; unrolled over
+          // 128 keys the warps stood without instructions, 275 us against 253
+          // with 2048 rows per kv head on 32768 keys)
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t pk[16];
+            for (int q = 0; q < 2; ++q) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 x = unpack_f2(fma_f2(pack_f2(sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]), scale2, off2));
-              const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-              if (k & 1) l1 = add_f2(l1, pack_f2(p0, p1));
-              else l0 = add_f2(l0, pack_f2(p0, p1));
-              pk[k] = hpack2<kBf16>(p0, p1);
+              for (int k = 0; k < 16; ++k) {
+                const float2 x = unpack_f2(fma_f2(pack_f2(sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]), scale2, off2));
+                const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
+                if (k & 1) l1 = add_f2(l1, pack_f2(p0, p1));
+                else l0 = add_f2(l0, pack_f2(p0, p1));
+                pk[k] = hpack2<kBf16>(p0, p1);
+              }
+              tmem_st16(tS + 32 * hf + 16 * q, pk);
             }
-            tmem_st16(tS + 16 * q, pk);
-            if (q == 1) {  // the first 64 keys: their half of P V may start
+            if (hf == 0) {  // the first 64 keys: their half of P V may start
               tmem_st_wait();
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&c.p_half[h]);
+              tmem_ld32(tS + 64, sv);
+              tmem_ld32(tS + 96, sv + 32);
+              tmem_ld_wait();
             }
           }
           const float2 ls = unpack_f2(add_f2(l0, l1));
