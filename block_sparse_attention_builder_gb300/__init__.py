@@ -4,8 +4,10 @@ Argument marshalling only -- every step runs in the library's CUDA kernels;
 PyTorch provides device memory and streams.  The entry points mirror the C
 ABI in include/mxsa.h (build_index, schedule, plan, kvouter_fwd, combine,
 read_status, store_kv, the paged-cache store that writes new tokens' K/V
-and index keys into the caches, and select_blocks, the top-k block
-selection over those index keys), plus ``kvouter_attention`` with the
+and index keys into the caches, load_kv, its read side, norm_rope_store,
+the store behind a layer's norms and rotation, select_blocks, the top-k
+block selection over those index keys, dense_fwd and dense_shared_fwd, the
+dense attention of a batch that may share prefixes), plus ``kvouter_attention`` with the
 call shape of the fw-ai/minimax-kernels README's Quick start and
 ``SparseAttention`` which keeps the workspaces of one problem shape for
 repeated calls.

@@ -108,4 +108,38 @@ __device__ __forceinline__ uint32_t nvfp4_code(float x, float sd) {
   return (sd == 0.f || isnan(x)) ? 0u : e2m1_code(__fdiv_rn(x, sd));
 }
 
+// y, which has x's sign or is a zero, with x's sign
+__device__ __forceinline__ float with_sign(float y, float x) {
+  return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));
+}
+
+// codes of eight elements of a group under the scale value sd, the first in
+// the low bits.  Quotients by the reciprocal and one residual step, correctly
+// rounded for a correctly rounded reciprocal (Markstein 1990, theorem 8), so
+// the same as nvfp4_code's but for the sign of a zero, which is x's; a quotient
+// too small for an exact residual has code 0 either way.  Groups with infinities or NaN, and a scale of
+// 0, take nvfp4_code.
+__device__ __forceinline__ uint32_t nvfp4_codes8(const float* x, float sd) {
+  const float s = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+  uint32_t codes = 0;
+  if (sd != 0.f && fabsf(s) < INFINITY) {
+    const float r = __frcp_rn(sd);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float q0 = x[i] * r, q1 = x[i + 1] * r;
+      const float y0 = with_sign(fmaf(fmaf(-q0, sd, x[i]), r, q0), x[i]);
+      const float y1 = with_sign(fmaf(fmaf(-q1, sd, x[i + 1]), r, q1), x[i + 1]);
+      uint32_t c;
+      asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}"
+          : "=r"(c)
+          : "f"(y1), "f"(y0));
+      codes |= c << (4 * i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) codes |= nvfp4_code(x[i], sd) << (4 * i);
+  }
+  return codes;
+}
+
 }  // namespace mxsa

@@ -7,7 +7,9 @@
 // Bound: HBM, the cached rows once and the 16-bit rows once.  One thread
 // makes 16 output bytes (8 values) of K and the same 8 of V, and the index
 // keys' chunks follow, as in the store: consecutive threads read and write
-// consecutive bytes, and the slot is looked up once for both.
+// consecutive bytes, and the slot is looked up once for both.  36864 tokens
+// of 8 heads, e4m3 (227 MB): 37.5 us, 6.0 TB/s; 30011 of 4 heads, NVFP4 (79
+// MB): 16.3 us, 4.8 TB/s with the launch.
 #include <algorithm>
 #include <climits>
 

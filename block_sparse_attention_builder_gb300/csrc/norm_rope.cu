@@ -26,7 +26,9 @@
 // 386 us with sixteen consecutive bytes to a lane and the partner's bytes by
 // shuffle, each value normed twice; 324 us with a lane's pieces as above (runs
 // of a token's rows with the next rows prefetched: 340 us); 240 us, 5.7 TB/s,
-// now.  2 or 8 rows at a time: 294 and 332 us.
+// now.  2 or 8 rows at a time: 294 and 332 us.  FP8 cache 257 us (193 us at
+// the copy rate), NVFP4 341 us (189 us; its casts are 100 us of it: 452 us
+// with a division and the comparisons for each value).
 #include <algorithm>
 #include <climits>
 
@@ -268,9 +270,7 @@ __global__ void __launch_bounds__(kRopeThreads, kKind == kKindFp4 ? 4 : 5) k_nor
       amax = fmaxf(amax, __shfl_xor_sync(hmask, amax, 1));
       float sd;
       const uint32_t sc = nvfp4_scale(amax, &sd);
-      uint32_t codes = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) codes |= nvfp4_code(x[i], sd) << (4 * i);
+      const uint32_t codes = nvfp4_codes8(x, sd);
       if (u < left) {
         *reinterpret_cast<uint32_t*>(to + off * 64 + (ea >> 1)) = codes;
         if (!(lane & 1)) to[(64LL << a.page_shift) + off * 8 + (ea >> 4)] = (uint8_t)sc;

@@ -108,14 +108,7 @@ __device__ __forceinline__ void put_group_fp4(const uint16_t* src, uint8_t* code
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));  // fmaxf drops a NaN operand
   float sd;
   const uint32_t sc = nvfp4_scale(amax, &sd);
-  uint32_t lo = 0, hi = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t c = nvfp4_code(x[i], sd);
-    if (i < 8) lo |= c << (4 * i);
-    else hi |= c << (4 * (i - 8));
-  }
-  *reinterpret_cast<uint2*>(codes) = make_uint2(lo, hi);
+  *reinterpret_cast<uint2*>(codes) = make_uint2(nvfp4_codes8(x, sd), nvfp4_codes8(x + 8, sd));
   *scale = (uint8_t)sc;
 }
 

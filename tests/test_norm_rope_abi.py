@@ -2,6 +2,7 @@
 C ABI and in the binding (no GPU)."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -165,3 +166,26 @@ def test_dense_shared_arguments(lib):
         with pytest.raises(mx.MxsaError) as ei:
             mx.dense_shared_fwd(p, **dict(good, **kw))
         assert ei.value.status == 1
+
+
+def test_quotient_by_a_residual_step_is_the_division():
+    """The NVFP4 casts' x / scale: q = x r, then q + (x - q s) r, r the rounded reciprocal; every E4M3 scale, values at
+    and next to the ties of E2M1 and anywhere."""
+    e = np.arange(1, 127)
+    s = np.where(e < 8, e * 2.0 ** -9, (8 + e % 8) * 2.0 ** (e // 8 - 10.0)).astype(np.float32)[:, None]
+    ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, 6], np.float32)
+    near = [s * ties]
+    for _ in range(3):
+        near.append(np.nextafter(near[-1], np.float32(np.inf)))
+    low = s * ties
+    for _ in range(3):
+        low = np.nextafter(low, np.float32(0))
+        near.append(low)
+    rand = np.random.RandomState(0).rand(len(s), 20000).astype(np.float32) * s * 8
+    x = np.concatenate(near + [rand, rand * np.float32(2.0 ** -100)], 1)
+    L = np.longdouble
+    r = np.float32(1) / s
+    q = x * r
+    rest = (L(x) - L(q) * L(s)).astype(np.float32)  # exact: one fused step
+    y = (L(q) + L(rest) * L(r)).astype(np.float32)
+    assert (y == x / s).all()
