@@ -20,7 +20,7 @@
 // of the work fixed beforehand, tiles cut where a share ended: the slowest
 // CTAs took 540 us where the median took 490 us.)  A queue's tiles are in row
 // tile order within a chunk, so the CTAs that run at the same time read the
-// same keys and meet in L2.  A chunk is a quarter of a CTA's share of all
+// same keys and meet in L2.  A chunk is half of a CTA's share of all
 // work, which bounds the partial buffer by the shapes alone.
 //
 // Three launches: k_shared_plan (one CTA: jobs, tiles, queues), k_shared
@@ -49,10 +49,10 @@ constexpr int kHMaxCtas = 160;     // workspaces are sized for this many
 // CTAs begin with which queue.
 constexpr int kHCostRows = 8, kHCostKeys = 4, kHCostTile = 10;
 constexpr int kHCostRatio = (kHCostRows + kHCostKeys - 1) / kHCostKeys;
-// A CTA's share of all work is kHPerCta chunks; the end of a long column (four
-// chunks and more) is cut kHSmall times as fine, and these small tiles come
-// last in their queue.  A share of at most kHOneChunk blocks is one chunk.
-constexpr int kHPerCta = 2, kHSmall = 4, kHOneChunk = 24;
+// A CTA's share of all work is kHPerCta chunks (3, or a column's end cut finer
+// so that the CTAs end together: more partial rows, and slower); a share of at
+// most kHOneChunk blocks is one.
+constexpr int kHPerCta = 2, kHOneChunk = 24;
 
 // One tile: keys [128 blk0, 128 (blk0 + nblk)) of [lo, hi) for ntok tokens.
 struct alignas(16) HTile {
@@ -74,7 +74,6 @@ struct HJob {
   int32_t tok0, ntok, row, lo, hi;
   int32_t tile0;                   // first tile
   int32_t nch, chunk, nrt;         // chunks, blocks of one, row tiles
-  int32_t nfull, small;            // chunks of `chunk` blocks, and the blocks of the others
 };
 
 // A token: its sequence (-1: none), the keys it sees, and the tiles of its
@@ -114,11 +113,11 @@ HLayout shared_layout(const mxsa_problem& p) {
   const long long triples = p.num_kv_heads * (2 * (p.total_q / (2 * T)) + 2LL * p.num_seqs);
   // Chunks beyond the first.  A job's chunk is at least 1 / kHPerCta of a
   // CTA's share of the whole cost, in blocks of two halves' cost where the
-  // job has such tiles; a tile of one half then costs kHCostRatio less.  With
-  // small tiles a column of x >= 4 chunks has at most x + 2 kHSmall - 1, without
-  // x + 1/2.  And no more than there are blocks.  A kv head has its share.
+  // job has such tiles; a tile of one half then costs kHCostRatio less.  A
+  // column of x chunks is cut into at most x + 1/2 and no more than there are
+  // blocks.  A kv head has its share.
   const long long blocks = max_blocks_per_seq(p);
-  const long long by_cost = (long long)kHPerCta * kHCostRatio * kHMaxCtas * (4 + 2 * kHSmall - 1) / 4;
+  const long long by_cost = (long long)kHPerCta * kHCostRatio * kHMaxCtas;
   const long long extra = std::min(by_cost, triples * (blocks - 1));
   HLayout L;
   L.tile_cap = triples + extra;
@@ -191,7 +190,7 @@ struct HPlanSmem {
   int32_t gp[kHMaxSeqs + 1], want[kHMaxSeqs], shortest[kHMaxSeqs];
   int32_t tile0[2 * kHMaxSeqs];
   HJob job[2 * kHMaxSeqs];
-  long long scan[6][kHPlanThreads / 32];
+  long long scan[5][kHPlanThreads / 32];
 };
 
 // Exclusive sums over the block of kN values at once; total gets the wholes.
@@ -344,16 +343,8 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     const long long whole =
         j.chunk ? (share + kHCostRows - 1) / kHCostRows : (share + kHCostKeys - 1) / kHCostKeys;
     const int want = (int)min(whole <= kHOneChunk ? whole : (whole + kHPerCta - 1) / kHPerCta, (long long)max(nb, 1));
-    if (whole <= kHOneChunk || nb < 4 * want) {  // chunks of one size, the nearest number of them
-      j.nfull = j.nch = nb > 0 ? max((nb + want / 2) / want, 1) : 0;
-      j.chunk = nb > 0 ? (nb + j.nch - 1) / j.nch : 1;
-      j.small = 1;
-    } else {
-      j.chunk = want;
-      j.nfull = nb / want - 1;
-      j.small = (want + kHSmall - 1) / kHSmall;
-      j.nch = j.nfull + (nb - j.nfull * want + j.small - 1) / j.small;
-    }
+    j.nch = nb > 0 ? max((nb + want / 2) / want, 1) : 0;  // of one size, the nearest number of them
+    j.chunk = nb > 0 ? (nb + j.nch - 1) / j.nch : 1;
     tiles[0] += (long long)a.Hkv * j.nch * j.nrt;
   }
   block_scan<1>(tiles, s.scan[2], all);
@@ -396,28 +387,23 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     int end = (j.hi + 127) >> 7;
     if (a.causal && c.q >= NG)  // keys past the last token's position are nobody's
       end = min(end, (max(j.hi - j.ntok + c.rt * T2 + *ntok, 0) + 127) >> 7);
-    const int fine = max(c.ch - j.nfull, 0);
-    *blk0 = (j.lo >> 7) + (c.ch - fine) * j.chunk + fine * j.small;
-    *nblk = max(min(*blk0 + (c.ch < j.nfull ? j.chunk : j.small), end) - *blk0, 0);
+    *blk0 = (j.lo >> 7) + c.ch * j.chunk;
+    *nblk = max(min(*blk0 + j.chunk, end) - *blk0, 0);
   };
-  // tiles of each queue (in one word; full and small ones) and partial rows
-  // before the thread's own
-  long long sums[3] = {0, 0, 0}, wholes[3];  // full, small, rows
+  // tiles of each queue (in one word) and partial rows before the thread's own
+  long long sums[2] = {0, 0}, wholes[2];
   int blk0, nblk, ntok;
   HCursor c = c0;
   for (int i = i0; i < i1; ++i, advance(&c)) {
     size_of(c, &blk0, &nblk, &ntok);
     const bool keys = ntok <= a.T;
     if (nblk) {
-      const long long one = keys ? 1LL << 32 : 1LL;
-      if (c.ch < s.job[c.q].nfull) sums[0] += one;
-      else sums[1] += one;
-      sums[2] += ntok * a.G * (keys ? 2 : 1);
+      sums[0] += keys ? 1LL << 32 : 1LL;
+      sums[1] += ntok * a.G * (keys ? 2 : 1);
     }
   }
-  block_scan<3>(sums, s.scan[3], wholes);
-  long long full = sums[0], small = sums[1] + wholes[0];  // (behind the queue's full ones)
-  long long part = sums[2];
+  block_scan<2>(sums, s.scan[3], wholes);
+  long long place = sums[0], part = sums[1];
   c = c0;
   for (int i = i0; i < i1; ++i, advance(&c)) {
     size_of(c, &blk0, &nblk, &ntok);
@@ -438,7 +424,6 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     a.ws.pieces[i] = HPieces{(int)part, t.tok0, ntok, keys ? min(nblk, 2) : min(nblk, 1)};  // (rows fit 32 bits)
     if (nblk) {
       part += ntok * a.G * (keys ? 2 : 1);
-      long long& place = c.ch < j.nfull ? full : small;
       a.ws.queue[keys][keys ? place >> 32 : (int)place] = t;
       place += keys ? 1LL << 32 : 1LL;
     }
@@ -465,10 +450,9 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     a.ws.tok[i] = v;
   }
   if (tid == 0) {
-    const long long all_queued = wholes[0] + wholes[1];
-    const int n0 = (int)all_queued, n1 = (int)(all_queued >> 32);
-    // (half of the share: the second kind's smaller tiles fill up the end)
-    int with1 = (int)(total[1] * a.ctas / 2 / max(total[0] + total[1], 1LL));
+    const int n0 = (int)wholes[0], n1 = (int)(wholes[0] >> 32);
+    // (5/8 of the share: the second kind's smaller tiles fill up the end)
+    int with1 = (int)(total[1] * a.ctas * 5 / 8 / max(total[0] + total[1], 1LL));
     with1 = n1 == 0 ? 0 : (n0 == 0 ? a.ctas : min(max(with1, 1), a.ctas - 1));
     *a.ws.hdr = HHeader{{n0, n1}, {a.ctas - with1, with1}, {a.ctas - with1, with1}};
   }

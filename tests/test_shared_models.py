@@ -18,7 +18,7 @@ from tests.test_barrier_models import Bar
 
 MAXC, WR, WK, TILE, STAGES, WORK = 160, 8, 4, 10, 5, 4
 WINDOWS, WINDOW = 2, 3
-PER_CTA, SMALL, ONE_CHUNK = 2, 4, 24
+PER_CTA, ONE_CHUNK = 2, 24
 
 
 def cdiv(a, b):
@@ -59,12 +59,8 @@ def plan(p):
         whole = cdiv(share, j["w"])
         nb = j["nb"]
         c = min(whole if whole <= ONE_CHUNK else cdiv(whole, PER_CTA), max(nb, 1))
-        if whole <= ONE_CHUNK or nb < 4 * c:
-            nfull = nch = max((nb + c // 2) // c, 1) if nb else 0
-            c, small = cdiv(nb, nch) if nch else 1, 1
-        else:
-            nfull, small = nb // c - 1, cdiv(c, SMALL)
-            nch = nfull + cdiv(nb - nfull * c, small)
+        nch = max((nb + c // 2) // c, 1) if nb else 0
+        c = cdiv(nb, nch) if nch else 1
         j["chunk"], j["nch"] = c, nch
         j["tile0"] = len(tiles)
         for g in range(p["hkv"]):
@@ -74,10 +70,9 @@ def plan(p):
                     end = cdiv(j["hi"], 128)
                     if p["causal"] and j["own"]:
                         end = min(end, cdiv(max(j["hi"] - j["ntok"] + rt * 2 * T + ntok, 0), 128))
-                    fine = max(ch - nfull, 0)
-                    b0 = j["lo"] // 128 + (ch - fine) * c + fine * small
+                    b0 = j["lo"] // 128 + ch * c
                     tiles.append(dict(tok0=j["tok0"] + rt * 2 * T, ntok=ntok, g=g, lo=j["lo"], hi=j["hi"], b0=b0,
-                                      n=max(min(b0 + (c if ch < nfull else small), end) - b0, 0), keys=ntok <= T, job=j))
+                                      n=max(min(b0 + c, end) - b0, 0), keys=ntok <= T, job=j))
     part = 0
     for t in tiles:
         t["part0"] = part
@@ -110,7 +105,7 @@ def test_plan_covers_every_key_once_within_its_bounds(seed):
     tiles, part = plan(p)
     triples = p["hkv"] * (2 * (p["total_q"] // (2 * T)) + 2 * B)
     blocks = max(1, cdiv(max(p["lens"]), 128))
-    by_cost = PER_CTA * 2 * MAXC * (4 + 2 * SMALL - 1) // 4
+    by_cost = PER_CTA * 2 * MAXC
     extra = min(by_cost, triples * (blocks - 1))
     assert len(tiles) <= triples + extra
     assert part <= 4 * p["total_q"] * p["hq"] + min(256, 2 * p["total_q"] * G) * extra
