@@ -20,11 +20,13 @@
 // of the work fixed beforehand, tiles cut where a share ended: the slowest
 // CTAs took 540 us where the median took 490 us.)  A queue's tiles are in row
 // tile order within a chunk, so the CTAs that run at the same time read the
-// same keys and meet in L2.  A chunk is half of a CTA's share of all
-// work, which bounds the partial buffer by the shapes alone.
+// same keys and meet in L2.  A chunk is half of a CTA's share of all work,
+// which bounds the partial buffer by the shapes alone.
 //
 // Three launches: k_shared_plan (one CTA: jobs, tiles, queues), k_shared
-// (persistent, one CTA per SM) and k_shared_join.
+// (persistent, one CTA per SM) and k_shared_join.  64 decoding sequences of
+// 64 + 8 heads on a prefix of 32768 keys and 128 to 2048 of their own: 7, 84
+// and 8 us, 109 us in all.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -481,8 +483,8 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
 // (250 and 300) and its products; the tensor pipe's own 2176 cycles of both
 // groups' four products are 0.7 of it.  256 decoding sequences of 64 + 8
 // heads on a shared prefix of 65536 keys and 64 to 2048 of their own (558
-// GFLOP, 1.36 GB): 515 us in all, 1.08 PFLOP/s.  Tiles of one half: memory;
-// 256 sequences with 2048 keys of their own and no prefix (2.16 GB): 351 us,
+// GFLOP, 1.36 GB): 515 to 535 us in all, 1.06 PFLOP/s.  Tiles of one half: memory;
+// 256 sequences with 2048 keys of their own and no prefix (2.16 GB): 354 us,
 // 6.1 TB/s.  Code that is run once or rarely is kept in loops: unrolled, its
 // first use in a launch costs 3 to 4 us of instruction fetches.
 constexpr int kHThreads = 384;
