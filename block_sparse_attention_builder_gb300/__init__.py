@@ -175,6 +175,23 @@ def _need(what: str, name: str, t: Optional[torch.Tensor], nbytes: int):
     raise MxsaError(1, f"{what}: {name} holds {t.nbytes} bytes, the problem needs {nbytes}")
 
 
+_I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
+_ROW_TYPE = {BF16: torch.bfloat16, FP16: torch.float16, FP8_E4M3: torch.float8_e4m3fn, NVFP4: torch.uint8}
+
+
+def _refuse_types(what: str, rows, exact):
+    """Refuses tensors of a type that the kernels would read wrongly.  rows:
+    (name, tensor, row type), in that type or as raw integers; exact: (name,
+    tensor, dtype).  Tensors may be None.  (Called when something is not of
+    the plain type: the callers' own comparisons cost a call a third of it.)"""
+    for name, t, dtype in rows:
+        if t is not None and t.dtype.is_floating_point and t.dtype is not dtype:
+            raise MxsaError(1, f"{what}: {name} is {t.dtype}, the problem's rows are {dtype}")
+    for name, t, dtype in exact:
+        if t is not None and t.dtype is not dtype:
+            raise MxsaError(1, f"{what}: {name} is {t.dtype}, not {dtype}")
+
+
 def _need_attention(what: str, prob: Problem, q=None, k_cache=None, v_cache=None, block_tables=None,
                     cu_seqlens_q=None, used_kv_lens=None, sel=None, out=None, lse=None):
     qb, kb = _ELEM_BYTES.get(prob.q_dtype, 2), _ELEM_BYTES.get(prob.kv_dtype, 2)
@@ -324,6 +341,15 @@ def dense_shared_fwd(prob, q, k_cache, v_cache, block_tables, cu_seqlens_q, used
     _need(what, "prefix_lens", prefix_lens, ng * 4)
     _need(what, "ws", ws, 0)
     _need(what, "flags", flags, 4)
+    qt, kt = _ROW_TYPE.get(prob.q_dtype), _ROW_TYPE.get(prob.kv_dtype)
+    if not (q.dtype is qt and k_cache.dtype is kt and v_cache.dtype is kt and out.dtype is qt and
+            block_tables.dtype is _I32 and cu_seqlens_q.dtype is _I64 and used_kv_lens.dtype is _I32 and
+            (group_ptr is None or (group_ptr.dtype is _I32 and prefix_lens.dtype is _I32)) and
+            (lse is None or lse.dtype is _F32) and (flags is None or flags.dtype is _I32)):
+        _refuse_types(what, (("q", q, qt), ("k_cache", k_cache, kt), ("v_cache", v_cache, kt), ("out", out, qt)),
+                      (("block_tables", block_tables, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
+                       ("used_kv_lens", used_kv_lens, _I32), ("group_ptr", group_ptr, _I32),
+                       ("prefix_lens", prefix_lens, _I32), ("lse", lse, _F32), ("flags", flags, _I32)))
     _check(_lib.mxsa_dense_shared_fwd(ctypes.byref(prob), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                       _ptr(cu_seqlens_q), _ptr(used_kv_lens), ng, _ptr(group_ptr), _ptr(prefix_lens),
                                       _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), _ptr(lse), _ptr(flags),
@@ -371,6 +397,12 @@ def load_kv(prob, loc, k_cache, v_cache, k, v, idx_cache=None, idx_k=None, flags
     _need(what, "idx_k", idx_k, n * ih * idim * qb)
     _need(what, "idx_cache", idx_cache, max(prob.num_pages, 0) * ih * max(prob.page_size, 0) * idim * kb)
     _need(what, "flags", flags, 4)
+    qt, kt = _ROW_TYPE.get(prob.q_dtype), _ROW_TYPE.get(prob.kv_dtype)
+    if not (k.dtype is qt and v.dtype is qt and k_cache.dtype is kt and v_cache.dtype is kt and loc.dtype is _I64 and
+            idx_k is None and (flags is None or flags.dtype is _I32)):
+        _refuse_types(what, (("k", k, qt), ("v", v, qt), ("k_cache", k_cache, kt), ("v_cache", v_cache, kt),
+                             ("idx_k", idx_k, qt), ("idx_cache", idx_cache, kt)),
+                      (("loc", loc, _I64), ("flags", flags, _I32)))
     _check(_lib.mxsa_load_kv(ctypes.byref(prob), n, _ptr(loc), _ptr(k_cache), _ptr(v_cache), _ptr(k), _ptr(v),
                              _ptr(idx_cache), _ptr(idx_k), ih, idim, _ptr(flags), _stream(stream)), what)
 
@@ -447,6 +479,20 @@ def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_ca
     if idx_k_weight is not None:
         weight("idx_k_weight", idx_k_weight, hkv, idx)
     _need(what, "flags", flags, 4)
+    qt, kt = _ROW_TYPE.get(prob.q_dtype), _ROW_TYPE.get(prob.kv_dtype)
+    if not (q.dtype is qt and k.dtype is qt and v.dtype is qt and q_out.dtype is qt and k_cache.dtype is kt and
+            v_cache.dtype is kt and positions.dtype is _I64 and loc.dtype is _I64 and
+            (q_weight is None or q_weight.dtype is qt) and (k_weight is None or k_weight.dtype is qt) and
+            (flags is None or flags.dtype is _I32) and
+            (idx == 0 or (idx_q.dtype is qt and idx_k.dtype is qt and idx_q_out.dtype is kt and
+                          idx_cache.dtype is kt and (idx_q_weight is None or idx_q_weight.dtype is qt) and
+                          (idx_k_weight is None or idx_k_weight.dtype is qt)))):
+        _refuse_types(what, (("q", q, qt), ("k", k, qt), ("v", v, qt), ("q_out", q_out, qt),
+                             ("q_weight", q_weight, qt), ("k_weight", k_weight, qt), ("k_cache", k_cache, kt),
+                             ("v_cache", v_cache, kt), ("idx_q", idx_q, qt), ("idx_k", idx_k, qt),
+                             ("idx_q_weight", idx_q_weight, qt), ("idx_k_weight", idx_k_weight, qt),
+                             ("idx_q_out", idx_q_out, kt), ("idx_cache", idx_cache, kt)),
+                      (("positions", positions, _I64), ("loc", loc, _I64), ("flags", flags, _I32)))
     cfg = NormRope(q_stride, k_stride, v_stride, iq_stride, ik_stride, cos_sin.shape[0], cos_sin.shape[1],
                    bool(interleaved), bool(per_head), idx, eps)
     _check(_lib.mxsa_norm_rope_store(ctypes.byref(prob), ctypes.byref(cfg), n, _ptr(positions), _ptr(loc),
