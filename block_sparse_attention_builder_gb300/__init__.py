@@ -342,10 +342,14 @@ def dense_shared_fwd(prob, q, k_cache, v_cache, block_tables, cu_seqlens_q, used
     _need(what, "ws", ws, 0)
     _need(what, "flags", flags, 4)
     qt, kt = _ROW_TYPE.get(prob.q_dtype), _ROW_TYPE.get(prob.kv_dtype)
-    if not (q.dtype is qt and k_cache.dtype is kt and v_cache.dtype is kt and out.dtype is qt and
-            block_tables.dtype is _I32 and cu_seqlens_q.dtype is _I64 and used_kv_lens.dtype is _I32 and
-            (group_ptr is None or (group_ptr.dtype is _I32 and prefix_lens.dtype is _I32)) and
-            (lse is None or lse.dtype is _F32) and (flags is None or flags.dtype is _I32)):
+    try:
+        plain = (q.dtype is qt and k_cache.dtype is kt and v_cache.dtype is kt and out.dtype is qt and
+                 block_tables.dtype is _I32 and cu_seqlens_q.dtype is _I64 and used_kv_lens.dtype is _I32 and
+                 (group_ptr is None or (group_ptr.dtype is _I32 and prefix_lens.dtype is _I32)) and
+                 (lse is None or lse.dtype is _F32) and (flags is None or flags.dtype is _I32))
+    except AttributeError:  # a None: the library says whether it may be one
+        plain = False
+    if not plain:
         _refuse_types(what, (("q", q, qt), ("k_cache", k_cache, kt), ("v_cache", v_cache, kt), ("out", out, qt)),
                       (("block_tables", block_tables, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
                        ("used_kv_lens", used_kv_lens, _I32), ("group_ptr", group_ptr, _I32),
@@ -398,8 +402,12 @@ def load_kv(prob, loc, k_cache, v_cache, k, v, idx_cache=None, idx_k=None, flags
     _need(what, "idx_cache", idx_cache, max(prob.num_pages, 0) * ih * max(prob.page_size, 0) * idim * kb)
     _need(what, "flags", flags, 4)
     qt, kt = _ROW_TYPE.get(prob.q_dtype), _ROW_TYPE.get(prob.kv_dtype)
-    if not (k.dtype is qt and v.dtype is qt and k_cache.dtype is kt and v_cache.dtype is kt and loc.dtype is _I64 and
-            idx_k is None and (flags is None or flags.dtype is _I32)):
+    try:
+        plain = (k.dtype is qt and v.dtype is qt and k_cache.dtype is kt and v_cache.dtype is kt and
+                 loc.dtype is _I64 and idx_k is None and (flags is None or flags.dtype is _I32))
+    except AttributeError:  # a None: the library says whether it may be one
+        plain = False
+    if not plain:
         _refuse_types(what, (("k", k, qt), ("v", v, qt), ("k_cache", k_cache, kt), ("v_cache", v_cache, kt),
                              ("idx_k", idx_k, qt), ("idx_cache", idx_cache, kt)),
                       (("loc", loc, _I64), ("flags", flags, _I32)))
@@ -480,13 +488,17 @@ def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_ca
         weight("idx_k_weight", idx_k_weight, hkv, idx)
     _need(what, "flags", flags, 4)
     qt, kt = _ROW_TYPE.get(prob.q_dtype), _ROW_TYPE.get(prob.kv_dtype)
-    if not (q.dtype is qt and k.dtype is qt and v.dtype is qt and q_out.dtype is qt and k_cache.dtype is kt and
-            v_cache.dtype is kt and positions.dtype is _I64 and loc.dtype is _I64 and
-            (q_weight is None or q_weight.dtype is qt) and (k_weight is None or k_weight.dtype is qt) and
-            (flags is None or flags.dtype is _I32) and
-            (idx == 0 or (idx_q.dtype is qt and idx_k.dtype is qt and idx_q_out.dtype is kt and
-                          idx_cache.dtype is kt and (idx_q_weight is None or idx_q_weight.dtype is qt) and
-                          (idx_k_weight is None or idx_k_weight.dtype is qt)))):
+    try:
+        plain = (q.dtype is qt and k.dtype is qt and v.dtype is qt and q_out.dtype is qt and k_cache.dtype is kt and
+                 v_cache.dtype is kt and positions.dtype is _I64 and loc.dtype is _I64 and
+                 (q_weight is None or q_weight.dtype is qt) and (k_weight is None or k_weight.dtype is qt) and
+                 (flags is None or flags.dtype is _I32) and
+                 (idx == 0 or (idx_q.dtype is qt and idx_k.dtype is qt and idx_q_out.dtype is kt and
+                               idx_cache.dtype is kt and (idx_q_weight is None or idx_q_weight.dtype is qt) and
+                               (idx_k_weight is None or idx_k_weight.dtype is qt))))
+    except AttributeError:  # a None: the library says whether it may be one
+        plain = False
+    if not plain:
         _refuse_types(what, (("q", q, qt), ("k", k, qt), ("v", v, qt), ("q_out", q_out, qt),
                              ("q_weight", q_weight, qt), ("k_weight", k_weight, qt), ("k_cache", k_cache, kt),
                              ("v_cache", v_cache, kt), ("idx_q", idx_q, qt), ("idx_k", idx_k, qt),

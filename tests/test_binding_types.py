@@ -116,3 +116,19 @@ def test_norm_rope_store_and_load_kv(no_call, q, kv):
     for name in ("k_cache", "v_cache") + (() if fp4 else ("idx_cache",)):
         passes(fn, load, **{name: load[name].view(raw)})
         refused(fn, load, **{name: load[name].view(wrong)})
+
+
+def test_none_is_left_to_the_library(no_call):
+    """A missing tensor is the C entry's to refuse (or, with nothing to do, to take)."""
+    p = mx.make_problem(1, 0, 16, 2, 1, 64, 10, 10)
+    some = dict(block_tables=z(1, 10, dt=I32), cu_seqlens_q=z(2, dt=I64), used_kv_lens=z(1, dt=I32), group_ptr=None,
+                prefix_lens=None, ws=z(mx.dense_shared_workspace_size(p), dt=torch.uint8))
+    passes(mx.dense_shared_fwd, dict(prob=p, q=None, k_cache=None, v_cache=None, out=None, **some))
+    passes(mx.dense_shared_fwd, dict(some, prob=p, q=None, k_cache=None, v_cache=None, out=None, block_tables=None))
+    passes(mx.load_kv, dict(prob=p, loc=z(0, dt=I64), k_cache=None, v_cache=None, k=None, v=None))
+    row = lambda *s: z(0, *s)
+    passes(mx.norm_rope_store, dict(prob=p, positions=None, loc=z(0, dt=I64), cos_sin=torch.zeros(50, 64),
+                                    q=row(16, 128), k=row(2, 128), v=row(2, 128), q_out=None, k_cache=None,
+                                    v_cache=None))
+    with pytest.raises(mx.MxsaError):  # a wrong type beside it is still refused
+        mx.load_kv(p, z(0, dt=torch.float64), None, None, None, None)
