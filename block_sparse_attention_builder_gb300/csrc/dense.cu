@@ -569,14 +569,14 @@ cudaError_t launch_dense(const mxsa_problem& p, const void* q, const void* k_cac
   const float scale = p.softmax_scale > 0.f ? p.softmax_scale : 0.08838834764831845f;  // 1/sqrt(128)
   a.scale_log2 = scale * 1.4426950408889634f;
   const size_t smem = dense_smem_bytes();
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [smem] {
-    attr_err = cudaFuncSetAttribute(k_dense<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(k_dense<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static PerDevice limits;
+  const cudaError_t e = limits([smem] {
+    cudaError_t x = cudaFuncSetAttribute(k_dense<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (x == cudaSuccess)
+      x = cudaFuncSetAttribute(k_dense<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return x;
   });
-  if (attr_err != cudaSuccess) return attr_err;
+  if (e != cudaSuccess) return e;
   int sms = 148, dev = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -865,17 +865,17 @@ cudaError_t launch_fwd(const mxsa_problem& p, const void* q, const void* k_cache
   }
   const bool fp8 = kv_widened(p);  // FP8 or NVFP4: staged and widened
   const size_t smem = fwd_smem_bytes(fp8);
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
+  static PerDevice limits;
+  const cudaError_t e = limits([] {
     const int bytes = (int)std::max(fwd_smem_bytes(true), fwd_smem_bytes(false));
-    attr_err = cudaFuncSetAttribute(k_fwd<dec::kKv16>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(k_fwd<dec::kKvFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(k_fwd<dec::kKvFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t x = cudaFuncSetAttribute(k_fwd<dec::kKv16>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (x == cudaSuccess)
+      x = cudaFuncSetAttribute(k_fwd<dec::kKvFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (x == cudaSuccess)
+      x = cudaFuncSetAttribute(k_fwd<dec::kKvFp4>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return x;
   });
-  if (attr_err != cudaSuccess) return attr_err;
+  if (e != cudaSuccess) return e;
   FwdArgs a;
   a.q = static_cast<const uint8_t*>(q);
   a.block_tables = block_tables;

@@ -1,6 +1,7 @@
 // Internal declarations shared by the library's translation units:
 // workspace layouts, per-sequence metadata and the kernel launchers.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <utility>
@@ -211,6 +212,28 @@ inline int log2_exact(int x) {
   while ((1 << s) < x) ++s;
   return s;
 }
+
+// What belongs to a device and has to be set before a kernel's first launch
+// on it (its limit of dynamic shared memory): `set` runs at the first call on
+// each device, and again at the next call after a failure.
+class PerDevice {
+ public:
+  template <typename F>
+  cudaError_t operator()(F set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool kept = dev >= 0 && dev < kMax;
+    if (kept && done_[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = set();
+    if (e == cudaSuccess && kept) done_[dev].store(true, std::memory_order_release);
+    return e;
+  }
+
+ private:
+  static constexpr int kMax = 64;
+  std::atomic<bool> done_[kMax] = {};
+};
 
 // Launch with programmatic stream serialization: the kernel may be scheduled
 // while the previous kernel on the stream finishes; it waits for that

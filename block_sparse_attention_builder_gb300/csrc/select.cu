@@ -733,18 +733,19 @@ cudaError_t launch_select(const mxsa_problem& p, int idx_dim, const void* iq, co
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int esz = p.kv_dtype == MXSA_FP8_E4M3 ? 1 : 2;
-  static cudaError_t attr_err = [] {
-    cudaError_t e = cudaSuccess;
+  static PerDevice limits;
+  cudaError_t e = limits([] {
+    cudaError_t x = cudaSuccess;
     const void* k[6] = {(const void*)k_select_short<64, false>, (const void*)k_select_short<128, false>,
                         (const void*)k_select_short<64, true>,  (const void*)k_select_short<128, true>,
                         (const void*)k_select_long<64>,         (const void*)k_select_long<128>};
     const size_t bytes[6] = {short_smem(64, 2), short_smem(128, 2), short_smem(64, 1),
                              short_smem(128, 1), long_smem(64),     long_smem(128)};
-    for (int i = 0; i < 6 && e == cudaSuccess; ++i)
-      e = cudaFuncSetAttribute(k[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes[i]);
-    return e;
-  }();
-  if (attr_err != cudaSuccess) return attr_err;
+    for (int i = 0; i < 6 && x == cudaSuccess; ++i)
+      x = cudaFuncSetAttribute(k[i], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes[i]);
+    return x;
+  });
+  if (e != cudaSuccess) return e;
   CUtensorMap tmk;
   if (!make_idx_map(&tmk, ik, p, idx_dim)) return cudaErrorInvalidValue;
   // persistent grids: as many CTAs as fit at once (a second, partial wave
@@ -755,7 +756,7 @@ cudaError_t launch_select(const mxsa_problem& p, int idx_dim, const void* iq, co
       per_sm = 1;
     return dim3((unsigned)(sms * per_sm));
   };
-  cudaError_t e = launch_pdl(k_select_prep, dim3(1), dim3(kPrepThreads), 0, st, a);
+  e = launch_pdl(k_select_prep, dim3(1), dim3(kPrepThreads), 0, st, a);
   if (e != cudaSuccess) return e;
   const size_t ss = short_smem(idx_dim, esz), sl = long_smem(idx_dim);
   auto short_kernel = [&](auto kern) {

@@ -1524,15 +1524,15 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int ctas = std::min(sms, kHMaxCtas);
   const size_t smem = kHOffCtrl + sizeof(HCtrl) + 1024;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [smem] {
+  static PerDevice limits;
+  cudaError_t e = limits([smem] {
     const auto a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    attr_err = cudaFuncSetAttribute(k_shared<true>, a, (int)smem);
-    if (attr_err == cudaSuccess) attr_err = cudaFuncSetAttribute(k_shared<false>, a, (int)smem);
-    if (attr_err == cudaSuccess) attr_err = cudaFuncSetAttribute(k_shared_plan, a, (int)sizeof(HPlanSmem));
+    cudaError_t x = cudaFuncSetAttribute(k_shared<true>, a, (int)smem);
+    if (x == cudaSuccess) x = cudaFuncSetAttribute(k_shared<false>, a, (int)smem);
+    if (x == cudaSuccess) x = cudaFuncSetAttribute(k_shared_plan, a, (int)sizeof(HPlanSmem));
+    return x;
   });
-  if (attr_err != cudaSuccess) return attr_err;
+  if (e != cudaSuccess) return e;
 
   HPlanArgs pa{};
   pa.cu = cu;
@@ -1552,7 +1552,7 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
   pa.max_len = p.max_pages_per_seq * p.page_size;
   pa.causal = p.causal;
   pa.ctas = ctas;
-  cudaError_t e = launch_pdl(k_shared_plan, dim3(1), dim3(kHPlanThreads), sizeof(HPlanSmem), st, pa);
+  e = launch_pdl(k_shared_plan, dim3(1), dim3(kHPlanThreads), sizeof(HPlanSmem), st, pa);
   if (e != cudaSuccess) return e;
 
   HArgs fa{};
