@@ -36,7 +36,6 @@
 
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -509,20 +508,6 @@ bool dense_kv_map(CUtensorMap* m, const void* base, const mxsa_problem& p, PFN_c
          CUDA_SUCCESS;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 dense_encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
 size_t dense_smem_bytes() { return kDOffCtrl + sizeof(DCtrl) + 1024; }
 
 }  // namespace
@@ -531,7 +516,7 @@ cudaError_t launch_dense(const mxsa_problem& p, const void* q, const void* k_cac
                          const int32_t* block_tables, const int64_t* cu, const int32_t* lens, void* out, float* lse,
                          int32_t* flags, cudaStream_t st) {
   if (p.total_q == 0) return cudaSuccess;
-  auto fn = dense_encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
   const int G = p.num_q_heads / p.num_kv_heads, T = 128 / G;
   CUtensorMap tmq, tmk, tmv;

@@ -37,7 +37,6 @@
 
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -811,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // 128-byte column slab (64 x 16-bit, swizzled) or the full 128 e4m3 row.
 
 bool make_cache_map(CUtensorMap* m, const void* base, const mxsa_problem& p) {
-  auto fn = dec::encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return false;
   if (p.kv_dtype == MXSA_NVFP4) {
     // the code rows of the NVFP4 slabs [pages * Hkv][page_size * 72 bytes]:

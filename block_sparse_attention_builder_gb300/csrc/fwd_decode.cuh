@@ -31,7 +31,6 @@
 
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -813,22 +812,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& tmk, const CUtens
   __syncthreads();
 }
 
-inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 inline bool make_q_map(CUtensorMap* m, const void* q, const mxsa_problem& p, int n_rows_box) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[2] = {128, (cuuint64_t)p.total_q * p.num_q_heads};
   cuuint64_t strides[1] = {256};

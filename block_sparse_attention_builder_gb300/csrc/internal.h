@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <utility>
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include "../../include/mxsa.h"
@@ -234,6 +235,22 @@ class PerDevice {
   static constexpr int kMax = 64;
   std::atomic<bool> done_[kMax] = {};
 };
+
+// The driver's tensor map encoder; null while it cannot be found (looked up
+// again at the next call, then kept: the driver is the process's).
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> kept{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = kept.load(std::memory_order_acquire);
+  if (fn) return fn;
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  kept.store(fn, std::memory_order_release);
+  return fn;
+}
 
 // Launch with programmatic stream serialization: the kernel may be scheduled
 // while the previous kernel on the stream finishes; it waits for that

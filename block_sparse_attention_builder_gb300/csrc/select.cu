@@ -672,15 +672,7 @@ size_t select_workspace_bytes(const mxsa_problem& p) {
 // short scorer: box = one page's rows x one segment of at most 128 bytes,
 // 128-byte swizzle (64-byte for the 64-byte rows of FP8 64-dim keys).
 static bool make_idx_map(CUtensorMap* m, const void* ik, const mxsa_problem& p, int D) {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
+  const auto fn = tensor_map_encoder();
   if (!fn) return false;
   const bool fp8 = p.kv_dtype == MXSA_FP8_E4M3;
   const cuuint64_t esz = fp8 ? 1 : 2;

@@ -34,7 +34,6 @@
 
 #include <algorithm>
 #include <climits>
-#include <mutex>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -1473,20 +1472,6 @@ __global__ void __launch_bounds__(kHJoinWarps * 32) k_shared_join(HJoinArgs a) {
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 shared_encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  });
-  return fn;
-}
-
 }  // namespace
 
 size_t shared_workspace_bytes(const mxsa_problem& p) { return shared_layout(p).total; }
@@ -1499,7 +1484,7 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
                                 const int32_t* group_ptr, const int32_t* prefix_lens, void* ws, void* out, float* lse,
                                 int32_t* flags, cudaStream_t st) {
   if (p.total_q == 0) return cudaSuccess;
-  auto fn = shared_encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
   const int G = p.num_q_heads / p.num_kv_heads, T = 128 / G;
   const bool bf16 = p.q_dtype == MXSA_BF16;

@@ -22,7 +22,16 @@ def program(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("what", ["devices", "attributes"])
-def test_launchers(program, what):
-    r = subprocess.run([program, B.LIB, what], capture_output=True, text=True, timeout=120)
+def run(program, *args):
+    r = subprocess.run([program, B.LIB, *args], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_several_devices(program):
+    run(program, "devices")
+
+
+@pytest.mark.parametrize("call", range(4))
+@pytest.mark.parametrize("kind", ["attributes", "entry points"])
+def test_a_failure_is_not_kept(program, kind, call):
+    run(program, kind, str(call))
