@@ -353,7 +353,8 @@ mxsa_status mxsa_load_kv(const mxsa_problem* problem, int64_t n_tokens, const in
  * whose squares sum past FP32's range give 0), rounded once:
  *   q_out[t][h][:]     = the row of q[t][h], in q_dtype, dense;
  *   k_cache, v_cache   = the rows of k, and v as it is, at slot loc[t], with
- *                        mxsa_store_kv's casts (applied to the FP32 row of k);
+ *                        mxsa_store_kv's casts (applied to the FP32 row of k,
+ *                        whose NaN have no sign: 0x7F in an FP8 cache);
  *   idx_q_out[t][g][:] = the row of idx_q[t][g], in kv_dtype, dense (what
  *                        mxsa_select_blocks takes), g < Hkv;
  *   idx_cache          = the rows of idx_k, at slot loc[t], in kv_dtype.
@@ -364,8 +365,9 @@ mxsa_status mxsa_load_kv(const mxsa_problem* problem, int64_t n_tokens, const in
  * A token with positions[t] < 0 is padding: nothing of it is written.  One
  * at or past num_positions is left out too and sets MXSA_FLAG_POS.  loc[t] <
  * 0: its k, v and idx_k are not stored; past the cache: the same, and
- * MXSA_FLAG_PAGE.  Slots that occur twice get one token's rows, column by
- * column (each 16-byte piece of one of them).
+ * MXSA_FLAG_PAGE.  Slots should be distinct: one that occurs twice holds a
+ * mixture of its tokens' rows, each value (in an NVFP4 cache: each byte, so
+ * that codes may stand under the other token's scale) one of theirs.
  * idx_dim 0: the idx_* pointers are NULL; else 64 or 128, none of idx_q,
  * idx_k, idx_q_out, idx_cache NULL, rot_dim <= idx_dim, kv_dtype not NVFP4.
  * Of the problem, the call reads what mxsa_store_kv reads and num_q_heads.
