@@ -273,7 +273,9 @@ mxsa_status mxsa_dense_fwd(const mxsa_problem* problem, const void* q, const voi
  * everything else is FP32.  A NaN or infinity at a key outside
  * [0, used_kv_len) of a sequence does not reach its rows; under causal masking
  * the V rows of keys that come after a token but that others of its group see
- * have to be finite.  Results do not depend on timing: the same call gives the
+ * have to be finite.  An infinity in V at a key that a row sees makes its
+ * column of the row infinite or NaN (a tile of few rows multiplies it by
+ * zeros too).  Results do not depend on timing: the same call gives the
  * same bits.  Two calls that may run at the same time, captured graphs
  * included, need a ws each.
  * cu_seqlens_q must be non-decreasing within [0, total_q], else MXSA_FLAG_CU
