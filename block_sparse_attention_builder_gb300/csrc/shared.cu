@@ -122,10 +122,13 @@ HLayout shared_layout(const mxsa_problem& p) {
   const long long extra = std::min(by_cost, triples * (blocks - 1));
   HLayout L;
   L.tile_cap = triples + extra;
-  // A row and its twin (halves that split the blocks) in two jobs; a further
-  // chunk's tile has at most 256 rows, twins counted.
-  const long long rows = (long long)p.total_q * G;
-  L.row_cap = 4LL * p.total_q * p.num_q_heads + std::min(256LL, 2 * rows) * extra;
+  // A row in each of its token's jobs (a prefix needs a second sequence), its
+  // twin in a job's last row tile where that is of one half (halves that split
+  // the blocks, at most T tokens); a further chunk's tile has at most 256
+  // rows, twins counted.
+  const long long rows = (long long)p.total_q * G, in_jobs = (p.num_seqs > 1 ? 2 : 1) * rows;
+  const long long jobs = p.num_seqs + p.num_seqs / 2;
+  L.row_cap = p.num_kv_heads * (in_jobs + std::min(in_jobs, jobs * T * G)) + std::min(256LL, 2 * rows) * extra;
   L.join_cap = (int)(2 * std::min(2 + by_cost / p.num_kv_heads, 2 * blocks + 2));
   size_t o = 0;
   auto take = [&o](size_t n) {
@@ -177,7 +180,7 @@ struct HPlanArgs {
   const int32_t* prefix_lens;
   int32_t* flags;  // may be null
   HPtrs ws;
-  long long tile_cap, row_cap;
+  long long tile_cap;
   int32_t num_seqs, num_groups, total_q, Hkv, G, T, max_len, causal, ctas;
 };
 
@@ -1527,7 +1530,6 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
   pa.flags = flags;
   pa.ws = ptrs;
   pa.tile_cap = L.tile_cap;
-  pa.row_cap = L.row_cap;
   pa.num_seqs = p.num_seqs;
   pa.num_groups = num_groups;
   pa.total_q = p.total_q;
