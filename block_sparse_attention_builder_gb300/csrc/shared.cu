@@ -804,6 +804,12 @@ __device__ __forceinline__ bool join_copies(uint32_t mem, uint32_t tO, HGroupSyn
   return true;
 }
 
+#ifdef MXSA_TEST_HOOKS
+// Test builds only: CTA g_skip_window keeps its first window of pages to
+// itself, so that every role's next wait runs out.
+__device__ int g_skip_window = -1;
+#endif
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kHThreads, 1)
     k_shared(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmq1,
@@ -1024,7 +1030,12 @@ __global__ void __launch_bounds__(kHThreads, 1)
             x.last = k + size >= t.nblk;
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&c.win_full[wn % kHWindows]);
+#ifdef MXSA_TEST_HOOKS
+          const bool skip = cta == g_skip_window && wn == 0;
+#else
+          constexpr bool skip = false;
+#endif
+          if (lane == 0 && !skip) mbar_arrive(&c.win_full[wn % kHWindows]);
           ++wn;
           k += size;
           page = ahead;
@@ -1597,3 +1608,11 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
 }
 
 }  // namespace mxsa
+
+#ifdef MXSA_TEST_HOOKS
+// Test builds only: the CTA of the next dense_shared_fwd launches that keeps
+// its first window to itself; -1 turns the switch off.  Synchronous.
+extern "C" mxsa_status mxsa_test_skip_window(int32_t cta) {
+  return cudaMemcpyToSymbol(mxsa::g_skip_window, &cta, sizeof(cta)) == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
+}
+#endif
