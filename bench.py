@@ -33,6 +33,7 @@ import hashlib
 import json
 import math
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -73,12 +74,51 @@ def measured_peaks():
     return dict(hbm_gbs=6800.0, bf16_tflops=1900.0, bf16_tflops_sustained=1700.0, src="fallback")
 
 
-def fwd_source_hash() -> str:
-    h = hashlib.sha256()
-    for f in ("fwd.cu", "fwd_decode.cuh", "ptx.cuh", "internal.h"):
-        with open(os.path.join(ROOT, "block_sparse_attention_builder_gb300", "csrc", f), "rb") as fh:
-            h.update(fh.read())
-    return h.hexdigest()[:16]
+def _without_comments(text: str) -> str:
+    text = re.sub(r"/\*.*?\*/|//[^\n]*", " ", text, flags=re.S)
+    return "\n".join(filter(None, (" ".join(line.split()) for line in text.splitlines())))
+
+
+def _definitions(text: str):
+    """The top-level definitions of a header, as (names, text); preprocessor
+    lines other than #define and namespaces are left out."""
+    out, lines, depth = [], [], 0
+    for line in _without_comments(text).splitlines():
+        if depth == 0 and (re.match(r"namespace\b|#(?!\s*define)", line) or line == "}" and not lines):
+            continue
+        lines.append(line)
+        depth += line.count("{") - line.count("}")
+        if depth == 0 and (line[0] == "#" or line[-1] in ";}"):
+            whole = " ".join(lines)
+            head = whole.split("{")[0]
+            names = set(re.findall(r"([A-Za-z_]\w*)\s*(?:\(|=|;|\[)", head))
+            names |= set(re.findall(r"\b(?:struct|class|enum|using|define)\s+(?:alignas\([^)]*\)\s*)?(\w+)", whole))
+            if re.match(r"enum\b", head):
+                names |= set(re.findall(r"[A-Za-z_]\w*", whole))
+            out.append((names, whole))
+            lines = []
+    return out
+
+
+def fwd_source_hash(headers=None) -> str:
+    """Of the forward kernels' own files and of what they use of the headers
+    that the library's kernels share (headers: their texts)."""
+    csrc = os.path.join(ROOT, "block_sparse_attention_builder_gb300", "csrc")
+
+    def read(name):
+        with open(os.path.join(csrc, name)) as fh:
+            return fh.read()
+
+    own = _without_comments(read("fwd.cu") + read("fwd_decode.cuh"))
+    rest = [d for text in headers or (read("ptx.cuh"), read("internal.h")) for d in _definitions(text)]
+    used, words, new = [], set(), set(re.findall(r"\w+", own))
+    while new:
+        words |= new
+        take = [d for d in rest if d[0] & words]
+        rest = [d for d in rest if not d[0] & words]
+        used += [whole for _, whole in take]
+        new = set(re.findall(r"\w+", " ".join(whole for _, whole in take))) - words
+    return hashlib.sha256("\n".join([own] + sorted(used)).encode()).hexdigest()[:16]
 
 
 def fwd_phases_label(n_dec_items: int, n_kvs_items: int) -> str:
