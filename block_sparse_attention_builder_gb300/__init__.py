@@ -194,18 +194,18 @@ def _refuse_types(what: str, rows, exact):
 
 def _need_attention(what: str, prob: Problem, q=None, k_cache=None, v_cache=None, block_tables=None,
                     cu_seqlens_q=None, used_kv_lens=None, sel=None, out=None, lse=None):
-    qb, kb = _ELEM_BYTES.get(prob.q_dtype, 2), _ELEM_BYTES.get(prob.kv_dtype, 2)
-    rows = max(prob.total_q, 0) * max(prob.num_q_heads, 0)
-    cache = max(prob.num_pages, 0) * max(prob.num_kv_heads, 0) * max(prob.page_size, 0) * \
-        _ROW_BYTES.get(prob.kv_dtype, 256)
-    _need(what, "q", q, rows * 128 * qb)
+    total_q, seqs, hkv = max(prob.total_q, 0), max(prob.num_seqs, 0), max(prob.num_kv_heads, 0)
+    rows = total_q * max(prob.num_q_heads, 0)
+    out_bytes = rows * 128 * _ELEM_BYTES.get(prob.q_dtype, 2)
+    cache = max(prob.num_pages, 0) * hkv * max(prob.page_size, 0) * _ROW_BYTES.get(prob.kv_dtype, 256)
+    _need(what, "q", q, out_bytes)
     _need(what, "k_cache", k_cache, cache)
     _need(what, "v_cache", v_cache, cache)
-    _need(what, "block_tables", block_tables, max(prob.num_seqs, 0) * max(prob.max_pages_per_seq, 0) * 4)
-    _need(what, "cu_seqlens_q", cu_seqlens_q, (max(prob.num_seqs, 0) + 1) * 8)
-    _need(what, "used_kv_lens", used_kv_lens, max(prob.num_seqs, 0) * 4)
-    _need(what, "selected", sel, max(prob.total_q, 0) * max(prob.num_kv_heads, 0) * max(prob.topk, 0) * 4)
-    _need(what, "out", out, rows * 128 * qb)
+    _need(what, "block_tables", block_tables, seqs * max(prob.max_pages_per_seq, 0) * 4)
+    _need(what, "cu_seqlens_q", cu_seqlens_q, (seqs + 1) * 8)
+    _need(what, "used_kv_lens", used_kv_lens, seqs * 4)
+    _need(what, "selected", sel, total_q * hkv * max(prob.topk, 0) * 4)
+    _need(what, "out", out, out_bytes)
     _need(what, "lse", lse, rows * 4)
 
 
@@ -391,20 +391,22 @@ def load_kv(prob, loc, k_cache, v_cache, k, v, idx_cache=None, idx_k=None, flags
     n = loc.numel()
     ih, idim = (int(idx_k.shape[1]), int(idx_k.shape[2])) if idx_k is not None else (0, 0)
     what = "mxsa_load_kv"
-    qb, kb = _ELEM_BYTES.get(prob.q_dtype, 2), _ELEM_BYTES.get(prob.kv_dtype, 2)
+    qd, kd, hkv = prob.q_dtype, prob.kv_dtype, prob.num_kv_heads
+    slots = max(prob.num_pages, 0) * max(prob.page_size, 0)
+    rows, cache = n * hkv * 128 * _ELEM_BYTES.get(qd, 2), slots * max(hkv, 0) * _ROW_BYTES.get(kd, 256)
     _need(what, "loc", loc, n * 8)
-    _need(what, "k", k, n * prob.num_kv_heads * 128 * qb)
-    _need(what, "v", v, n * prob.num_kv_heads * 128 * qb)
-    cache = max(prob.num_pages, 0) * max(prob.num_kv_heads, 0) * max(prob.page_size, 0)
-    _need(what, "k_cache", k_cache, cache * _ROW_BYTES.get(prob.kv_dtype, 256))
-    _need(what, "v_cache", v_cache, cache * _ROW_BYTES.get(prob.kv_dtype, 256))
-    _need(what, "idx_k", idx_k, n * ih * idim * qb)
-    _need(what, "idx_cache", idx_cache, max(prob.num_pages, 0) * ih * max(prob.page_size, 0) * idim * kb)
+    _need(what, "k", k, rows)
+    _need(what, "v", v, rows)
+    _need(what, "k_cache", k_cache, cache)
+    _need(what, "v_cache", v_cache, cache)
+    _need(what, "idx_k", idx_k, n * ih * idim * _ELEM_BYTES.get(qd, 2))
+    _need(what, "idx_cache", idx_cache, slots * ih * idim * _ELEM_BYTES.get(kd, 2))
     _need(what, "flags", flags, 4)
-    qt, kt = _ROW_TYPE.get(prob.q_dtype), _ROW_TYPE.get(prob.kv_dtype)
+    qt, kt = _ROW_TYPE.get(qd), _ROW_TYPE.get(kd)
     try:
         plain = (k.dtype is qt and v.dtype is qt and k_cache.dtype is kt and v_cache.dtype is kt and
-                 loc.dtype is _I64 and idx_k is None and (flags is None or flags.dtype is _I32))
+                 loc.dtype is _I64 and (idx_k is None or (idx_k.dtype is qt and idx_cache.dtype is kt)) and
+                 (flags is None or flags.dtype is _I32))
     except AttributeError:  # a None: the library says whether it may be one
         plain = False
     if not plain:
@@ -415,10 +417,10 @@ def load_kv(prob, loc, k_cache, v_cache, k, v, idx_cache=None, idx_k=None, flags
                              _ptr(idx_cache), _ptr(idx_k), ih, idim, _ptr(flags), _stream(stream)), what)
 
 
-def _token_stride(what: str, name: str, t: torch.Tensor, n: int, heads: int, dim: int) -> int:
+def _token_stride(what: str, name: str, t: torch.Tensor, dtype, n: int, heads: int, dim: int) -> int:
     """Elements between the tokens of t [n, heads, dim], a dense tensor or a
     view of a packed projection (a token's heads next to each other)."""
-    if t.shape != (n, heads, dim) or t.element_size() != 2:
+    if t.shape != (n, heads, dim) or (t.dtype is not dtype and t.element_size() != 2):
         raise MxsaError(1, f"{what}: {name} is {tuple(t.shape)} of {t.dtype}, the problem needs "
                            f"{(n, heads, dim)} of a 16-bit type")
     token, head, one = t.stride()
@@ -445,25 +447,27 @@ def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_ca
     n, hq, hkv = loc.numel(), prob.num_q_heads, prob.num_kv_heads
     if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
         raise MxsaError(1, f"{what}: cos_sin must be float32 [positions, rot_dim]")
-    q_stride = _token_stride(what, "q", q, n, hq, 128)
-    k_stride = _token_stride(what, "k", k, n, hkv, 128)
-    v_stride = _token_stride(what, "v", v, n, hkv, 128)
+    qd, kd = prob.q_dtype, prob.kv_dtype
+    qt, kt = _ROW_TYPE.get(qd), _ROW_TYPE.get(kd)
+    q_stride = _token_stride(what, "q", q, qt, n, hq, 128)
+    k_stride = _token_stride(what, "k", k, qt, n, hkv, 128)
+    v_stride = _token_stride(what, "v", v, qt, n, hkv, 128)
     _need(what, "cos_sin", cos_sin, 0)
     _need(what, "positions", positions, n * 8)
     _need(what, "loc", loc, n * 8)
     _need(what, "q_out", q_out, n * hq * 256)
     rows = max(prob.num_pages, 0) * max(hkv, 0) * max(prob.page_size, 0)
-    cache = rows * _ROW_BYTES.get(prob.kv_dtype, 256)
+    cache = rows * _ROW_BYTES.get(kd, 256)
     _need(what, "k_cache", k_cache, cache)
     _need(what, "v_cache", v_cache, cache)
     idx = iq_stride = ik_stride = 0
     if idx_q is not None or idx_k is not None:
         if idx_q is None or idx_k is None or idx_q_out is None or idx_cache is None:
             raise MxsaError(1, f"{what}: idx_q, idx_k, idx_q_out and idx_cache come together")
-        kb = _ELEM_BYTES.get(prob.kv_dtype, 2)
+        kb = _ELEM_BYTES.get(kd, 2)
         idx = int(idx_q.shape[-1])
-        iq_stride = _token_stride(what, "idx_q", idx_q, n, hkv, idx)
-        ik_stride = _token_stride(what, "idx_k", idx_k, n, hkv, idx)
+        iq_stride = _token_stride(what, "idx_q", idx_q, qt, n, hkv, idx)
+        ik_stride = _token_stride(what, "idx_k", idx_k, qt, n, hkv, idx)
         _need(what, "idx_q_out", idx_q_out, n * hkv * idx * kb)
         _need(what, "idx_cache", idx_cache, rows * idx * kb)
     per_head = None
@@ -473,7 +477,7 @@ def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_ca
         ph = w.dim() == 2
         if per_head not in (None, ph) or w.shape != ((heads, dim) if ph else (dim,)):
             raise MxsaError(1, f"{what}: {name} is {tuple(w.shape)}: all weights are [dim], or all [heads, dim]")
-        if w.element_size() != 2:
+        if w.dtype is not qt and w.element_size() != 2:
             raise MxsaError(1, f"{what}: {name} is {w.dtype}: the weights have the query's type")
         _need(what, name, w, 0)
         per_head = ph
@@ -487,7 +491,6 @@ def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_ca
     if idx_k_weight is not None:
         weight("idx_k_weight", idx_k_weight, hkv, idx)
     _need(what, "flags", flags, 4)
-    qt, kt = _ROW_TYPE.get(prob.q_dtype), _ROW_TYPE.get(prob.kv_dtype)
     try:
         plain = (q.dtype is qt and k.dtype is qt and v.dtype is qt and q_out.dtype is qt and k_cache.dtype is kt and
                  v_cache.dtype is kt and positions.dtype is _I64 and loc.dtype is _I64 and
