@@ -512,7 +512,7 @@ struct alignas(16) HWindow {
 
 struct HCtrl {
   uint64_t q_full[4], q_empty[2], kv_full[2 * kHStages], kv_empty[kHStages];
-  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2], turn[2], group[2], done;
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2], turn[2], done;
   uint64_t work_full[kHWork], work_empty[kHWork];
   uint64_t win_full[kHWindows], win_empty[kHWindows];
   HTile work[kHWork];  // the CTA's tiles, from the scheduler to the issuers and the softmax; no blocks: the end
@@ -727,32 +727,29 @@ __device__ __forceinline__ void few_rows(uint32_t tS, int copy, int k0, int lo, 
   *l += ls.x + ls.y;
 }
 
-// Barrier of one softmax group's four warps, `n` of them so far.  An mbarrier
-// and no named barrier: when another role has given up, a warp may leave at
-// the wait before while the others pass it, and a named barrier would wait for
-// it without a limit.
-struct HGroupSync {
-  uint64_t* bar;
-  volatile int* abort_flag;
-  int32_t* flags;
-  int n;
-  __device__ __forceinline__ bool operator()() {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-    return hwarp_all(mbar_wait(bar, n++ & 1, abort_flag, flags, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
-  }
-};
+// Barrier of softmax group h's four warps.  A named one knows no limit, so a
+// warp that gave up, or leaves after another role did, arrives once as it goes:
+// the others are let through, see the abort flag and leave too (false).  An
+// mbarrier, whose waits have a limit of their own, cost the 64 decoding
+// sequences' call 1 us of 110.
+__device__ __forceinline__ bool group_sync(int h, volatile int* abort_flag) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+  return hwarp_all(*abort_flag == 0);
+}
+__device__ __forceinline__ void group_leave(int h, volatile int* abort_flag) {
+  if (!hwarp_all(*abort_flag == 0)) asm volatile("bar.arrive %0, 128;" ::"r"(1 + h) : "memory");
+}
 
 // The partial rows of a tile with copies: the copies' sums join over shared
 // memory (32 KB at `mem`, the stage of the group's last V), 64 columns at a
 // time, 16-byte pieces of a row at places that change with the row.  False
 // when a wait gave up.
-__device__ __forceinline__ bool join_copies(uint32_t mem, uint32_t tO, HGroupSync& sync, int r, int row, int copy,
-                                            int copies, int rows, bool live, float m, float l, float* part_o,
-                                            float* part_lse) {
+__device__ __forceinline__ bool join_copies(uint32_t mem, uint32_t tO, int h, volatile int* abort_flag, int r, int row,
+                                            int copy, int copies, int rows, bool live, float m, float l,
+                                            float* part_o, float* part_lse) {
   const int apart = 128 / copies;
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(mem + r * 8), "f"(m), "f"(l) : "memory");
-  if (!sync()) return false;
+  if (!group_sync(h, abort_flag)) return false;
   float mq[4], lq[4], M = -INFINITY, L = 0.f;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -769,7 +766,7 @@ __device__ __forceinline__ bool join_copies(uint32_t mem, uint32_t tO, HGroupSyn
   for (int q = 0; q < 4; ++q) L += lq[q] * (M == -INFINITY ? 1.f : ex2_approx(mq[q] - M));  // (a NaN stays one)
   const float f = L == 0.f ? 0.f : (M == -INFINITY ? 1.f : ex2_approx(m - M)) / L;
   if (live && copy == 0) part_lse[row] = L == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) + lg2_approx(L);
-  if (!sync()) return false;
+  if (!group_sync(h, abort_flag)) return false;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
@@ -784,7 +781,7 @@ __device__ __forceinline__ bool join_copies(uint32_t mem, uint32_t tO, HGroupSyn
                        __float_as_uint(ov[4 * k + 1] * f), __float_as_uint(ov[4 * k + 2] * f),
                        __float_as_uint(ov[4 * k + 3] * f));
     }
-    if (!sync()) return false;
+    if (!group_sync(h, abort_flag)) return false;
     for (int x = r; x < rows * 16; x += 128) {
       const int rr = x >> 4, c4 = x & 15;
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -799,7 +796,7 @@ __device__ __forceinline__ bool join_copies(uint32_t mem, uint32_t tO, HGroupSyn
       *reinterpret_cast<float4*>(part_o + rr * 128 + pass * 64 + c4 * 4) = sum;
     }
     fence_proxy_async_smem();  // the stage's next copy comes after what was done here
-    if (!sync()) return false;
+    if (!group_sync(h, abort_flag)) return false;
   }
   return true;
 }
@@ -830,7 +827,6 @@ __global__ void __launch_bounds__(kHThreads, 1)
       mbar_init(&c.o_full[i], 1);
       mbar_init(&c.turn[i], 1);
       mbar_init(&c.o_empty[i], 4);
-      mbar_init(&c.group[i], 4);
     }
     for (int i = 0; i < kHStages; ++i) {
       mbar_init(&c.kv_full[i], 1);
@@ -1202,7 +1198,6 @@ __global__ void __launch_bounds__(kHThreads, 1)
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + h * 256 + lane_addr, tO = tS + 128;
     int at = 0, qn = 0, n_s = 0, n_o = 0;
-    HGroupSync sync{&c.group[h], abort_flag, fl, 0};
     bool ok = true;
     HTile t;
     while (ok && next_tile(&t)) {
@@ -1344,8 +1339,8 @@ __global__ void __launch_bounds__(kHThreads, 1)
       if (keys > 1) {
         tc_fence_after();
         const int pl = at - 2 * n + place_v(((n - 1 - half) & ~1) + half, n), st = pl % kHStages;  // its last block's V
-        ok = join_copies(sbase + kHOffKV + st * kHTileBytes, tO, sync, r, row, copy, keys, (int)rows, live, m, l,
-                         a.ws.part_o + base * 128, a.ws.part_lse + base);
+        ok = join_copies(sbase + kHOffKV + st * kHTileBytes, tO, h, abort_flag, r, row, copy, keys, (int)rows, live, m,
+                         l, a.ws.part_o + base * 128, a.ws.part_lse + base);
         if (!ok) break;
         if (r == 0) {
           mbar_arrive(&c.kv_empty[st]);
@@ -1373,6 +1368,7 @@ __global__ void __launch_bounds__(kHThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&c.o_empty[h]);
     }
+    group_leave(h, abort_flag);
   }
   tc_fence_before();
   __syncthreads();

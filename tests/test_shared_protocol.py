@@ -7,7 +7,8 @@ the hardware does, and checks that it was that phase.  Random interleavings
 look for deadlocks, phases mistaken for others, and buffers refilled or
 overwritten before their readers are done.  With `give_up`, a wait runs out in
 the middle although what it waits for may still come: every role has to return
-all the same.  A barrier that knows no limit (a named one) does not let them.
+all the same.  The groups' barrier knows no limit: a warp that leaves arrives
+there once, and whoever is let through looks at the abort.
 """
 import os
 import random
@@ -31,9 +32,9 @@ class Barrier:
 
 
 class Forward:
-    def __init__(self, tiles, rnd, named=False):
+    def __init__(self, tiles, rnd, leave=True):
         """tiles: (blocks, keys, edge); keys: 0 two halves, 1 one half, 2 or 4 one half with copies of its rows."""
-        self.tiles, self.rnd, self.named = tiles, rnd, named
+        self.tiles, self.rnd, self.leave = tiles, rnd, leave
         self.bar, self.landing, self.abort = {}, {}, False
         for name, count, n in (("q_full", 1, 4), ("q_empty", 2, 2), ("kv_full", 1, 2 * STAGES),
                                ("kv_empty", 2, STAGES), ("s_full", 1, 2), ("p_half", 4, 2), ("p_full", 4, 2),
@@ -70,7 +71,7 @@ class Forward:
 
     def ready(self, w):
         b = self.bar[w[0], w[1]]
-        return (b.phases - 1) & 1 == w[2] & 1
+        return b.phases > w[2] if w[0] == "group" else (b.phases - 1) & 1 == w[2] & 1
 
     def kv_full(self, place):
         return "kv_full", place % (2 * STAGES), place // (2 * STAGES)
@@ -351,8 +352,10 @@ class Forward:
                 for _ in range(6):
                     self.check(self.stage[place % STAGES] == place, "the join's memory is another block's")
                     self.arrive("group", h)
-                    ok = yield ("group", h, syncs) + (("drain",) if self.named else ())
+                    yield "group", h, syncs, "no limit"
                     syncs += 1
+                    yield None
+                    ok = not self.abort
                     if not ok:
                         break
                 if not ok:
@@ -362,6 +365,9 @@ class Forward:
                     self.arrive("kv_empty", place % STAGES, 2)
             self.o_read[h][warp] = no
             self.arrive("o_empty", h)
+        yield None
+        if self.abort and self.leave:
+            self.arrive("group", h)
 
 
 def random_tiles(r):
@@ -384,12 +390,12 @@ def test_every_role_returns_when_one_gives_up(seed):
         Forward(random_tiles(r), r).run(give_up=True)
 
 
-def test_a_barrier_without_a_limit_would_wait_for_ever():
-    """The model sees it: a warp that gave up at the wait before never comes to the group's barrier."""
+def test_a_warp_that_left_without_arriving_would_be_waited_for():
+    """The model sees it: warps that give up at the wait before the groups' barrier, while others pass that wait."""
     def hangs(seed):
         r = random.Random(seed)
         try:
-            Forward([(2, 4, False)] * 3 + [(3, 2, False)], r, named=True).run(give_up=True)
+            Forward([(2, 4, False)] * 3 + [(3, 2, False)], r, leave=False).run(give_up=True)
         except AssertionError as e:
             return "deadlock" in str(e)
         return False
@@ -397,6 +403,7 @@ def test_a_barrier_without_a_limit_would_wait_for_ever():
     assert any(hangs(s) for s in range(600))
 
 
-def test_the_forward_has_no_such_barrier():
+def test_the_forward_arrives_as_it_leaves():
     src = open(os.path.join(ROOT, "block_sparse_attention_builder_gb300", "csrc", "shared.cu")).read()
-    assert not re.search(r"bar(rier)?\.(cta\.)?sync", src)
+    assert len(re.findall(r"bar\.sync", src)) == 1 and len(re.findall(r"bar\.arrive", src)) == 1
+    assert re.search(r"bar\.sync[^\n]*\n\s*return hwarp_all\(\*abort_flag == 0\);", src)
