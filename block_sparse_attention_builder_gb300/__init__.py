@@ -429,6 +429,18 @@ def _token_stride(what: str, name: str, t: torch.Tensor, dtype, n: int, heads: i
     return token if n > 1 else heads * dim
 
 
+def _weight_form(what: str, name: str, w: torch.Tensor, dtype, heads: int, dim: int, per_head) -> bool:
+    """Whether w is [heads, dim] and not [dim]; per_head: the weights before it (None: the first)."""
+    form = w.dim() == 2
+    if per_head not in (None, form) or w.shape != ((heads, dim) if form else (dim,)):
+        raise MxsaError(1, f"{what}: {name} is {tuple(w.shape)}: all weights are [dim], or all [heads, dim]")
+    if w.dtype is not dtype and w.element_size() != 2:
+        raise MxsaError(1, f"{what}: {name} is {w.dtype}: the weights have the query's type")
+    if not w.is_contiguous():
+        raise MxsaError(1, f"{what}: {name} is not contiguous")
+    return form
+
+
 def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_cache, q_weight=None, k_weight=None,
                     eps=1e-6, interleaved=False, idx_q=None, idx_k=None, idx_q_weight=None, idx_k_weight=None,
                     idx_q_out=None, idx_cache=None, flags=None, stream=None):
@@ -471,25 +483,14 @@ def norm_rope_store(prob, positions, loc, cos_sin, q, k, v, q_out, k_cache, v_ca
         _need(what, "idx_q_out", idx_q_out, n * hkv * idx * kb)
         _need(what, "idx_cache", idx_cache, rows * idx * kb)
     per_head = None
-
-    def weight(name, w, heads, dim):
-        nonlocal per_head
-        ph = w.dim() == 2
-        if per_head not in (None, ph) or w.shape != ((heads, dim) if ph else (dim,)):
-            raise MxsaError(1, f"{what}: {name} is {tuple(w.shape)}: all weights are [dim], or all [heads, dim]")
-        if w.dtype is not qt and w.element_size() != 2:
-            raise MxsaError(1, f"{what}: {name} is {w.dtype}: the weights have the query's type")
-        _need(what, name, w, 0)
-        per_head = ph
-
     if q_weight is not None:
-        weight("q_weight", q_weight, hq, 128)
+        per_head = _weight_form(what, "q_weight", q_weight, qt, hq, 128, per_head)
     if k_weight is not None:
-        weight("k_weight", k_weight, hkv, 128)
+        per_head = _weight_form(what, "k_weight", k_weight, qt, hkv, 128, per_head)
     if idx_q_weight is not None:
-        weight("idx_q_weight", idx_q_weight, hkv, idx)
+        per_head = _weight_form(what, "idx_q_weight", idx_q_weight, qt, hkv, idx, per_head)
     if idx_k_weight is not None:
-        weight("idx_k_weight", idx_k_weight, hkv, idx)
+        per_head = _weight_form(what, "idx_k_weight", idx_k_weight, qt, hkv, idx, per_head)
     _need(what, "flags", flags, 4)
     try:
         plain = (q.dtype is qt and k.dtype is qt and v.dtype is qt and q_out.dtype is qt and k_cache.dtype is kt and
