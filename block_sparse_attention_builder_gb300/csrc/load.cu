@@ -8,8 +8,8 @@
 // makes 16 output bytes (8 values) of K and the same 8 of V, and the index
 // keys' chunks follow, as in the store: consecutive threads read and write
 // consecutive bytes, and the slot is looked up once for both.  36864 tokens
-// of 8 heads, e4m3 (227 MB): 37.5 us, 6.0 TB/s; 30011 of 4 heads, NVFP4 (79
-// MB): 16.3 us, 4.8 TB/s with the launch.
+// of 8 heads, e4m3 (227 MB): 37.4 us, 6.1 TB/s; 30011 of 4 heads, NVFP4 (79
+// MB): 16.1 us, 4.9 TB/s with the launch.
 #include <algorithm>
 #include <climits>
 

@@ -28,7 +28,10 @@
 // of a token's rows with the next rows prefetched: 340 us); 240 us, 5.7 TB/s,
 // now.  2 or 8 rows at a time: 294 and 332 us.  FP8 cache 257 us (193 us at
 // the copy rate), NVFP4 341 us (189 us; its casts are 100 us of it: 452 us
-// with a division and the comparisons for each value).
+// with a division and the comparisons for each value).  All forms but NVFP4
+// with pairs side by side spill registers, 36 to 84 bytes stored and 52 to 248
+// loaded a thread (the most: FP8 with pairs (i, i + R/2)), which takes issue
+// slots too; launch bounds with more registers, and fewer warps, were slower.
 #include <algorithm>
 #include <climits>
 

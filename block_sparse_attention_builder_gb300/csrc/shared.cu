@@ -26,7 +26,7 @@
 // Three launches: k_shared_plan (one CTA: jobs, tiles, queues), k_shared
 // (persistent, one CTA per SM) and k_shared_join.  64 decoding sequences of
 // 64 + 8 heads on a prefix of 32768 keys and 128 to 2048 of their own: 7, 84
-// and 8 us, 109 us in all.
+// and 8 us, 109 to 110 us in all.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -485,9 +485,9 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
 // (250 and 300) and its products; the tensor pipe's own 2176 cycles of both
 // groups' four products are 0.7 of it.  256 decoding sequences of 64 + 8
 // heads on a shared prefix of 65536 keys and 64 to 2048 of their own (558
-// GFLOP, 1.36 GB): 515 to 535 us in all, 1.06 PFLOP/s.  Tiles of one half: memory;
-// 256 sequences with 2048 keys of their own and no prefix (2.16 GB): 354 us,
-// 6.1 TB/s.  Code that is run once or rarely is kept in loops: unrolled, its
+// GFLOP, 1.36 GB): 525 to 543 us in all on different GPUs, 1.03 to 1.06
+// PFLOP/s.  Tiles of one half: memory; 256 sequences with 2048 keys of their
+// own and no prefix (2.16 GB): 332 us, 6.5 TB/s.  Code that is run once or rarely is kept in loops: unrolled, its
 // first use in a launch costs 3 to 4 us of instruction fetches.
 constexpr int kHThreads = 384;
 constexpr int kHProducer = 8, kHMma = 9, kHSched = 11;
@@ -498,11 +498,6 @@ constexpr float kHRescale = 8.f;         // log2 units
 constexpr uint32_t kHOffKV = 2 * kHTileBytes;
 constexpr uint32_t kHOffCtrl = kHOffKV + kHStages * kHTileBytes;
 
-// A role may pass over places and q slots of the other group without looking
-// at their barriers.  A parity only tells a phase from the one before, so a
-// stage's (and a q buffer's) uses alternate between two "full" barriers: to
-// mistake a phase a role would have to be two uses ahead of the copies, and
-// each wait comes after one for a copy that was issued later than that.
 // Some blocks of a tile, from the scheduler to the producer: the pages' third
 // coordinates (two a block; -1: none).  No blocks: the end.
 struct alignas(16) HWindow {
@@ -510,6 +505,11 @@ struct alignas(16) HWindow {
   int32_t n, first, last;  // blocks; whether they are their tile's first and last ones
 };
 
+// A role may pass over places and q slots of the other group without looking
+// at their barriers.  A parity only tells a phase from the one before, so a
+// stage's (and a q buffer's) uses alternate between two "full" barriers: to
+// mistake a phase a role would have to be two uses ahead of the copies, and
+// each wait comes after one for a copy that was issued later than that.
 struct HCtrl {
   uint64_t q_full[4], q_empty[2], kv_full[2 * kHStages], kv_empty[kHStages];
   uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_empty[2], turn[2], done;
