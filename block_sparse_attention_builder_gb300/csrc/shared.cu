@@ -487,8 +487,9 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
 // heads on a shared prefix of 65536 keys and 64 to 2048 of their own (558
 // GFLOP, 1.36 GB): 525 to 543 us in all on different GPUs, 1.03 to 1.06
 // PFLOP/s.  Tiles of one half: memory; 256 sequences with 2048 keys of their
-// own and no prefix (2.16 GB): 332 us, 6.5 TB/s.  Code that is run once or rarely is kept in loops: unrolled, its
-// first use in a launch costs 3 to 4 us of instruction fetches.
+// own and no prefix (2.16 GB): 332 us, 6.5 TB/s.  Code that is run once or
+// rarely is kept in loops: unrolled, its first use in a launch costs 3 to 4 us
+// of instruction fetches.
 constexpr int kHThreads = 384;
 constexpr int kHProducer = 8, kHMma = 9, kHSched = 11;
 constexpr uint32_t kHTileBytes = 32768;  // 128 rows x 128 x 16-bit
@@ -731,7 +732,7 @@ __device__ __forceinline__ void few_rows(uint32_t tS, int copy, int k0, int lo, 
 // warp that gave up, or leaves after another role did, arrives once as it goes:
 // the others are let through, see the abort flag and leave too (false).  An
 // mbarrier, whose waits have a limit of their own, cost the 64 decoding
-// sequences' call 1 us of 110.
+// sequences' call 1 to 3 us of 110.
 __device__ __forceinline__ bool group_sync(int h, volatile int* abort_flag) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
   return hwarp_all(*abort_flag == 0);
