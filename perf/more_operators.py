@@ -319,6 +319,7 @@ def _prepare_prompt(case, seed):
     if own:
         import block_sparse_attention_builder_gb300 as mx
         s["prob"] = mx.make_problem(len(lens), total, hq, hkv, 1, 64, 1, 1, True, q_dtype=t)
+        s["ws"] = torch.empty(mx.prompt_workspace_size(s["prob"]), dtype=torch.uint8, device="cuda")
     return s
 
 
@@ -482,7 +483,7 @@ def _own_commit(s):
 
 def _own_prompt(s):
     import block_sparse_attention_builder_gb300 as mx
-    mx.prompt_fwd(s["prob"], s["q"], s["k"], s["v"], s["cu"], s["out"], s["lse"])
+    mx.prompt_fwd(s["prob"], s["q"], s["k"], s["v"], s["cu"], s["ws"], s["out"], s["lse"])
     return s["out"], s["lse"]
 
 
