@@ -7,7 +7,10 @@ read_status, store_kv, the paged-cache store that writes new tokens' K/V
 and index keys into the caches, load_kv, its read side, norm_rope_store,
 the store behind a layer's norms and rotation, select_blocks, the top-k
 block selection over those index keys, dense_fwd and dense_shared_fwd, the
-dense attention of a batch that may share prefixes), plus ``kvouter_attention`` with the
+dense attention of a batch that may share prefixes, build_tables, the page
+tables and slots of a step from its requests' lengths, tree_mask, tree_fwd and
+tree_commit, the masks, attention and accepted paths of drafted trees, and
+prompt_fwd, the attention of whole packed prompts), plus ``kvouter_attention`` with the
 call shape of the fw-ai/minimax-kernels README's Quick start and
 ``SparseAttention`` which keeps the workspaces of one problem shape for
 repeated calls.
@@ -39,7 +42,7 @@ _CODE_DTYPE = {BF16: torch.bfloat16, FP16: torch.float16, FP8_E4M3: torch.float8
 NVFP4_ROW_BYTES = 72
 
 FLAG_NAMES = {1: "SEL_RANGE", 2: "SEL_DUP", 4: "PAGE", 8: "CAUSAL_LEN", 16: "LEN", 32: "TIMEOUT",
-              64: "SCHEDULE", 128: "CU", 256: "POS", 512: "GROUP"}
+              64: "SCHEDULE", 128: "CU", 256: "POS", 512: "GROUP", 1024: "TREE", 2048: "PAGES"}
 STATUS_NAMES = {0: "MXSA_OK", 1: "MXSA_ERR_INVALID_ARG", 2: "MXSA_ERR_UNSUPPORTED", 3: "MXSA_ERR_WORKSPACE",
                 4: "MXSA_ERR_CUDA", 5: "MXSA_ERR_DATA"}
 EXPORTED = ["mxsa_version", "mxsa_status_string", "mxsa_workspace_size", "mxsa_build_index", "mxsa_schedule",
@@ -48,7 +51,8 @@ EXPORTED = ["mxsa_version", "mxsa_status_string", "mxsa_workspace_size", "mxsa_b
             "mxsa_sched_layout_query", "mxsa_store_kv", "mxsa_dense_fwd", "mxsa_select_workspace_size",
             "mxsa_select_blocks", "mxsa_dedup_workspace_size", "mxsa_build_index_dedup",
             "mxsa_attention_noalloc", "mxsa_noalloc_read_status", "mxsa_load_kv", "mxsa_norm_rope_store",
-            "mxsa_shared_workspace_size", "mxsa_dense_shared_fwd"]
+            "mxsa_shared_workspace_size", "mxsa_dense_shared_fwd", "mxsa_tree_fwd", "mxsa_tree_mask",
+            "mxsa_tree_commit", "mxsa_prompt_workspace_size", "mxsa_prompt_fwd", "mxsa_build_tables"]
 
 
 class MxsaError(RuntimeError):
@@ -124,6 +128,12 @@ def _load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "mxsa_norm_rope_store": [P, P, ctypes.c_int64] + [P] * 19,
         "mxsa_shared_workspace_size": [P, P],
         "mxsa_dense_shared_fwd": [P] * 7 + [ctypes.c_int32, P, P, P, S, P, P, P, P],
+        "mxsa_tree_fwd": [P] * 8 + [ctypes.c_int32, ctypes.c_int32, P, P, P, S, P, P, P, P],
+        "mxsa_tree_mask": [P] * 4 + [ctypes.c_int32, P, P, P, P],
+        "mxsa_tree_commit": [P] * 5 + [ctypes.c_int32, P, P, P, P, ctypes.c_int32, ctypes.c_int32, P, P, P],
+        "mxsa_prompt_workspace_size": [P, P],
+        "mxsa_prompt_fwd": [P, P, ctypes.c_int64, P, ctypes.c_int64, P, ctypes.c_int64, P, P, S, P, P, P, P],
+        "mxsa_build_tables": [P] * 15,
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -358,6 +368,171 @@ def dense_shared_fwd(prob, q, k_cache, v_cache, block_tables, cu_seqlens_q, used
                                       _ptr(cu_seqlens_q), _ptr(used_kv_lens), ng, _ptr(group_ptr), _ptr(prefix_lens),
                                       _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), _ptr(lse), _ptr(flags),
                                       _stream(stream)), what)
+
+
+def _need_types(what: str, exact):
+    """Refuses tensors of another type than a kernel reads: (name, tensor, dtype); tensors may be None."""
+    for name, t, dtype in exact:
+        if t is not None and t.dtype is not dtype:
+            raise MxsaError(1, f"{what}: {name} is {t.dtype}, not {dtype}")
+
+
+def _need_mask(what: str, tree_mask: torch.Tensor, total_q: int) -> int:
+    """The words of a token's mask in tree_mask, int32 (or uint32) [total_q, words]."""
+    if tree_mask.dtype is not _I32 and tree_mask.dtype is not torch.uint32:
+        raise MxsaError(1, f"{what}: tree_mask is {tree_mask.dtype}, not torch.int32")
+    if tree_mask.dim() != 2 or tree_mask.shape[0] < total_q:
+        raise MxsaError(1, f"{what}: tree_mask is {tuple(tree_mask.shape)}, not [total_q, words]")
+    _need(what, "tree_mask", tree_mask, 0)
+    return tree_mask.shape[1]
+
+
+def tree_fwd(prob, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens, tree_mask, group_ptr, prefix_lens,
+             ws, out, lse=None, flags=None, stream=None):
+    """Attention of drafted token trees (mxsa_tree_fwd): token t of a sequence
+    sees its committed keys (all but its new tokens') and those of its new
+    tokens whose bits are set in tree_mask[t] (int32 [total_q, words], as
+    tree_mask writes it).  group_ptr, prefix_lens (None: no groups), ws and the
+    rest as for dense_shared_fwd; the problem's causal is not used."""
+    what = "mxsa_tree_fwd"
+    if (group_ptr is None) != (prefix_lens is None):
+        raise MxsaError(1, f"{what}: group_ptr and prefix_lens come together")
+    ng = 0 if prefix_lens is None else prefix_lens.numel()
+    _need_attention(what, prob, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                    cu_seqlens_q=cu_seqlens_q, used_kv_lens=used_kv_lens, out=out, lse=lse)
+    words = _need_mask(what, tree_mask, prob.total_q)
+    _need(what, "group_ptr", group_ptr, (ng + 1) * 4)
+    _need(what, "prefix_lens", prefix_lens, ng * 4)
+    _need(what, "ws", ws, 0)
+    _need(what, "flags", flags, 4)
+    qt, kt = _ROW_TYPE.get(prob.q_dtype), _ROW_TYPE.get(prob.kv_dtype)
+    _refuse_types(what, (("q", q, qt), ("k_cache", k_cache, kt), ("v_cache", v_cache, kt), ("out", out, qt)),
+                  (("block_tables", block_tables, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
+                   ("used_kv_lens", used_kv_lens, _I32), ("group_ptr", group_ptr, _I32),
+                   ("prefix_lens", prefix_lens, _I32), ("lse", lse, _F32), ("flags", flags, _I32)))
+    _check(_lib.mxsa_tree_fwd(ctypes.byref(prob), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                              _ptr(cu_seqlens_q), _ptr(used_kv_lens), _ptr(tree_mask), words, ng, _ptr(group_ptr),
+                              _ptr(prefix_lens), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), _ptr(lse),
+                              _ptr(flags), _stream(stream)), what)
+
+
+def tree_mask(prob, parents, cu_seqlens_q, used_kv_lens, mask, positions=None, flags=None, stream=None):
+    """Ancestor masks and positions of drafted trees (mxsa_tree_mask): parents
+    int32 [total_q], a token's parent among its sequence's new tokens (-1: the
+    last committed token) -> mask int32 [total_q, words], positions int64
+    [total_q] (committed tokens + ancestors) or None."""
+    what = "mxsa_tree_mask"
+    total_q, seqs = max(prob.total_q, 0), max(prob.num_seqs, 0)
+    words = _need_mask(what, mask, total_q)
+    _need(what, "parents", parents, total_q * 4)
+    _need(what, "cu_seqlens_q", cu_seqlens_q, (seqs + 1) * 8)
+    _need(what, "used_kv_lens", used_kv_lens, seqs * 4)
+    _need(what, "positions", positions, total_q * 8)
+    _need(what, "flags", flags, 4)
+    _need_types(what, (("parents", parents, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
+                       ("used_kv_lens", used_kv_lens, _I32), ("positions", positions, _I64), ("flags", flags, _I32)))
+    _check(_lib.mxsa_tree_mask(ctypes.byref(prob), _ptr(parents), _ptr(cu_seqlens_q), _ptr(used_kv_lens), words,
+                               _ptr(mask), _ptr(positions), _ptr(flags), _stream(stream)), what)
+
+
+def tree_commit(prob, cu_seqlens_q, used_kv_lens, block_tables, path, path_lens, k_cache, v_cache, kv_lens_out=None,
+                idx_cache=None, flags=None, stream=None):
+    """The accepted path of each drafted tree moved to its places in the caches
+    (mxsa_tree_commit): rows of new tokens path[s, :path_lens[s]] (int32,
+    ascending) to the first places behind the committed keys.  idx_cache:
+    [pages, index heads, page_size, index dim] in the cache dtype, or None;
+    kv_lens_out int32 [B]: committed and accepted tokens."""
+    what = "mxsa_tree_commit"
+    seqs = max(prob.num_seqs, 0)
+    _need_attention(what, prob, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                    cu_seqlens_q=cu_seqlens_q, used_kv_lens=used_kv_lens)
+    if path.dim() != 2:
+        raise MxsaError(1, f"{what}: path is {tuple(path.shape)}, not [num_seqs, longest path]")
+    wide = path.shape[1]
+    _need(what, "path", path, seqs * wide * 4)
+    _need(what, "path_lens", path_lens, seqs * 4)
+    _need(what, "kv_lens_out", kv_lens_out, seqs * 4)
+    _need(what, "flags", flags, 4)
+    ih = idim = 0
+    if idx_cache is not None:
+        if idx_cache.dim() != 4 or idx_cache.shape[0] < prob.num_pages or idx_cache.shape[2] != prob.page_size:
+            raise MxsaError(1, f"{what}: idx_cache is {tuple(idx_cache.shape)}, not [pages, heads, page_size, dim]")
+        ih, idim = idx_cache.shape[1], idx_cache.shape[3]
+        _need(what, "idx_cache", idx_cache, prob.num_pages * ih * prob.page_size * idim *
+              _ELEM_BYTES.get(prob.kv_dtype, 2))
+    kt = _ROW_TYPE.get(prob.kv_dtype)
+    _refuse_types(what, (("k_cache", k_cache, kt), ("v_cache", v_cache, kt), ("idx_cache", idx_cache, kt)),
+                  (("block_tables", block_tables, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
+                   ("used_kv_lens", used_kv_lens, _I32), ("path", path, _I32), ("path_lens", path_lens, _I32),
+                   ("kv_lens_out", kv_lens_out, _I32), ("flags", flags, _I32)))
+    _check(_lib.mxsa_tree_commit(ctypes.byref(prob), _ptr(cu_seqlens_q), _ptr(used_kv_lens), _ptr(block_tables),
+                                 _ptr(path), wide, _ptr(path_lens), _ptr(k_cache), _ptr(v_cache), _ptr(idx_cache), ih,
+                                 idim, _ptr(kv_lens_out), _ptr(flags), _stream(stream)), what)
+
+
+def prompt_workspace_size(prob: Problem) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.mxsa_prompt_workspace_size(ctypes.byref(prob), ctypes.byref(n)), "mxsa_prompt_workspace_size")
+    return n.value
+
+
+def prompt_fwd(prob, q, k, v, cu_seqlens, ws, out, lse=None, flags=None, stream=None):
+    """Attention of whole prompts packed one behind the other (mxsa_prompt_fwd),
+    causal per the problem, straight from the projection: q [total_q, Hq, 128],
+    k and v [total_q, Hkv, 128] in the problem's q dtype, dense or views of one
+    packed projection; cu_seqlens int64 [B + 1]; out [total_q, Hq, 128], lse
+    [Hq, total_q].  ws: uint8 device tensor of prompt_workspace_size bytes.
+    The problem's pages are not used."""
+    what = "mxsa_prompt_fwd"
+    n, hq, hkv = max(prob.total_q, 0), prob.num_q_heads, prob.num_kv_heads
+    qt = _ROW_TYPE.get(prob.q_dtype)
+    q_stride = _token_stride(what, "q", q, qt, n, hq, 128)
+    k_stride = _token_stride(what, "k", k, qt, n, hkv, 128)
+    v_stride = _token_stride(what, "v", v, qt, n, hkv, 128)
+    _need(what, "cu_seqlens", cu_seqlens, (max(prob.num_seqs, 0) + 1) * 8)
+    _need(what, "ws", ws, 0)
+    _need(what, "out", out, n * hq * 256)
+    _need(what, "lse", lse, n * hq * 4)
+    _need(what, "flags", flags, 4)
+    _refuse_types(what, (("q", q, qt), ("k", k, qt), ("v", v, qt), ("out", out, qt)),
+                  (("cu_seqlens", cu_seqlens, _I64), ("lse", lse, _F32), ("flags", flags, _I32)))
+    _check(_lib.mxsa_prompt_fwd(ctypes.byref(prob), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                                _ptr(cu_seqlens), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), _ptr(lse),
+                                _ptr(flags), _stream(stream)), what)
+
+
+def build_tables(prob, kv_lens, new_lens, pages_held, block_tables, free_pages, free_count, cu_seqlens_q,
+                 used_kv_lens, positions, loc, pages_held_out=None, free_count_out=None, flags=None, stream=None):
+    """A serving step's tables on the GPU (mxsa_build_tables).  Request s has
+    kv_lens[s] cached tokens in its row's first pages_held[s] pages and
+    new_lens[s] new ones (< 0: finished, its pages go back); pages come off the
+    end of free_pages[:free_count] (int32 [num_pages], int32 [1]).  Writes
+    cu_seqlens_q int64 [B + 1], used_kv_lens int32 [B], positions and loc int64
+    [total_q] (-1: padding) and the rows of block_tables.  pages_held_out and
+    free_count_out: None writes pages_held and free_count themselves;
+    used_kv_lens may be kv_lens."""
+    what = "mxsa_build_tables"
+    seqs, total_q = max(prob.num_seqs, 0), max(prob.total_q, 0)
+    pages_held_out = pages_held if pages_held_out is None else pages_held_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    ints = (("kv_lens", kv_lens, seqs), ("new_lens", new_lens, seqs), ("pages_held", pages_held, seqs),
+            ("block_tables", block_tables, seqs * max(prob.max_pages_per_seq, 0)),
+            ("free_pages", free_pages, max(prob.num_pages, 0)), ("free_count", free_count, 1),
+            ("used_kv_lens", used_kv_lens, seqs), ("pages_held_out", pages_held_out, seqs),
+            ("free_count_out", free_count_out, 1))
+    for name, t, n in ints:
+        _need(what, name, t, n * 4)
+    _need(what, "cu_seqlens_q", cu_seqlens_q, (seqs + 1) * 8)
+    _need(what, "positions", positions, total_q * 8)
+    _need(what, "loc", loc, total_q * 8)
+    _need(what, "flags", flags, 4)
+    _need_types(what, tuple((name, t, _I32) for name, t, _ in ints) +
+                (("cu_seqlens_q", cu_seqlens_q, _I64), ("positions", positions, _I64), ("loc", loc, _I64),
+                 ("flags", flags, _I32)))
+    _check(_lib.mxsa_build_tables(ctypes.byref(prob), _ptr(kv_lens), _ptr(new_lens), _ptr(pages_held),
+                                  _ptr(block_tables), _ptr(free_pages), _ptr(free_count), _ptr(cu_seqlens_q),
+                                  _ptr(used_kv_lens), _ptr(positions), _ptr(loc), _ptr(pages_held_out),
+                                  _ptr(free_count_out), _ptr(flags), _stream(stream)), what)
 
 
 def store_kv(prob, loc, k, v, k_cache, v_cache, idx_k=None, idx_cache=None, flags=None, stream=None):

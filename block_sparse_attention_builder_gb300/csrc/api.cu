@@ -458,11 +458,12 @@ mxsa_status mxsa_shared_workspace_size(const mxsa_problem* problem, size_t* shar
   return MXSA_OK;
 }
 
-mxsa_status mxsa_dense_shared_fwd(const mxsa_problem* problem, const void* q, const void* k_cache,
-                                  const void* v_cache, const int32_t* block_tables, const int64_t* cu_seqlens_q,
-                                  const int32_t* used_kv_lens, int32_t num_groups, const int32_t* group_ptr,
-                                  const int32_t* prefix_lens, void* ws, size_t shared_bytes, void* out, float* lse,
-                                  int32_t* device_flags, void* stream) {
+// mxsa_dense_shared_fwd, and mxsa_tree_fwd with a mask.
+static mxsa_status shared_fwd(const mxsa_problem* problem, const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, const int64_t* cu_seqlens_q, const int32_t* used_kv_lens,
+                              const uint32_t* tree_mask, int32_t mask_words, int32_t num_groups,
+                              const int32_t* group_ptr, const int32_t* prefix_lens, void* ws, size_t shared_bytes,
+                              void* out, float* lse, int32_t* device_flags, void* stream) {
   if (!problem) return MXSA_ERR_INVALID_ARG;
   mxsa_status s = validate_shared(*problem);
   if (s != MXSA_OK) return s;
@@ -470,16 +471,152 @@ mxsa_status mxsa_dense_shared_fwd(const mxsa_problem* problem, const void* q, co
   if (num_groups < 0 || num_groups > p.num_seqs) return MXSA_ERR_INVALID_ARG;
   if (!block_tables || !cu_seqlens_q || !used_kv_lens || !ws) return MXSA_ERR_INVALID_ARG;
   if (num_groups > 0 && (!group_ptr || !prefix_lens)) return MXSA_ERR_INVALID_ARG;
-  if (p.total_q > 0 && (!q || !k_cache || !v_cache || !out)) return MXSA_ERR_INVALID_ARG;
+  if (p.total_q > 0 && (!q || !k_cache || !v_cache || !out || (mask_words && !tree_mask))) return MXSA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
       !aligned(block_tables, 4) || !aligned(cu_seqlens_q, 8) || !aligned(used_kv_lens, 4) || !aligned(lse, 4) ||
-      !aligned(group_ptr, 4) || !aligned(prefix_lens, 4) || !aligned(ws, 256) || !aligned(device_flags, 4))
+      !aligned(group_ptr, 4) || !aligned(prefix_lens, 4) || !aligned(ws, 256) || !aligned(device_flags, 4) ||
+      !aligned(tree_mask, 4))
     return MXSA_ERR_INVALID_ARG;
   if (shared_bytes < shared_workspace_bytes(p)) return MXSA_ERR_WORKSPACE;
   if (!kernel_writable(out) || !kernel_writable(lse)) return MXSA_ERR_INVALID_ARG;
   cudaError_t e = launch_dense_shared(p, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens, num_groups,
-                                      num_groups > 0 ? group_ptr : nullptr, prefix_lens, ws, out, lse, device_flags,
-                                      static_cast<cudaStream_t>(stream));
+                                      num_groups > 0 ? group_ptr : nullptr, prefix_lens, tree_mask, mask_words, ws,
+                                      out, lse, device_flags, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
+}
+
+mxsa_status mxsa_dense_shared_fwd(const mxsa_problem* problem, const void* q, const void* k_cache,
+                                  const void* v_cache, const int32_t* block_tables, const int64_t* cu_seqlens_q,
+                                  const int32_t* used_kv_lens, int32_t num_groups, const int32_t* group_ptr,
+                                  const int32_t* prefix_lens, void* ws, size_t shared_bytes, void* out, float* lse,
+                                  int32_t* device_flags, void* stream) {
+  return shared_fwd(problem, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens, nullptr, 0, num_groups,
+                    group_ptr, prefix_lens, ws, shared_bytes, out, lse, device_flags, stream);
+}
+
+mxsa_status mxsa_tree_fwd(const mxsa_problem* problem, const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, const int64_t* cu_seqlens_q, const int32_t* used_kv_lens,
+                          const uint32_t* tree_mask, int32_t mask_words, int32_t num_groups,
+                          const int32_t* group_ptr, const int32_t* prefix_lens, void* ws, size_t shared_bytes,
+                          void* out, float* lse, int32_t* device_flags, void* stream) {
+  if (mask_words < 1) return MXSA_ERR_INVALID_ARG;
+  if (mask_words > kMaxMaskWords) return MXSA_ERR_UNSUPPORTED;
+  return shared_fwd(problem, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens, tree_mask, mask_words,
+                    num_groups, group_ptr, prefix_lens, ws, shared_bytes, out, lse, device_flags, stream);
+}
+
+mxsa_status mxsa_tree_mask(const mxsa_problem* problem, const int32_t* parents, const int64_t* cu_seqlens_q,
+                           const int32_t* used_kv_lens, int32_t mask_words, uint32_t* tree_mask, int64_t* positions,
+                           int32_t* device_flags, void* stream) {
+  if (!problem) return MXSA_ERR_INVALID_ARG;
+  mxsa_status s = validate_shape(*problem);
+  if (s != MXSA_OK) return s;
+  const mxsa_problem& p = *problem;
+  if (mask_words < 1) return MXSA_ERR_INVALID_ARG;
+  if (mask_words > kMaxMaskWords || p.num_seqs > 1024) return MXSA_ERR_UNSUPPORTED;
+  if (!cu_seqlens_q || !used_kv_lens || (p.total_q > 0 && (!parents || !tree_mask))) return MXSA_ERR_INVALID_ARG;
+  if (!aligned(parents, 4) || !aligned(cu_seqlens_q, 8) || !aligned(used_kv_lens, 4) || !aligned(tree_mask, 4) ||
+      !aligned(positions, 8) || !aligned(device_flags, 4))
+    return MXSA_ERR_INVALID_ARG;
+  cudaError_t e = launch_tree_mask(p, parents, cu_seqlens_q, used_kv_lens, mask_words, tree_mask, positions,
+                                   device_flags, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
+}
+
+mxsa_status mxsa_tree_commit(const mxsa_problem* problem, const int64_t* cu_seqlens_q, const int32_t* used_kv_lens,
+                             const int32_t* block_tables, const int32_t* path, int32_t max_path,
+                             const int32_t* path_lens, void* k_cache, void* v_cache, void* idx_cache,
+                             int32_t idx_heads, int32_t idx_dim, int32_t* kv_lens_out, int32_t* device_flags,
+                             void* stream) {
+  if (!problem) return MXSA_ERR_INVALID_ARG;
+  mxsa_status s = validate_shape(*problem);
+  if (s != MXSA_OK) return s;
+  const mxsa_problem& p = *problem;
+  if (max_path < 1) return MXSA_ERR_INVALID_ARG;
+  if (p.kv_dtype == MXSA_NVFP4 && idx_cache) return MXSA_ERR_UNSUPPORTED;  // index keys stay 16-bit or FP8
+  if (idx_cache && (idx_heads <= 0 || idx_dim <= 0 || idx_dim % 8 != 0)) return MXSA_ERR_INVALID_ARG;
+  if (!cu_seqlens_q || !used_kv_lens || !block_tables || !path || !path_lens || !k_cache || !v_cache ||
+      kv_lens_out == used_kv_lens)
+    return MXSA_ERR_INVALID_ARG;
+  if (!aligned(cu_seqlens_q, 8) || !aligned(used_kv_lens, 4) || !aligned(block_tables, 4) || !aligned(path, 4) ||
+      !aligned(path_lens, 4) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(idx_cache, 16) ||
+      !aligned(kv_lens_out, 4) || !aligned(device_flags, 4))
+    return MXSA_ERR_INVALID_ARG;
+  const int64_t heads = (int64_t)p.num_kv_heads + (idx_cache ? idx_heads : 0);
+  if (heads * p.num_seqs >= (1ll << 31) || (idx_cache && (int64_t)idx_dim * 2 >= (1ll << 31)))
+    return MXSA_ERR_UNSUPPORTED;
+  cudaError_t e = launch_tree_commit(p, cu_seqlens_q, used_kv_lens, block_tables, path, max_path, path_lens, k_cache,
+                                     v_cache, idx_cache, idx_heads, idx_dim, kv_lens_out, device_flags,
+                                     static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
+}
+
+// Shape checks of whole prompts: no pages.
+static mxsa_status validate_prompt(const mxsa_problem& problem) {
+  mxsa_problem p = problem;
+  p.page_size = 64;
+  p.num_pages = p.max_pages_per_seq = 1;
+  mxsa_status s = validate_shape(p);
+  if (s != MXSA_OK) return s;
+  if (p.kv_dtype != p.q_dtype || p.num_seqs > 1024) return MXSA_ERR_UNSUPPORTED;
+  if ((int64_t)p.total_q * p.num_q_heads >= (1ll << 31)) return MXSA_ERR_UNSUPPORTED;
+  if (((int64_t)p.total_q + p.num_seqs) * p.num_kv_heads >= (1ll << 31)) return MXSA_ERR_UNSUPPORTED;
+  return MXSA_OK;
+}
+
+mxsa_status mxsa_prompt_workspace_size(const mxsa_problem* problem, size_t* prompt_bytes) {
+  if (!problem || !prompt_bytes) return MXSA_ERR_INVALID_ARG;
+  mxsa_status s = validate_prompt(*problem);
+  if (s != MXSA_OK) return s;
+  *prompt_bytes = prompt_workspace_bytes(*problem);
+  return MXSA_OK;
+}
+
+mxsa_status mxsa_prompt_fwd(const mxsa_problem* problem, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, const int64_t* cu_seqlens, void* ws,
+                            size_t prompt_bytes, void* out, float* lse, int32_t* device_flags, void* stream) {
+  if (!problem) return MXSA_ERR_INVALID_ARG;
+  mxsa_status s = validate_prompt(*problem);
+  if (s != MXSA_OK) return s;
+  const mxsa_problem& p = *problem;
+  // (2^37 elements: a tensor map's strides are below 2^40 bytes)
+  auto stride_ok = [](int64_t stride, int64_t row) { return stride >= row && stride % 8 == 0 && stride < (1ll << 37); };
+  if (!stride_ok(q_stride, p.num_q_heads * 128LL) || !stride_ok(k_stride, p.num_kv_heads * 128LL) ||
+      !stride_ok(v_stride, p.num_kv_heads * 128LL))
+    return MXSA_ERR_INVALID_ARG;
+  if (!cu_seqlens || !ws || (p.total_q > 0 && (!q || !k || !v || !out))) return MXSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_seqlens, 8) ||
+      !aligned(ws, 256) || !aligned(lse, 4) || !aligned(device_flags, 4))
+    return MXSA_ERR_INVALID_ARG;
+  if (prompt_bytes < prompt_workspace_bytes(p)) return MXSA_ERR_WORKSPACE;
+  if (!kernel_writable(out) || !kernel_writable(lse)) return MXSA_ERR_INVALID_ARG;
+  cudaError_t e = launch_prompt(p, q, q_stride, k, k_stride, v, v_stride, cu_seqlens, ws, out, lse, device_flags,
+                                static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
+}
+
+mxsa_status mxsa_build_tables(const mxsa_problem* problem, const int32_t* kv_lens, const int32_t* new_lens,
+                              const int32_t* pages_held, int32_t* block_tables, int32_t* free_pages,
+                              const int32_t* free_count, int64_t* cu_seqlens_q, int32_t* used_kv_lens,
+                              int64_t* positions, int64_t* loc, int32_t* pages_held_out, int32_t* free_count_out,
+                              int32_t* device_flags, void* stream) {
+  if (!problem) return MXSA_ERR_INVALID_ARG;
+  mxsa_status s = validate_shape(*problem);
+  if (s != MXSA_OK) return s;
+  const mxsa_problem& p = *problem;
+  if (p.num_seqs > 1024) return MXSA_ERR_UNSUPPORTED;
+  if (!kv_lens || !new_lens || !pages_held || !block_tables || !free_pages || !free_count || !cu_seqlens_q ||
+      !used_kv_lens || !pages_held_out || !free_count_out || (p.total_q > 0 && (!positions || !loc)))
+    return MXSA_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)kv_lens, (const void*)new_lens, (const void*)pages_held,
+                        (const void*)block_tables, (const void*)free_pages, (const void*)free_count,
+                        (const void*)used_kv_lens, (const void*)pages_held_out, (const void*)free_count_out,
+                        (const void*)device_flags})
+    if (!aligned(x, 4)) return MXSA_ERR_INVALID_ARG;
+  if (!aligned(cu_seqlens_q, 8) || !aligned(positions, 16) || !aligned(loc, 16)) return MXSA_ERR_INVALID_ARG;
+  cudaError_t e = launch_tables(p, kv_lens, new_lens, pages_held, block_tables, free_pages, free_count, cu_seqlens_q,
+                                used_kv_lens, positions, loc, pages_held_out, free_count_out, device_flags,
+                                static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
 }
 

@@ -177,8 +177,23 @@ size_t shared_workspace_bytes(const mxsa_problem& p);
 bool shared_rows_fit(const mxsa_problem& p);
 cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void* k_cache, const void* v_cache,
                                 const int32_t* block_tables, const int64_t* cu, const int32_t* lens, int num_groups,
-                                const int32_t* group_ptr, const int32_t* prefix_lens, void* ws, void* out, float* lse,
-                                int32_t* flags, cudaStream_t st);
+                                const int32_t* group_ptr, const int32_t* prefix_lens, const uint32_t* tree_mask,
+                                int tree_words, void* ws, void* out, float* lse, int32_t* flags, cudaStream_t st);
+constexpr int kMaxMaskWords = 64;  // of a drafted tree's mask: 2048 tokens
+size_t prompt_workspace_bytes(const mxsa_problem& p);
+cudaError_t launch_prompt(const mxsa_problem& p, const void* q, long long q_stride, const void* k, long long k_stride,
+                          const void* v, long long v_stride, const int64_t* cu, void* ws, void* out, float* lse,
+                          int32_t* flags, cudaStream_t st);
+cudaError_t launch_tables(const mxsa_problem& p, const int32_t* kv_lens, const int32_t* new_lens,
+                          const int32_t* pages_held, int32_t* block_tables, int32_t* free_pages,
+                          const int32_t* free_count, int64_t* cu, int32_t* used, int64_t* positions, int64_t* loc,
+                          int32_t* held_out, int32_t* free_count_out, int32_t* flags, cudaStream_t st);
+cudaError_t launch_tree_mask(const mxsa_problem& p, const int32_t* parents, const int64_t* cu, const int32_t* lens,
+                             int words, uint32_t* mask, int64_t* positions, int32_t* flags, cudaStream_t st);
+cudaError_t launch_tree_commit(const mxsa_problem& p, const int64_t* cu, const int32_t* lens,
+                               const int32_t* block_tables, const int32_t* path, int max_path,
+                               const int32_t* path_lens, void* k_cache, void* v_cache, void* idx_cache,
+                               int idx_heads, int idx_dim, int32_t* lens_out, int32_t* flags, cudaStream_t st);
 cudaError_t launch_store(const mxsa_problem& p, long long n, const int64_t* loc, const void* k, const void* v,
                          void* k_cache, void* v_cache, const void* idx_k, void* idx_cache, int idx_heads,
                          int idx_dim, int32_t* flags, cudaStream_t st);

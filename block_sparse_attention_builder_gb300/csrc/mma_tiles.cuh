@@ -1,0 +1,117 @@
+// Pieces that the dense tcgen05 kernels over 128-row tiles share: the two
+// products of a block as eight MMAs each, and small helpers of the softmax.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ptx.cuh"
+
+namespace mxsa {
+
+// the largest of three in one instruction (NaN operands are ignored, as by fmaxf)
+__device__ __forceinline__ float hmax3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t hpack2(float a, float b) {
+  if (kBf16) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ bool hwarp_all(bool v) { return __all_sync(0xffffffffu, v); }
+
+// eight consecutive floats to global memory (32-byte aligned)
+__device__ __forceinline__ void st_global_v8(float* p, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Low words of the operands' shared-memory descriptors (the high word is the
+// same for all: 1024 bytes between groups of 8 rows, version 1, 128-byte
+// swizzle); the address field counts 16 bytes and does not overflow below.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t saddr) { return saddr >> 4; }
+__device__ __forceinline__ uint32_t desc_mn_major(uint32_t saddr) { return (saddr >> 4) | ((16384u >> 4) << 16); }
+// a value that all lanes hold, in a form the compiler knows to be uniform
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// The eight products over 16 columns each of one block.  S = q k^T: both
+// operands K-major, 64 columns to a 16 KB half, 32 bytes a step.  O (+)= P V:
+// P in TMEM, 8 columns a step, V MN-major, 16 rows (2 KB) a step.
+template <int kStep>
+__device__ __forceinline__ void mma_qk_step(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
+  constexpr int off = ((kStep >> 2) * 16384 + (kStep & 3) * 32) >> 4;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 u, v;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tadd.u32 u, %1, %5;\n\tadd.u32 v, %2, %5;\n\t"
+      "mov.b64 x, {u, %6};\n\tmov.b64 y, {v, %6};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(q), "r"(k), "r"(idesc), "n"(kStep > 0), "n"(off), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_qk(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
+  mma_qk_step<0>(d, q, k, idesc);
+  mma_qk_step<1>(d, q, k, idesc);
+  mma_qk_step<2>(d, q, k, idesc);
+  mma_qk_step<3>(d, q, k, idesc);
+  mma_qk_step<4>(d, q, k, idesc);
+  mma_qk_step<5>(d, q, k, idesc);
+  mma_qk_step<6>(d, q, k, idesc);
+  mma_qk_step<7>(d, q, k, idesc);
+}
+template <int kStep>
+__device__ __forceinline__ void mma_pv_step(uint32_t d, uint32_t tp, uint32_t v, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t.reg .b32 x, v;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tadd.u32 x, %1, %5;\n\tadd.u32 v, %2, %6;\n\tmov.b64 y, {v, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n\t}" ::"r"(d),
+      "r"(tp), "r"(v), "r"(idesc), "r"(acc), "n"(kStep * 8), "n"(kStep * (2048 >> 4)), "r"(kDescHi)
+      : "memory");
+}
+// the first and the second 64 keys
+__device__ __forceinline__ void mma_pv_lo(uint32_t d, uint32_t tp, uint32_t v, uint32_t idesc, uint32_t acc) {
+  mma_pv_step<0>(d, tp, v, idesc, acc);
+  mma_pv_step<1>(d, tp, v, idesc, 1u);
+  mma_pv_step<2>(d, tp, v, idesc, 1u);
+  mma_pv_step<3>(d, tp, v, idesc, 1u);
+}
+__device__ __forceinline__ void mma_pv_hi(uint32_t d, uint32_t tp, uint32_t v, uint32_t idesc) {
+  mma_pv_step<4>(d, tp, v, idesc, 1u);
+  mma_pv_step<5>(d, tp, v, idesc, 1u);
+  mma_pv_step<6>(d, tp, v, idesc, 1u);
+  mma_pv_step<7>(d, tp, v, idesc, 1u);
+}
+
+// O of the thread's row times f, 16 columns at a time
+__device__ __forceinline__ void scale_o(uint32_t tO, float f) {
+#pragma unroll 1
+  for (int cb = 0; cb < 8; ++cb) {
+    uint32_t w[16];
+    tmem_ld16(tO + cb * 16, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
+    tmem_st16(tO + cb * 16, w);
+  }
+}
+
+}  // namespace mxsa

@@ -36,6 +36,7 @@
 #include <climits>
 
 #include "internal.h"
+#include "mma_tiles.cuh"
 #include "ptx.cuh"
 
 namespace mxsa {
@@ -77,9 +78,10 @@ struct HJob {
   int32_t nch, chunk, nrt;         // chunks, blocks of one, row tiles
 };
 
-// A token: its sequence (-1: none), the keys it sees, and the tiles of its
-// sequence's own keys and of its group's prefix: for kv head g and chunk c <
-// nch, number base + (g * nch + c) * nrt.
+// A token: its sequence (-1: none), the keys it sees (of a drafted tree: its
+// sequence's committed keys), and the tiles of its sequence's own keys and of
+// its group's prefix: for kv head g and chunk c < nch, number base + (g * nch +
+// c) * nrt.
 struct alignas(16) HTok {
   int32_t seq, keys, own_base, own_nch;
   int32_t own_nrt, pre_base, pre_nch, pre_nrt;
@@ -182,6 +184,7 @@ struct HPlanArgs {
   HPtrs ws;
   long long tile_cap;
   int32_t num_seqs, num_groups, total_q, Hkv, G, T, max_len, causal, ctas;
+  int32_t tree_words;  // words of a token's tree mask; 0: no trees
 };
 
 // One CTA that the forward waits for: few barriers, and what a thread does
@@ -270,6 +273,10 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
       if (L < 0 || L > a.max_len) bad |= MXSA_FLAG_LEN;
       s.len[i] = min(max(L, 0), a.max_len);
       s.seq_group[i] = -1;
+      if (a.tree_words) {
+        if (nx - v > 32 * a.tree_words) bad |= MXSA_FLAG_TREE;
+        if (nx - v > s.len[i]) bad |= MXSA_FLAG_CAUSAL_LEN;
+      }
     }
     if (NG > 0 && i <= NG) {
       if (gv < 0 || gv > gn) bad |= MXSA_FLAG_GROUP;
@@ -287,14 +294,16 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     if (tid == 0) *a.ws.hdr = HHeader{{0, 0}, {0, 0}, {a.ctas, 0}};
     return;
   }
-  // a group's prefix is at most its shortest sequence with tokens
+  // a group's prefix is at most its shortest sequence with tokens (of drafted
+  // trees: what is committed of it)
   if (gp_ok && NG > 0)
     for (int i = tid; i < B; i += kHPlanThreads) {
       if (i < s.gp[0] || i >= s.gp[NG]) continue;
       const int j = last_le(s.gp, NG + 1, i);
       if (s.gp[j + 1] - s.gp[j] < 2) continue;  // one sequence alone shares nothing
       s.seq_group[i] = j;
-      if (s.cu[i + 1] > s.cu[i]) atomicMin(&s.shortest[j], s.len[i]);
+      const int tq = s.cu[i + 1] - s.cu[i];
+      if (tq > 0) atomicMin(&s.shortest[j], a.tree_words ? max(s.len[i] - tq, 0) : s.len[i]);
     }
   __syncthreads();
   auto prefix_of = [&](int j) {  // 0: no prefix (also for the group number -1)
@@ -437,7 +446,8 @@ __global__ void __launch_bounds__(kHPlanThreads) k_shared_plan(HPlanArgs a) {
     if (i >= s.cu[0] && i < s.cu[B]) {
       const int q = last_le(s.cu, B, i), L = s.len[q];
       v.seq = q;
-      v.keys = a.causal ? min(max(L - (s.cu[q + 1] - i) + 1, 0), L) : L;
+      v.keys = a.tree_words ? L - (s.cu[q + 1] - s.cu[q])
+                            : (a.causal ? min(max(L - (s.cu[q + 1] - i) + 1, 0), L) : L);
       const HJob& own = s.job[NG + q];
       if (own.nrt > 0) {
         v.own_base = own.tile0 + (i - own.tok0) / T2;
@@ -528,7 +538,19 @@ struct HArgs {
   HPtrs ws;
   int32_t G, T, Hkv, page_shift, max_pages, num_pages, causal;
   float scale_log2;
+  const uint32_t* tree_mask;  // [total_q][tree_words], of drafted trees
+  int32_t tree_words;
 };
+
+// Which of keys o .. o + 31 a row of a drafted tree sees, as bits; keys are
+// numbered from the first drafted one, those before it are seen by all.  row:
+// the token's mask, not read where o <= -32.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int o) {
+  if (o <= -32) return 0xFFFFFFFFu;
+  auto word = [&](int w) { return w < words ? __ldg(row + w) : 0u; };
+  if (o < 0) return (word(0) << -o) | ((1u << -o) - 1);
+  return __funnelshift_r(word(o >> 5), (o & 31) ? word((o >> 5) + 1) : 0u, o & 31);
+}
 
 __device__ __forceinline__ HTile load_tile(const HTile* p) {
   HTile t;
@@ -544,116 +566,11 @@ __device__ __forceinline__ HTile load_tile(const HTile* p) {
 __device__ __forceinline__ int place_k(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int place_v(int i, int n) { return i < n - 1 ? 2 * i + 2 : 2 * n - 1; }
 
-__device__ __forceinline__ float hmax3(float x, float y, float z) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
-
 // the larger of two; NaN when one is
 __device__ __forceinline__ float hmax_nan(float x, float y) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
   return r;
-}
-
-template <bool kBf16>
-__device__ __forceinline__ uint32_t hpack2(float a, float b) {
-  if (kBf16) {
-    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&h);
-  }
-  __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ bool hwarp_all(bool v) { return __all_sync(0xffffffffu, v); }
-
-// eight consecutive floats to global memory (32-byte aligned)
-__device__ __forceinline__ void st_global_v8(float* p, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-
-// One lane of a converged warp, always the same one.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, e;\n\t}"
-      : "=r"(p));
-  return p != 0;
-}
-
-// Low words of the operands' shared-memory descriptors (the high word is the
-// same for all: 1024 bytes between groups of 8 rows, version 1, 128-byte
-// swizzle); the address field counts 16 bytes and does not overflow below.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t desc_k_major(uint32_t saddr) { return saddr >> 4; }
-__device__ __forceinline__ uint32_t desc_mn_major(uint32_t saddr) { return (saddr >> 4) | ((16384u >> 4) << 16); }
-// a value that all lanes hold, in a form the compiler knows to be uniform
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
-
-// The eight products over 16 columns each of one block.  S = q k^T: both
-// operands K-major, 64 columns to a 16 KB half, 32 bytes a step.  O (+)= P V:
-// P in TMEM, 8 columns a step, V MN-major, 16 rows (2 KB) a step.
-template <int kStep>
-__device__ __forceinline__ void mma_qk_step(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
-  constexpr int off = ((kStep >> 2) * 16384 + (kStep & 3) * 32) >> 4;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b32 u, v;\n\t.reg .b64 x, y;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tadd.u32 u, %1, %5;\n\tadd.u32 v, %2, %5;\n\t"
-      "mov.b64 x, {u, %6};\n\tmov.b64 y, {v, %6};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-      "r"(q), "r"(k), "r"(idesc), "n"(kStep > 0), "n"(off), "r"(kDescHi)
-      : "memory");
-}
-__device__ __forceinline__ void mma_qk(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
-  mma_qk_step<0>(d, q, k, idesc);
-  mma_qk_step<1>(d, q, k, idesc);
-  mma_qk_step<2>(d, q, k, idesc);
-  mma_qk_step<3>(d, q, k, idesc);
-  mma_qk_step<4>(d, q, k, idesc);
-  mma_qk_step<5>(d, q, k, idesc);
-  mma_qk_step<6>(d, q, k, idesc);
-  mma_qk_step<7>(d, q, k, idesc);
-}
-template <int kStep>
-__device__ __forceinline__ void mma_pv_step(uint32_t d, uint32_t tp, uint32_t v, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t.reg .b32 x, v;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tadd.u32 x, %1, %5;\n\tadd.u32 v, %2, %6;\n\tmov.b64 y, {v, %7};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, p;\n\t}" ::"r"(d),
-      "r"(tp), "r"(v), "r"(idesc), "r"(acc), "n"(kStep * 8), "n"(kStep * (2048 >> 4)), "r"(kDescHi)
-      : "memory");
-}
-// the first and the second 64 keys
-__device__ __forceinline__ void mma_pv_lo(uint32_t d, uint32_t tp, uint32_t v, uint32_t idesc, uint32_t acc) {
-  mma_pv_step<0>(d, tp, v, idesc, acc);
-  mma_pv_step<1>(d, tp, v, idesc, 1u);
-  mma_pv_step<2>(d, tp, v, idesc, 1u);
-  mma_pv_step<3>(d, tp, v, idesc, 1u);
-}
-__device__ __forceinline__ void mma_pv_hi(uint32_t d, uint32_t tp, uint32_t v, uint32_t idesc) {
-  mma_pv_step<4>(d, tp, v, idesc, 1u);
-  mma_pv_step<5>(d, tp, v, idesc, 1u);
-  mma_pv_step<6>(d, tp, v, idesc, 1u);
-  mma_pv_step<7>(d, tp, v, idesc, 1u);
-}
-
-// O of the thread's row times f, 16 columns at a time
-__device__ __forceinline__ void scale_o(uint32_t tO, float f) {
-#pragma unroll 1
-  for (int cb = 0; cb < 8; ++cb) {
-    uint32_t w[16];
-    tmem_ld16(tO + cb * 16, w);
-    tmem_ld_wait();
-#pragma unroll
-    for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * f);
-    tmem_st16(tO + cb * 16, w);
-  }
 }
 
 // S of the thread's row outside columns [lo, hi) to -infinity.  A pass of its
@@ -672,20 +589,45 @@ __device__ __forceinline__ void mask_s(uint32_t tS, int lo, int hi) {
   tmem_st_wait();
 }
 
+// The same for a row of a drafted tree whose sequence has `base` committed
+// keys from the block's first on (it may be negative).
+__device__ __forceinline__ void mask_tree_s(uint32_t tS, int lo, int hi, const uint32_t* row, int words, int base) {
+#pragma unroll 1
+  for (int cb = 0; cb < 128; cb += 16) {
+    const uint32_t seen = tree_bits(row, words, cb - base);
+    uint32_t w[16];
+    tmem_ld16(tS + cb, w);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w[k] = cb + k >= lo && cb + k < hi && (seen >> k & 1) ? w[k] : 0xFF800000u;
+    tmem_st16(tS + cb, w);
+  }
+  tmem_st_wait();
+}
+
 // One block of a tile whose rows stand 128 / kKeys times in the MMA's: copy
 // `copy` takes the keys kKeys x copy .. of the block, with a maximum and a sum
 // of its own, and writes zeros as the other keys' weights.  A decode tile's
 // 8 rows then cost a quarter of the time of one warp with 128 keys to a
 // thread.
-template <int kKeys, bool kBf16>
+template <int kKeys, bool kBf16, bool kTree>
 __device__ __forceinline__ void few_rows(uint32_t tS, int copy, int k0, int lo, int hi, int warp_hi, bool live,
-                                         bool mine, float scale_log2, float* m, float* l) {
+                                         bool mine, float scale_log2, const uint32_t* mask, int words, int base,
+                                         float* m, float* l) {
   float sv[kKeys];
 #pragma unroll
   for (int q = 0; q < kKeys / 32; ++q) tmem_ld32(tS + copy * kKeys + q * 32, sv + q * 32);
   tmem_ld_wait();
   const int first = k0 + copy * kKeys;
   if (first < lo || first + kKeys > warp_hi) {
+    if (kTree) {
+#pragma unroll
+      for (int q = 0; q < kKeys / 32; ++q) {
+        const uint32_t seen = tree_bits(mask, words, first + 32 * q - base);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) sv[32 * q + k] = seen >> k & 1 ? sv[32 * q + k] : -INFINITY;
+      }
+    }
 #pragma unroll
     for (int k = 0; k < kKeys; ++k) sv[k] = first + k >= lo && first + k < hi ? sv[k] : -INFINITY;
   }
@@ -808,7 +750,9 @@ __device__ __forceinline__ bool join_copies(uint32_t mem, uint32_t tO, int h, vo
 __device__ int g_skip_window = -1;
 #endif
 
-template <bool kBf16>
+// kTree: drafted trees.  A row sees the keys before its sequence's drafted ones
+// and, of those, what its mask says; nothing else differs.
+template <bool kBf16, bool kTree>
 __global__ void __launch_bounds__(kHThreads, 1)
     k_shared(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmq1,
              const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, HArgs a) {
@@ -1218,8 +1162,11 @@ __global__ void __launch_bounds__(kHThreads, 1)
       const long long base = t.part0 + half * rows, pr = base + tt * G + (row - rt * G);
       const bool warp_live = __any_sync(0xffffffffu, live);
       int hi = key_end;  // the row sees the keys [lo, hi), all of the warp's rows [lo, warp_hi)
-      if (a.causal && live) hi = min(hi, a.ws.tok[t.tok0 + tt].keys);
-      const int warp_hi = __reduce_min_sync(0xffffffffu, hi);
+      if (!kTree && a.causal && live) hi = min(hi, a.ws.tok[t.tok0 + tt].keys);
+      // (a row that is not live sees everything: its mask is never read)
+      const int base_key = kTree && live ? a.ws.tok[t.tok0 + tt].keys : INT_MAX / 2;
+      const uint32_t* const mask = kTree && live ? a.tree_mask + (size_t)(t.tok0 + tt) * a.tree_words : a.tree_mask;
+      const int warp_hi = __reduce_min_sync(0xffffffffu, kTree ? min(hi, base_key) : hi);
       float m = -INFINITY, l = 0.f;
       bool mine = false;  // this group has blocks of the tile
       for (int i = half; i < n && ok; i += stride, ++n_s) {
@@ -1245,16 +1192,23 @@ __global__ void __launch_bounds__(kHThreads, 1)
         if (keys > 1) {
           tc_fence_after();
           if (keys == 4)
-            few_rows<32, kBf16>(tS, copy, k0, lo, hi, warp_hi, live, mine, a.scale_log2, &m, &l);
+            few_rows<32, kBf16, kTree>(tS, copy, k0, lo, hi, warp_hi, live, mine, a.scale_log2, mask, a.tree_words,
+                                       base_key, &m, &l);
           else
-            few_rows<64, kBf16>(tS, copy, k0, lo, hi, warp_hi, live, mine, a.scale_log2, &m, &l);
+            few_rows<64, kBf16, kTree>(tS, copy, k0, lo, hi, warp_hi, live, mine, a.scale_log2, mask, a.tree_words,
+                                       base_key, &m, &l);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&c.p_half[h]);
         } else if (warp_live) {
           tc_fence_after();
-          if (k0 < lo || k0 + 128 > warp_hi) mask_s(tS, lo - k0, hi - k0);
+          if (k0 < lo || k0 + 128 > warp_hi) {
+            if (kTree)
+              mask_tree_s(tS, lo - k0, hi - k0, mask, a.tree_words, base_key - k0);
+            else
+              mask_s(tS, lo - k0, hi - k0);
+          }
           // S 64 keys at a time, twice: the second ones and the first ones for
           // the maximum, then again the second ones for their exponentials.
           // A row's 128 scores at once would need registers that the other
@@ -1511,8 +1465,8 @@ bool shared_rows_fit(const mxsa_problem& p) { return shared_layout(p).row_cap < 
 
 cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void* k_cache, const void* v_cache,
                                 const int32_t* block_tables, const int64_t* cu, const int32_t* lens, int num_groups,
-                                const int32_t* group_ptr, const int32_t* prefix_lens, void* ws, void* out, float* lse,
-                                int32_t* flags, cudaStream_t st) {
+                                const int32_t* group_ptr, const int32_t* prefix_lens, const uint32_t* tree_mask,
+                                int tree_words, void* ws, void* out, float* lse, int32_t* flags, cudaStream_t st) {
   if (p.total_q == 0) return cudaSuccess;
   auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
@@ -1542,8 +1496,9 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
   static PerDevice limits;
   cudaError_t e = limits([smem] {
     const auto a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    cudaError_t x = cudaFuncSetAttribute(k_shared<true>, a, (int)smem);
-    if (x == cudaSuccess) x = cudaFuncSetAttribute(k_shared<false>, a, (int)smem);
+    cudaError_t x = cudaSuccess;
+    for (auto* k : {k_shared<true, false>, k_shared<false, false>, k_shared<true, true>, k_shared<false, true>})
+      if (x == cudaSuccess) x = cudaFuncSetAttribute(k, a, (int)smem);
     if (x == cudaSuccess) x = cudaFuncSetAttribute(k_shared_plan, a, (int)sizeof(HPlanSmem));
     return x;
   });
@@ -1564,7 +1519,8 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
   pa.G = G;
   pa.T = T;
   pa.max_len = p.max_pages_per_seq * p.page_size;
-  pa.causal = p.causal;
+  pa.causal = tree_words ? 0 : p.causal;
+  pa.tree_words = tree_words;
   pa.ctas = ctas;
   e = launch_pdl(k_shared_plan, dim3(1), dim3(kHPlanThreads), sizeof(HPlanSmem), st, pa);
   if (e != cudaSuccess) return e;
@@ -1582,8 +1538,11 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
   fa.causal = p.causal;
   const float scale = p.softmax_scale > 0.f ? p.softmax_scale : 0.08838834764831845f;  // 1/sqrt(128)
   fa.scale_log2 = scale * 1.4426950408889634f;
-  e = launch_pdl(bf16 ? k_shared<true> : k_shared<false>, dim3(ctas), dim3(kHThreads), smem, st, tmq, tmq1, tmk, tmv,
-                 fa);
+  fa.tree_mask = tree_mask;
+  fa.tree_words = tree_words;
+  auto* kern = tree_words ? (bf16 ? k_shared<true, true> : k_shared<false, true>)
+                          : (bf16 ? k_shared<true, false> : k_shared<false, false>);
+  e = launch_pdl(kern, dim3(ctas), dim3(kHThreads), smem, st, tmq, tmq1, tmk, tmv, fa);
   if (e != cudaSuccess) return e;
 
   HJoinArgs ja{};

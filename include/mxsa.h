@@ -79,6 +79,8 @@ typedef enum { MXSA_BF16 = 0, MXSA_FP16 = 1, MXSA_FP8_E4M3 = 2, MXSA_NVFP4 = 3 }
 #define MXSA_FLAG_CU 128        /* cu_seqlens_q is not a non-decreasing partition of total_q */
 #define MXSA_FLAG_POS 256       /* a token's position lies past the rotation table: token left out */
 #define MXSA_FLAG_GROUP 512     /* group_ptr is not a non-decreasing list of sequences: groups ignored */
+#define MXSA_FLAG_TREE 1024     /* a drafted tree's parents, path or mask width do not fit it */
+#define MXSA_FLAG_PAGES 2048    /* free list with too few pages, or one that does not fit: nothing given out */
 
 /* Problem description (sizes and flags of one call).  The sources: the
  * Quick-start signature and the supported-feature list of the
@@ -289,6 +291,145 @@ mxsa_status mxsa_dense_shared_fwd(const mxsa_problem* problem, const void* q, co
                                   const int32_t* used_kv_lens, int32_t num_groups, const int32_t* group_ptr,
                                   const int32_t* prefix_lens, void* ws, size_t shared_bytes, void* out, float* lse,
                                   int32_t* device_flags, void* stream);
+
+/* Attention of drafted token trees over the paged cache, the verification
+ * step of speculative decoding (this library's own; the plain dense path is
+ * mxsa_dense_shared_fwd).  A sequence's Tq_s new tokens are the nodes of a
+ * tree (or of several) whose keys already stand in the cache, in the order of
+ * the tokens, behind its base_s = L - Tq_s committed ones.  Token i of s sees
+ *   every key p < base_s, and key base_s + j when bit j % 32 of
+ *   tree_mask[t][j / 32] is set (its ancestors' and its own bit, as
+ *   mxsa_tree_mask writes them, or any other set),
+ * and out, lse are mxsa_dense_fwd's over those keys (none: out 0, lse -inf).
+ * tree_mask is device uint32 [total_q][mask_words], 1 <= mask_words <= 64; a
+ * sequence of more than 32 * mask_words new tokens sets MXSA_FLAG_TREE, and
+ * the further ones' keys are seen by no row.  L < Tq_s sets
+ * MXSA_FLAG_CAUSAL_LEN; the first Tq_s - L tokens then have no key.
+ * Everything else is mxsa_dense_shared_fwd's: the groups (each prefix at most
+ * the smallest base_s of the group's sequences with new tokens), the workspace
+ * (mxsa_shared_workspace_size), limits, types, roundings and flags;
+ * problem->causal is not used.  The V rows of drafted keys that a row does not
+ * see, but others of its sequence do, have to be finite.  Three launches,
+ * asynchronous on `stream`. */
+mxsa_status mxsa_tree_fwd(const mxsa_problem* problem, const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, const int64_t* cu_seqlens_q, const int32_t* used_kv_lens,
+                          const uint32_t* tree_mask, int32_t mask_words, int32_t num_groups,
+                          const int32_t* group_ptr, const int32_t* prefix_lens, void* ws, size_t shared_bytes,
+                          void* out, float* lse, int32_t* device_flags, void* stream);
+
+/* Masks and positions of drafted trees (this library's own).  parents[t] is
+ * the index of token t's parent among its sequence's new tokens, smaller than
+ * t's own, or -1 for a token that follows the last committed one.
+ *   tree_mask[t][w]: bit j of word w set when new token 32 w + j of the
+ *                    sequence is t or an ancestor of t
+ *   positions[t]   = used_kv_lens[s] - Tq_s + (number of t's ancestors), the
+ *                    position that its rotation takes (NULL to skip it)
+ *   parents        device int32 [total_q]
+ *   positions      device int64 [total_q]
+ * A parent outside [-1, own index) sets MXSA_FLAG_TREE and stands for -1; a
+ * sequence of more than 32 * mask_words tokens (1..64 words) sets it too, its
+ * further tokens' bits left out.  MXSA_FLAG_LEN and MXSA_FLAG_CAUSAL_LEN as for
+ * the calls that read the lengths (clamped; L < Tq_s: positions below zero).
+ * Tokens before cu_seqlens_q[0] and from cu_seqlens_q[B] on are not written;
+ * cu_seqlens_q out of order: MXSA_FLAG_CU and nothing is.  Of the problem the
+ * call reads num_seqs (<= 1024), total_q, page_size and max_pages_per_seq.
+ * One launch, asynchronous on `stream`. */
+mxsa_status mxsa_tree_mask(const mxsa_problem* problem, const int32_t* parents, const int64_t* cu_seqlens_q,
+                           const int32_t* used_kv_lens, int32_t mask_words, uint32_t* tree_mask, int64_t* positions,
+                           int32_t* device_flags, void* stream);
+
+/* The accepted tokens of drafted trees moved to their places (this library's
+ * own): for each sequence s, with base_s = used_kv_lens[s] - Tq_s and the
+ * accepted path p_0 < p_1 < ... of path_lens[s] token indices in path[s],
+ * the K and V rows of every kv head (and the index keys' of every index head)
+ * at position base_s + p_k become those at base_s + k, and
+ *   kv_lens_out[s] = base_s + path_lens[s].
+ * The result is that of reading every row before any is written.  Any cache
+ * type; rows are copied as they are.  One call per layer's caches.
+ *   path        device int32 [B][max_path], read up to path_lens[s]
+ *   path_lens   device int32 [B], 0 .. max_path
+ *   idx_cache   as for mxsa_store_kv, or NULL (idx_heads, idx_dim unused)
+ *   kv_lens_out device int32 [B], not used_kv_lens itself, or NULL
+ * A path that is not ascending within [0, Tq_s), or longer than max_path, sets
+ * MXSA_FLAG_TREE; a length out of range MXSA_FLAG_LEN or, below Tq_s,
+ * MXSA_FLAG_CAUSAL_LEN; cu_seqlens_q out of order MXSA_FLAG_CU: of such a
+ * sequence nothing is moved, and kv_lens_out[s] is what is committed of it (0
+ * at least).  A row whose page lies outside the cache is not moved
+ * (MXSA_FLAG_PAGE).  Sequences must not share the pages that hold their
+ * drafted tokens.  One launch, asynchronous on `stream`. */
+mxsa_status mxsa_tree_commit(const mxsa_problem* problem, const int64_t* cu_seqlens_q, const int32_t* used_kv_lens,
+                             const int32_t* block_tables, const int32_t* path, int32_t max_path,
+                             const int32_t* path_lens, void* k_cache, void* v_cache, void* idx_cache,
+                             int32_t idx_heads, int32_t idx_dim, int32_t* kv_lens_out, int32_t* device_flags,
+                             void* stream);
+
+/* Attention of whole prompts that have no cache yet (this library's own; the
+ * paged form is mxsa_dense_fwd): sequence s is the tokens cu_seqlens[s] <= t <
+ * cu_seqlens[s + 1] of q, k and v alike, and
+ *   out[t][h][:] = sum_u softmax_u(scale * q[t][h] . k[u][g]) v[u][g],
+ *   lse[h][t]    = log sum_u exp(scale * q[t][h] . k[u][g]),  g = h / G,
+ * over its tokens u (u <= t when problem->causal).  q is [total_q][Hq][128], k
+ * and v [total_q][Hkv][128] in q_dtype, a token's heads next to each other and
+ * the tokens *_stride elements apart (a multiple of 8, at least heads * 128),
+ * so they may be views of one packed projection; out [total_q][Hq][128] in
+ * q_dtype and lse [Hq][total_q] (or NULL) are dense and overlap no input.
+ *   ws   device, prompt_bytes from mxsa_prompt_workspace_size: the order of
+ *        the work; needs no initialisation, keeps nothing between calls.  Two
+ *        calls that may run at the same time need one each.
+ * The softmax weights are rounded to q_dtype before they multiply V,
+ * everything else is FP32; the same call gives the same bits.  NaN and
+ * infinities of one sequence do not reach another; under causal masking the V
+ * rows of a sequence's later tokens have to be finite.  kv_dtype must equal
+ * q_dtype; num_seqs <= 1024; topk and the pages of the problem are not used.
+ * Tokens before cu_seqlens[0] and from cu_seqlens[B] on are not written;
+ * cu_seqlens out of order: MXSA_FLAG_CU in device_flags (may be NULL) and
+ * nothing is written (MXSA_FLAG_TIMEOUT as everywhere).  Device pointers,
+ * 16-byte aligned (ws 256).  One or two launches, asynchronous on `stream`. */
+mxsa_status mxsa_prompt_workspace_size(const mxsa_problem* problem, size_t* prompt_bytes);
+mxsa_status mxsa_prompt_fwd(const mxsa_problem* problem, const void* q, int64_t q_stride, const void* k,
+                            int64_t k_stride, const void* v, int64_t v_stride, const int64_t* cu_seqlens, void* ws,
+                            size_t prompt_bytes, void* out, float* lse, int32_t* device_flags, void* stream);
+
+/* A serving step's tables, built on the GPU from the requests' lengths (this
+ * library's own): what every paged call above takes.  Request s has kv_lens[s]
+ * tokens in the cache, in pages_held[s] pages (the first entries of its row of
+ * block_tables), and new_lens[s] >= 0 new ones in this step; new_lens[s] < 0:
+ * it is finished.
+ *   1. The pages of finished requests go back to the free list, behind its
+ *      free_count[0] pages, in the order of the requests and of their rows.
+ *   2. Every other request gets the pages that its kv_lens[s] + new_lens[s]
+ *      tokens need beyond pages_held[s], in the order of the requests: the
+ *      list's last page first, each into the next entry of its row.
+ *   3. cu_seqlens_q = the running sums of the new tokens (0 of a finished
+ *      request); used_kv_lens[s] = kv_lens[s] + new_lens[s] (finished: 0);
+ *      positions[t] = kv_lens[s] + i and loc[t] = its slot page * page_size +
+ *      offset for token t = cu_seqlens_q[s] + i; -1 in both from
+ *      cu_seqlens_q[B] to total_q (padding to the calls that take them).
+ *      pages_held_out and free_count_out: what the requests hold now, and the
+ *      list's new length.
+ *   kv_lens, new_lens, pages_held   device int32 [B]
+ *   block_tables   device int32 [B][max_pages_per_seq] (updated)
+ *   free_pages     device int32 [num_pages] (updated)
+ *   free_count     device int32 [1]
+ *   cu_seqlens_q   device int64 [B + 1]; used_kv_lens, pages_held_out device
+ *                  int32 [B]; positions, loc device int64 [total_q]
+ *                  (total_q: the step's capacity); free_count_out int32 [1]
+ * used_kv_lens may be kv_lens, pages_held_out pages_held and free_count_out
+ * free_count; otherwise no two arrays overlap.  When the new tokens are more
+ * than total_q (MXSA_FLAG_CU), a length, a held count or a row does not fit
+ * (MXSA_FLAG_LEN: kv_lens[s] < 0 or beyond the held pages, pages_held[s]
+ * outside [0, max_pages_per_seq], more tokens than a row's pages hold), or the
+ * list has too few pages or would outgrow num_pages (MXSA_FLAG_PAGES), no page
+ * moves: cu_seqlens_q is all 0, positions and loc all -1, the lengths, held
+ * counts and list as they came.  A slot in a page outside [0, num_pages) is -1
+ * (MXSA_FLAG_PAGE).  Of the problem the call reads num_seqs (<= 1024), total_q,
+ * page_size, num_pages and max_pages_per_seq.  positions and loc 16-byte
+ * aligned.  One or two launches, asynchronous on `stream`. */
+mxsa_status mxsa_build_tables(const mxsa_problem* problem, const int32_t* kv_lens, const int32_t* new_lens,
+                              const int32_t* pages_held, int32_t* block_tables, int32_t* free_pages,
+                              const int32_t* free_count, int64_t* cu_seqlens_q, int32_t* used_kv_lens,
+                              int64_t* positions, int64_t* loc, int32_t* pages_held_out, int32_t* free_count_out,
+                              int32_t* device_flags, void* stream);
 
 /* Paged-cache store, the write side of the caches the forward reads (a
  * sglang pull request on these pages, "Summary": the fused K/V/index store
