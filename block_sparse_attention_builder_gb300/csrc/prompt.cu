@@ -29,6 +29,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "internal.h"
 #include "mma_tiles.cuh"
@@ -40,10 +41,13 @@ namespace {
 
 constexpr int kRMaxSeqs = 1024;
 constexpr int kRThreads = 384;
-constexpr int kRProducer = 8, kRMma = 9, kRQuery = 11;
+constexpr int kRProducer = 0, kRQuery = 1, kRMma = 2;  // warps 2, 3: the issuers of groups 0, 1
 constexpr uint32_t kRTile = 32768;  // 128 rows x 128 x 16-bit
 constexpr int kRStages = 5, kRWork = 2;
-constexpr float kRRescale = 8.f;    // log2 units
+// How far (log2 units) a row's scores may pass the reference m before it is
+// raised; in the second half of a block it may wait for the next block up to
+// kRLag (fp16 holds 2^15).
+constexpr float kRRescale = 8.f, kRLag = 14.f;
 constexpr uint32_t kROffKV = 2 * kRTile;
 constexpr uint32_t kROffCtrl = kROffKV + kRStages * kRTile;
 
@@ -59,7 +63,7 @@ struct RHeader {
 };
 
 struct RCtrl {
-  uint64_t q_full[2], q_empty[2], kv_full[kRStages], kv_empty[kRStages];
+  uint64_t q_full[2], q_empty[2], kv_full[2 * kRStages], kv_empty[kRStages];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], work_full[kRWork], work_empty[kRWork], done;
   RTile work[kRWork];
   uint32_t tmem_base;
@@ -192,38 +196,50 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// P = 2^(S * scale - m) of a row over S, packed; returns its sum.
+// P = 2^(S * scale - m) of 64 keys of a row, packed, to TMEM; returns their
+// sum, and the largest S in `most`.
 template <bool kBf16>
-__device__ __forceinline__ float exp_row(const float* sv, float scale_log2, float m, uint32_t tP) {
+__device__ __forceinline__ float exp_half(const float* sv, float scale_log2, float m, uint32_t tP, float* most) {
   const uint64_t scale2 = pack_f2(scale_log2, scale_log2), off2 = pack_f2(-m, -m);
   uint64_t l0 = pack_f2(0.f, 0.f), l1 = l0;
+  float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < 2; ++q) {
     uint32_t pk[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      const float2 x = unpack_f2(fma_f2(pack_f2(sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]), scale2, off2));
+      const float s0 = sv[32 * q + 2 * k], s1 = sv[32 * q + 2 * k + 1];
+      const float2 x = unpack_f2(fma_f2(pack_f2(s0, s1), scale2, off2));
       const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
       if (k & 1) l1 = add_f2(l1, pack_f2(p0, p1));
       else l0 = add_f2(l0, pack_f2(p0, p1));
+      if (k & 1) b1 = hmax3(b1, s0, s1);
+      else b0 = hmax3(b0, s0, s1);
       pk[k] = hpack2<kBf16>(p0, p1);
     }
     tmem_st16(tP + 16 * q, pk);
   }
   const float2 ls = unpack_f2(add_f2(l0, l1));
+  *most = fmaxf(b0, b1);
   return ls.x + ls.y;
 }
 
-__device__ __forceinline__ float max_row(const float* sv) {
-  float b0 = -INFINITY, b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
+// The first 64 keys' P of the thread's row times f, a power of two.  Rarely run.
+template <bool kBf16>
+__device__ __forceinline__ void scale_p(uint32_t tP, float f) {
+#pragma unroll 1
+  for (int q = 0; q < 2; ++q) {
+    uint32_t w[16];
+    tmem_ld16(tP + 16 * q, w);
+    tmem_ld_wait();
 #pragma unroll
-  for (int k = 0; k < 128; k += 8) {
-    b0 = hmax3(b0, sv[k], sv[k + 1]);
-    b1 = hmax3(b1, sv[k + 2], sv[k + 3]);
-    b2 = hmax3(b2, sv[k + 4], sv[k + 5]);
-    b3 = hmax3(b3, sv[k + 6], sv[k + 7]);
+    for (int k = 0; k < 16; ++k) {
+      const float2 x = kBf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]))
+                             : __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      w[k] = hpack2<kBf16>(x.x * f, x.y * f);
+    }
+    tmem_st16(tP + 16 * q, w);
   }
-  return fmaxf(fmaxf(b0, b1), fmaxf(b2, b3));
 }
 
 template <bool kBf16>
@@ -246,13 +262,14 @@ __global__ void __launch_bounds__(kRThreads, 1)
     }
     for (int i = 0; i < kRStages; ++i) {
       mbar_init(&c.kv_full[i], 1);
-      mbar_init(&c.kv_empty[i], 1);
+      mbar_init(&c.kv_full[i + kRStages], 1);
+      mbar_init(&c.kv_empty[i], 2);  // (see the issuers)
     }
     for (int i = 0; i < kRWork; ++i) {
       mbar_init(&c.work_full[i], 1);
-      mbar_init(&c.work_empty[i], 10);  // the issuer's, the q warp and the softmax groups' warps
+      mbar_init(&c.work_empty[i], 11);  // the q warp, the issuers and the softmax groups' warps
     }
-    mbar_init(&c.done, 1);
+    mbar_init(&c.done, 2);
     c.abort_flag = 0;
     c.local_flags = 0;
     fence_mbar_init();
@@ -284,7 +301,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
   };
 
   // 384 x 168 registers at launch: 256 x 208 for the softmax, 128 x 88 for the others
-  if (warp >= 8) {
+  if (warp < 4) {
     regs_down<88>();
     if (warp == kRProducer) {
       // -------------------------------------------------------------- producer
@@ -364,9 +381,10 @@ __global__ void __launch_bounds__(kRThreads, 1)
             uint8_t* dst = sm + kROffKV + st * kRTile;
             const int row = t.key0 + (p >> 1) * 128;
             const CUtensorMap* tm = p & 1 ? &tmv : &tmk;
-            mbar_arrive_expect_tx(&c.kv_full[st], kRTile);
-            tma_load_3d(dst, tm, &c.kv_full[st], 0, t.g, row);
-            tma_load_3d(dst + 16384, tm, &c.kv_full[st], 64, t.g, row);
+            uint64_t* full = &c.kv_full[at % (2 * kRStages)];
+            mbar_arrive_expect_tx(full, kRTile);
+            tma_load_3d(dst, tm, full, 0, t.g, row);
+            tma_load_3d(dst + 16384, tm, full, 64, t.g, row);
           }
         }
         ok = hwarp_all(ok);
@@ -376,19 +394,19 @@ __global__ void __launch_bounds__(kRThreads, 1)
       at = __shfl_sync(0xffffffffu, at, 0);
       if (lane == 0)  // drain: the copies in flight land before the CTA may exit
         for (int k = max(0, at - kRStages); k < at; ++k)
-          mbar_drain(&c.kv_full[k % kRStages], (k / kRStages) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
+          mbar_drain(&c.kv_full[k % (2 * kRStages)], (k / (2 * kRStages)) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
       __syncwarp();
     } else if (warp == kRQuery) {
       // --------------------------------------------------------------- queries
       if (lane == 0) tma_prefetch_desc(&tmq);
-      int nq[2] = {0, 0};
+      int nq0 = 0, nq1 = 0;
       bool ok = true;
       RTile t;
       while (ok && next_tile(&t)) {
         for (int h = 0; h < 2; ++h) {
           if (h && t.n1 == 0) break;
           ok = hwarp_all(
-              mbar_wait(&c.q_empty[h], (nq[h] & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
+              mbar_wait(&c.q_empty[h], ((h ? nq1 : nq0) & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
           if (!ok) break;
           if (lane == 0) {  // one box; rows past the half's tokens are never used
             uint8_t* qd = sm + h * kRTile;
@@ -396,68 +414,83 @@ __global__ void __launch_bounds__(kRThreads, 1)
             tma_load_3d(qd, &tmq, &c.q_full[h], 0, t.g * a.G, t.key0 + t.t0 + h * a.T);
             tma_load_3d(qd + 16384, &tmq, &c.q_full[h], 64, t.g * a.G, t.key0 + t.t0 + h * a.T);
           }
-          ++nq[h];
+          (h ? nq1 : nq0) += 1;
         }
       }
-      if (lane == 0)
-        for (int h = 0; h < 2; ++h)
-          if (nq[h]) mbar_drain(&c.q_full[h], (nq[h] - 1) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
+      if (lane == 0) {
+        if (nq0) mbar_drain(&c.q_full[0], (nq0 - 1) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
+        if (nq1) mbar_drain(&c.q_full[1], (nq1 - 1) & 1, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs);
+      }
       __syncwarp();
-    } else if (warp == kRMma) {
-      // ----------------------------------------------------------------- MMAs
-      // The whole warp walks the loop and one elected lane issues.
+    } else {
+      // --------------------------------------------------------- MMA issuers
+      // One warp per group: while it stands at its group's softmax the pipe has
+      // the other group's products, and what it does between its own (some
+      // hundred cycles) is under them.  The whole warp walks the loop and one
+      // elected lane issues, so that what the instructions take from uniform
+      // registers is known to be uniform.
+      const int h = warp - kRMma;
       const uint32_t id_qk = idesc_f16(128, 128, kBf16 ? 1u : 0u, 0, 0);
       const uint32_t id_pv = idesc_f16(128, 128, kBf16 ? 1u : 0u, 0, 1);
-      int at = 0;                              // ring place of the tile's first block
-      int nt[2] = {0, 0}, np[2] = {0, 0};      // tiles and P V products of each group
+      const uint32_t tS = uniform(tmem + h * 256);
+      const uint32_t dq = uniform(desc_k_major(sbase + h * kRTile));
+      const uint32_t dk0 = desc_k_major(sbase + kROffKV), dv0 = desc_mn_major(sbase + kROffKV);
+      int st = 0, full = 0, par = 0;  // the next ring place: stage, full barrier and its parity
+      int np = 0, nt = 0;             // P V products and tiles of the group
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) {
         ok = ok && hwarp_all(mbar_wait(bar, parity, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
       };
+      auto pass = [&] {
+        if (++st == kRStages) st = 0;
+        if (++full == 2 * kRStages) full = 0, par ^= 1;
+      };
       RTile t;
       while (ok && next_tile(&t)) {
-        const int n[2] = {t.n0, t.n1}, blocks = max(t.n0, t.n1), last = t.n1 > 0 ? 1 : 0;
-        for (int i = 0; i <= blocks && ok; ++i) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t tS = uniform(tmem + h * 256);
-            const int pk = at + 2 * i, pv = pk - 1;  // ring places: K of this block, V of the one before
-            if (i > 0 && i <= n[h]) {
-              wait(&c.kv_full[pv % kRStages], (pv / kRStages) & 1);
-              if (i == 1 && nt[h] > 0) wait(&c.o_empty[h], (nt[h] - 1) & 1);
-              wait(&c.p_full[h], np[h] & 1);
-              if (!ok) break;
-              ++np[h];
-              const uint32_t dv = uniform(desc_mn_major(sbase + kROffKV + (pv % kRStages) * kRTile));
-              tc_fence_after();
-              if (elect_one()) {
-                mma_pv_lo(tS + 128, tS, dv, id_pv, i > 1);
-                mma_pv_hi(tS + 128, tS, dv, id_pv);
-                if (h == last) mma_commit(&c.kv_empty[pv % kRStages]);
-                if (i == n[h]) mma_commit(&c.o_full[h]);
-              }
-              __syncwarp();
+        const int n = h ? t.n1 : t.n0, blocks = max(t.n0, t.n1);
+        for (int i = 0; n > 0 && i <= n && ok; ++i) {
+          // Two arrivals free a stage: one of each group, or both of the only
+          // one that reads it.
+          const bool alone_v = h ? i - 1 >= t.n0 : t.n1 == 0, alone_k = h ? i >= t.n0 : t.n1 == 0;
+          int vs = 0, ks = 0;
+          if (i > 0) {  // V of the block before
+            vs = st;
+            wait(&c.kv_full[full], par);
+            pass();
+          }
+          if (i < n) {
+            ks = st;
+            wait(&c.kv_full[full], par);
+            pass();
+          }
+          const uint32_t dv = uniform(dv0 + vs * (kRTile >> 4)), dk = uniform(dk0 + ks * (kRTile >> 4));
+          if (i == 0) wait(&c.q_full[h], nt & 1);
+          if (i == 1 && nt > 0) wait(&c.o_empty[h], (nt - 1) & 1);
+          if (i > 0) wait(&c.p_full[h], np++ & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (i > 0) {
+              mma_pv_lo(tS + 128, tS, dv, id_pv, i > 1);
+              mma_pv_hi(tS + 128, tS, dv, id_pv);
+              if (i == n) mma_commit(&c.o_full[h]);
             }
-            if (i < n[h]) {
-              if (i == 0) wait(&c.q_full[h], nt[h] & 1);
-              wait(&c.kv_full[pk % kRStages], (pk / kRStages) & 1);
-              if (!ok) break;
-              const uint32_t dq = uniform(desc_k_major(sbase + h * kRTile));
-              const uint32_t dk = uniform(desc_k_major(sbase + kROffKV + (pk % kRStages) * kRTile));
-              tc_fence_after();
-              if (elect_one()) {
-                mma_qk(tS, dq, dk, id_qk);
-                mma_commit(&c.s_full[h]);
-                if (h == last) mma_commit(&c.kv_empty[pk % kRStages]);
-                if (i == n[h] - 1) mma_commit(&c.q_empty[h]);
-              }
-              __syncwarp();
+            if (i < n) {
+              mma_qk(tS, dq, dk, id_qk);
+              mma_commit(&c.s_full[h]);
+              mma_commit(&c.kv_empty[ks]);
+              if (alone_k) mma_commit(&c.kv_empty[ks]);
+              if (i == n - 1) mma_commit(&c.q_empty[h]);
+            }
+            if (i > 0) {
+              mma_commit(&c.kv_empty[vs]);
+              if (alone_v) mma_commit(&c.kv_empty[vs]);
             }
           }
+          __syncwarp();
         }
-        at += 2 * blocks;
-        ++nt[0];
-        if (t.n1 > 0) ++nt[1];
+        for (int p = 2 * n; p < 2 * blocks; ++p) pass();
+        if (n > 0) ++nt;
       }
       if (elect_one()) {
         mma_commit(&c.done);
@@ -468,7 +501,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
   } else {
     // --------------------------------------------------------------- softmax
     regs_up<208>();
-    const int h = warp >> 2, r = tid & 127;  // row of the half == TMEM lane
+    const int h = (warp >> 2) - 1, r = tid & 127;  // row of the half == TMEM lane
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + h * 256 + lane_addr, tO = tS + 128;
     const int rt = r / a.G, tt = h * a.T + rt, hh = r - rt * a.G;
@@ -485,7 +518,8 @@ __global__ void __launch_bounds__(kRThreads, 1)
       // keys that the row sees (padding rows see all: nobody reads them)
       const int see = live ? (a.causal ? t.t0 + tt + 1 : t.len) : INT_MAX;
       const int warp_see = __reduce_min_sync(0xffffffffu, see);
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, bm = -INFINITY;
+      bool late = false;  // the block before passed m by more than kRRescale, and by kRLag at most
       for (int i = 0; i < n && ok; ++i, ++n_s) {
         const int k0 = i << 7;
         ok = hwarp_all(mbar_wait(&c.s_full[h], n_s & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
@@ -495,8 +529,8 @@ __global__ void __launch_bounds__(kRThreads, 1)
           // NaN and 0 * NaN would reach O (the writers' proxy fence orders them
           // before the product)
           const int pl = at0 + 2 * i + 1, st = pl % kRStages;
-          ok = hwarp_all(mbar_wait(&c.kv_full[st], (pl / kRStages) & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT,
-                                   kWaitLimitNs));
+          ok = hwarp_all(mbar_wait(&c.kv_full[pl % (2 * kRStages)], (pl / (2 * kRStages)) & 1, abort_flag, fl,
+                                   MXSA_FLAG_TIMEOUT, kWaitLimitNs));
           if (!ok) break;
           if (k0 + r >= t.len) {
             const uint32_t vs = sbase + kROffKV + st * kRTile + r * 128;
@@ -507,37 +541,48 @@ __global__ void __launch_bounds__(kRThreads, 1)
         }
         if (warp_live) {
           tc_fence_after();
-          float sv[128];
+#pragma unroll 1
+          for (int hf = 0; hf < 2; ++hf) {
+            float sv[64];
+            tmem_ld32(tS + 64 * hf, sv);
+            tmem_ld32(tS + 64 * hf + 32, sv + 32);
+            tmem_ld_wait();
+            const int kh = k0 + 64 * hf;
+            bool up = late;  // (the same in every lane) rows have passed m
+            if (kh + 64 > warp_see || kh == 0) {  // masked keys, or no maximum yet
+              float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, sv + 32 * q);
-          tmem_ld_wait();
-          bool known = i == 0 || k0 + 128 > warp_see;  // the block's maximum comes first
-          if (k0 + 128 > warp_see) {
-            const int lim = see - k0;
-#pragma unroll
-            for (int k = 0; k < 128; ++k) sv[k] = k < lim ? sv[k] : -INFINITY;
-          }
-          float bm = known ? max_row(sv) * a.scale_log2 : -INFINITY;
-          float sum;
-          while (true) {
-            if (known) {
-              const bool raise = bm > m + kRRescale || (m == -INFINITY && bm > -INFINITY);
-              if (__any_sync(0xffffffffu, raise)) {
-                const float f = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - bm)) : 1.f;
-                if (i > 0) scale_o(tO, f);  // (complete: S's barrier follows every product issued before)
+              for (int k = 0; k < 64; k += 2) {
+                sv[k] = kh + k < see ? sv[k] : -INFINITY;
+                sv[k + 1] = kh + k + 1 < see ? sv[k + 1] : -INFINITY;
+                if (k & 2) b1 = hmax3(b1, sv[k], sv[k + 1]);
+                else b0 = hmax3(b0, sv[k], sv[k + 1]);
+              }
+              bm = fmaxf(late ? bm : -INFINITY, fmaxf(b0, b1) * a.scale_log2);
+              up = __any_sync(0xffffffffu, bm > m + kRRescale);
+            }
+            float sum;
+            while (true) {
+              if (up) {
+                tmem_st_wait();
+                const bool raise = bm > m + kRRescale;
+                const float to = ceilf(bm), f = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - to)) : 1.f;
+                // O is complete: S's barrier follows every product issued before
+                if (i > 0) scale_o(tO, f);
+                if (hf) scale_p<kBf16>(tS, f);
                 if (raise) {
                   l *= f;
-                  m = bm;
+                  m = to;
                 }
               }
+              sum = exp_half<kBf16>(sv, a.scale_log2, m == -INFINITY ? 0.f : m, tS + 32 * hf, &bm);
+              bm *= a.scale_log2;
+              up = late = __any_sync(0xffffffffu, bm > m + kRRescale);
+              if (!up) break;
+              if (hf && !__any_sync(0xffffffffu, bm > m + kRLag)) break;
             }
-            sum = exp_row<kBf16>(sv, a.scale_log2, m == -INFINITY ? 0.f : m, tS);
-            if (known) break;
-            bm = max_row(sv) * a.scale_log2;
-            known = true;
-            if (!__any_sync(0xffffffffu, bm > m + kRRescale)) break;
+            l += sum;
           }
-          l += sum;
           tmem_st_wait();
         }
         tc_fence_before();
