@@ -5,23 +5,36 @@
 // A tile is 2T tokens (T = 128 / G) x the G query heads of one kv head of one
 // sequence: two halves of up to 128 (token, head) rows that share every
 // 128-key block of K and V.  Persistent, one CTA per SM, 384 threads:
-//   warps 0-3, 4-7  softmax groups, one per half: thread = TMEM lane = row.
-//   warp 8     producer: claims tiles, K and V blocks into a ring of five
+//   warp 0     producer: claims tiles, K and V blocks into a ring of five
 //              32 KB stages in the order K0 V0 K1 V1 ...
-//   warp 9     MMA issuer: for each block P V of the one before and q k^T of
-//              this one, group 0's two products and then group 1's, so that
-//              each group's softmax runs under the other's products.  S is
-//              overwritten by the product after the one that reads P from it;
-//              one thread issues both, and the pipe keeps their order.
-//   warp 11    q halves.
+//   warp 1     q halves.
+//   warps 2, 3 MMA issuers, one per group: P V of a block (its first 64 keys
+//              once their P is there) and q k^T of the next one, in turns, so
+//              that each group's softmax runs under the other's products.  S
+//              is overwritten by the product after the one that reads P from
+//              it; one thread issues both, and the pipe keeps their order.
+//   warps 4-7, 8-11  softmax groups, one per half: thread = TMEM lane = row.
 // TMEM: S (P over it) and O of each group, 512 columns.
 //
-// Softmax of a block.  S = 128 scores of a row in registers.  Where every key
-// is visible P = 2^(S - m) is made with the running maximum m of the blocks
-// before while the block's own maximum is found beside it; only if a row
-// passes m by 2^8 (rare past the first blocks) is m raised, O in TMEM rescaled
-// and P made again.  So the maximum is not in the way of the exponentials.
-// First and masked blocks find their maximum first.
+// Softmax of a block, 64 keys at a time.  P = 2^(S - m) is made with the
+// reference m of the blocks before while the keys' own maximum is found beside
+// it; only when a row passes m by 2^8 (rare past the first blocks) is m raised,
+// O in TMEM rescaled and P made again.  So neither the maximum nor a second
+// reading of S is in the way of the exponentials.  First and masked blocks find
+// their maximum first.
+//
+// Bound: a group's chain of softmax (1400 cycles a block, one warp of the group
+// per scheduler at a time: 64 exponentials of 32 rows take 256 of the 590 that
+// their code takes), its hand-overs (230 and 300) and its products (1024); with
+// both groups in turn 2870 cycles a block pair, of which the tensor pipe works
+// 2048.  8192 tokens of 64 + 8 heads, causal: 681 us, 1.61 PFLOP/s; 16384: 2.56
+// ms, 1.72 PFLOP/s (the SM clock then falls to 1.82 GHz).  On the way there:
+// one issuer for both groups 841 us (its own bookkeeping of 600 cycles a block
+// stood between the products), without turns 731, P handed over whole 747, rows
+// written one to a thread 705.  A row's 128 scores held at once, loads of the
+// second 64 ahead of the first ones' exponentials, a split of the registers
+// between the warps and a hand-over of the turn before q k^T's last products
+// were each slower.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -29,7 +42,6 @@
 
 #include <algorithm>
 #include <climits>
-#include <type_traits>
 
 #include "internal.h"
 #include "mma_tiles.cuh"
@@ -62,9 +74,12 @@ struct RHeader {
   int32_t count, next;  // tiles (times kv heads), the next one to claim
 };
 
+// The full barriers alternate between two for a stage: a role that passes over
+// places of the other half could otherwise take a phase for the one before.
 struct RCtrl {
   uint64_t q_full[2], q_empty[2], kv_full[2 * kRStages], kv_empty[kRStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], work_full[kRWork], work_empty[kRWork], done;
+  uint64_t s_full[2], p_half[2], lo_done[2], p_full[2], o_full[2], o_empty[2], turn[2], done;
+  uint64_t work_full[kRWork], work_empty[kRWork];
   RTile work[kRWork];
   uint32_t tmem_base;
   int32_t abort_flag, local_flags;
@@ -187,15 +202,6 @@ __global__ void __launch_bounds__(kRPlanThreads) k_prompt_plan(RArgs a, RHeader*
 }
 
 // ---------------------------------------------------------------- forward
-template <int kRegs>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
 // P = 2^(S * scale - m) of 64 keys of a row, packed, to TMEM; returns their
 // sum, and the largest S in `most`.
 template <bool kBf16>
@@ -206,16 +212,22 @@ __device__ __forceinline__ float exp_half(const float* sv, float scale_log2, flo
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     uint32_t pk[16];
+    float2 x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      x[k] = unpack_f2(fma_f2(pack_f2(sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]), scale2, off2));
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      const float s0 = sv[32 * q + 2 * k], s1 = sv[32 * q + 2 * k + 1];
-      const float2 x = unpack_f2(fma_f2(pack_f2(s0, s1), scale2, off2));
-      const float p0 = ex2_approx(x.x), p1 = ex2_approx(x.y);
-      if (k & 1) l1 = add_f2(l1, pack_f2(p0, p1));
-      else l0 = add_f2(l0, pack_f2(p0, p1));
-      if (k & 1) b1 = hmax3(b1, s0, s1);
-      else b0 = hmax3(b0, s0, s1);
-      pk[k] = hpack2<kBf16>(p0, p1);
+      x[k].x = ex2_approx(x[k].x);
+      x[k].y = ex2_approx(x[k].y);
+      if (k & 1) b1 = hmax3(b1, sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]);
+      else b0 = hmax3(b0, sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (k & 1) l1 = add_f2(l1, pack_f2(x[k].x, x[k].y));
+      else l0 = add_f2(l0, pack_f2(x[k].x, x[k].y));
+      pk[k] = hpack2<kBf16>(x[k].x, x[k].y);
     }
     tmem_st16(tP + 16 * q, pk);
   }
@@ -224,21 +236,18 @@ __device__ __forceinline__ float exp_half(const float* sv, float scale_log2, flo
   return ls.x + ls.y;
 }
 
-// The first 64 keys' P of the thread's row times f, a power of two.  Rarely run.
-template <bool kBf16>
-__device__ __forceinline__ void scale_p(uint32_t tP, float f) {
-#pragma unroll 1
-  for (int q = 0; q < 2; ++q) {
-    uint32_t w[16];
-    tmem_ld16(tP + 16 * q, w);
-    tmem_ld_wait();
+// The 4 x 4 words that four neighbouring lanes hold, transposed.
+__device__ __forceinline__ void quad_transpose(uint32_t* w, int lane) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float2 x = kBf16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]))
-                             : __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-      w[k] = hpack2<kBf16>(x.x * f, x.y * f);
-    }
-    tmem_st16(tP + 16 * q, w);
+  for (int d = 1; d < 4; d <<= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (!(k & d)) {
+        const uint32_t x = __shfl_xor_sync(0xffffffffu, up ? w[k] : w[k + d], d);
+        if (up) w[k] = x;
+        else w[k + d] = x;
+      }
   }
 }
 
@@ -256,9 +265,12 @@ __global__ void __launch_bounds__(kRThreads, 1)
       mbar_init(&c.q_full[i], 1);
       mbar_init(&c.q_empty[i], 1);
       mbar_init(&c.s_full[i], 1);
-      mbar_init(&c.p_full[i], 4);  // one arrival per warp of the group
+      mbar_init(&c.p_half[i], 4);  // one arrival per warp of the group
+      mbar_init(&c.p_full[i], 4);
+      mbar_init(&c.lo_done[i], 1);
       mbar_init(&c.o_full[i], 1);
       mbar_init(&c.o_empty[i], 4);
+      mbar_init(&c.turn[i], 1);
     }
     for (int i = 0; i < kRStages; ++i) {
       mbar_init(&c.kv_full[i], 1);
@@ -302,7 +314,6 @@ __global__ void __launch_bounds__(kRThreads, 1)
 
   // 384 x 168 registers at launch: 256 x 208 for the softmax, 128 x 88 for the others
   if (warp < 4) {
-    regs_down<88>();
     if (warp == kRProducer) {
       // -------------------------------------------------------------- producer
       if (lane == 0) {
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
       const uint32_t dq = uniform(desc_k_major(sbase + h * kRTile));
       const uint32_t dk0 = desc_k_major(sbase + kROffKV), dv0 = desc_mn_major(sbase + kROffKV);
       int st = 0, full = 0, par = 0;  // the next ring place: stage, full barrier and its parity
-      int np = 0, nt = 0;             // P V products and tiles of the group
+      int np = 0, nt = 0, turns = 0;  // P V products, tiles and turns of the group
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) {
         ok = ok && hwarp_all(mbar_wait(bar, parity, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
@@ -448,7 +459,19 @@ __global__ void __launch_bounds__(kRThreads, 1)
       RTile t;
       while (ok && next_tile(&t)) {
         const int n = h ? t.n1 : t.n0, blocks = max(t.n0, t.n1);
-        for (int i = 0; n > 0 && i <= n && ok; ++i) {
+        // In a tile of two halves the groups take turns at the pipe.  Left alone
+        // they fall into step: both sets of products in the pipe at once, then
+        // both groups in their softmax.
+        const bool both = t.n1 > 0;
+        for (int i = 0; i <= (both ? blocks : n) && ok; ++i) {
+          if (i > n || n == 0) {  // nothing left of this group's: its turns pass
+            if (!both) break;
+            if (h == 1 || turns > 0) wait(&c.turn[h], (turns + h + 1) & 1);
+            ++turns;
+            if (ok && lane == 0) mbar_arrive(&c.turn[h ^ 1]);
+            __syncwarp();
+            continue;
+          }
           // Two arrivals free a stage: one of each group, or both of the only
           // one that reads it.
           const bool alone_v = h ? i - 1 >= t.n0 : t.n1 == 0, alone_k = h ? i >= t.n0 : t.n1 == 0;
@@ -466,21 +489,37 @@ __global__ void __launch_bounds__(kRThreads, 1)
           const uint32_t dv = uniform(dv0 + vs * (kRTile >> 4)), dk = uniform(dk0 + ks * (kRTile >> 4));
           if (i == 0) wait(&c.q_full[h], nt & 1);
           if (i == 1 && nt > 0) wait(&c.o_empty[h], (nt - 1) & 1);
-          if (i > 0) wait(&c.p_full[h], np++ & 1);
+          if (i > 0) wait(&c.p_half[h], np & 1);
+          if (both) {
+            if (h == 1 || turns > 0) wait(&c.turn[h], (turns + h + 1) & 1);
+            ++turns;
+          }
+          if (i > 0) {
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              mma_pv_lo(tS + 128, tS, dv, id_pv, i > 1);
+              mma_commit(&c.lo_done[h]);
+            }
+            __syncwarp();
+            wait(&c.p_full[h], np++ & 1);
+          }
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             if (i > 0) {
-              mma_pv_lo(tS + 128, tS, dv, id_pv, i > 1);
               mma_pv_hi(tS + 128, tS, dv, id_pv);
               if (i == n) mma_commit(&c.o_full[h]);
             }
             if (i < n) {
               mma_qk(tS, dq, dk, id_qk);
+              if (both) mbar_arrive(&c.turn[h ^ 1]);
               mma_commit(&c.s_full[h]);
               mma_commit(&c.kv_empty[ks]);
               if (alone_k) mma_commit(&c.kv_empty[ks]);
               if (i == n - 1) mma_commit(&c.q_empty[h]);
+            } else if (both) {
+              mbar_arrive(&c.turn[h ^ 1]);
             }
             if (i > 0) {
               mma_commit(&c.kv_empty[vs]);
@@ -500,7 +539,6 @@ __global__ void __launch_bounds__(kRThreads, 1)
     }
   } else {
     // --------------------------------------------------------------- softmax
-    regs_up<208>();
     const int h = (warp >> 2) - 1, r = tid & 127;  // row of the half == TMEM lane
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + h * 256 + lane_addr, tO = tS + 128;
@@ -550,13 +588,15 @@ __global__ void __launch_bounds__(kRThreads, 1)
             const int kh = k0 + 64 * hf;
             bool up = late;  // (the same in every lane) rows have passed m
             if (kh + 64 > warp_see || kh == 0) {  // masked keys, or no maximum yet
+              if (kh + 64 > warp_see) {
+#pragma unroll
+                for (int k = 0; k < 64; ++k) sv[k] = kh + k < see ? sv[k] : -INFINITY;
+              }
               float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-              for (int k = 0; k < 64; k += 2) {
-                sv[k] = kh + k < see ? sv[k] : -INFINITY;
-                sv[k + 1] = kh + k + 1 < see ? sv[k + 1] : -INFINITY;
-                if (k & 2) b1 = hmax3(b1, sv[k], sv[k + 1]);
-                else b0 = hmax3(b0, sv[k], sv[k + 1]);
+              for (int k = 0; k < 64; k += 4) {
+                b0 = hmax3(b0, sv[k], sv[k + 1]);
+                b1 = hmax3(b1, sv[k + 2], sv[k + 3]);
               }
               bm = fmaxf(late ? bm : -INFINITY, fmaxf(b0, b1) * a.scale_log2);
               up = __any_sync(0xffffffffu, bm > m + kRRescale);
@@ -564,15 +604,21 @@ __global__ void __launch_bounds__(kRThreads, 1)
             float sum;
             while (true) {
               if (up) {
-                tmem_st_wait();
+                // O is complete up to the block before (S's barrier follows
+                // every product issued before it); in the second half the
+                // first one's product has to be done too
+                if (hf) {
+                  ok = hwarp_all(mbar_wait(&c.lo_done[h], n_s & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
+                  if (!ok) break;
+                  tc_fence_after();
+                }
                 const bool raise = bm > m + kRRescale;
-                const float to = ceilf(bm), f = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - to)) : 1.f;
-                // O is complete: S's barrier follows every product issued before
-                if (i > 0) scale_o(tO, f);
-                if (hf) scale_p<kBf16>(tS, f);
+                const float f = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - bm)) : 1.f;
+                tmem_st_wait();
+                if (kh > 0) scale_o(tO, f);
                 if (raise) {
                   l *= f;
-                  m = to;
+                  m = bm;
                 }
               }
               sum = exp_half<kBf16>(sv, a.scale_log2, m == -INFINITY ? 0.f : m, tS + 32 * hf, &bm);
@@ -581,13 +627,17 @@ __global__ void __launch_bounds__(kRThreads, 1)
               if (!up) break;
               if (hf && !__any_sync(0xffffffffu, bm > m + kRLag)) break;
             }
+            if (!ok) break;
             l += sum;
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(hf ? &c.p_full[h] : &c.p_half[h]);
           }
-          tmem_st_wait();
+        } else if (lane == 0) {
+          mbar_arrive(&c.p_half[h]);
+          mbar_arrive(&c.p_full[h]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.p_full[h]);
       }
       if (!ok) break;
       // ---- the half's output rows
@@ -597,25 +647,36 @@ __global__ void __launch_bounds__(kRThreads, 1)
       if (warp_live) {
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN stays one)
-        const size_t tok = (size_t)t.key0 + t.t0 + tt;
-        uint8_t* orow = a.out + (tok * a.Hq + (size_t)t.g * a.G + hh) * 256;
-#pragma unroll
-        for (int cb = 0; cb < 4; ++cb) {
-          float ov[32];
-          tmem_ld32(tO + cb * 32, ov);  // every lane: the load is warp-collective
+        // 16 rows and 64 columns at a time, a row's columns spread over four
+        // lanes, which then exchange words until each has 16 consecutive bytes:
+        // a store then covers 64 bytes of 8 rows.  (With a row to a thread it
+        // touches 32 rows, and the eight warps' stores take 4000 cycles.)
+#pragma unroll 1
+        for (int part = 0; part < 4; ++part) {
+          const int r0 = (part >> 1) * 16, c0 = (part & 1) * 64;
+          float v[32];
+          tmem_ld16x256b_x8(tO + ((uint32_t)r0 << 16) + c0, v);
           tmem_ld_wait();
-          if (live) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
+          for (int x = 0; x < 2; ++x) {  // rows lane / 4 and lane / 4 + 8 of the 16
+            const int src = r0 + (lane >> 2) + 8 * x, row = (warp & 3) * 32 + src;
+            const float f = __shfl_sync(0xffffffffu, inv, src);
+            uint32_t w[8];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) w[j] = hpack2<kBf16>(ov[8 * k + 2 * j] * inv, ov[8 * k + 2 * j + 1] * inv);
-              *reinterpret_cast<uint4*>(orow + cb * 64 + k * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 8; ++k) w[k] = hpack2<kBf16>(v[4 * k + 2 * x] * f, v[4 * k + 2 * x + 1] * f);
+            quad_transpose(w, lane);
+            quad_transpose(w + 4, lane);
+            const int to = row / a.G, ho = row - to * a.G;
+            if (to < a.T && h * a.T + to < t.ntok) {
+              uint8_t* orow = a.out + (((size_t)t.key0 + t.t0 + h * a.T + to) * a.Hq + (size_t)t.g * a.G + ho) * 256 +
+                              c0 * 2 + (lane & 3) * 16;
+              *reinterpret_cast<uint4*>(orow) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(orow + 64) = make_uint4(w[4], w[5], w[6], w[7]);
             }
           }
         }
         if (live && a.lse)
-          a.lse[(size_t)(t.g * a.G + hh) * a.total_q + tok] =
+          a.lse[(size_t)(t.g * a.G + hh) * a.total_q + t.key0 + t.t0 + tt] =
               l == 0.f ? -INFINITY : (m + lg2_approx(l)) * 0.69314718055994530942f;
       }
       tc_fence_before();
