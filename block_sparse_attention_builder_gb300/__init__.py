@@ -154,7 +154,7 @@ def library() -> ctypes.CDLL:
 
 class _LazyLib:
     def __getattr__(self, name):
-        return getattr(library(), name)
+        return getattr(_lib_handle or library(), name)
 
 
 _lib = _LazyLib()
@@ -168,6 +168,8 @@ def _check(status: int, what: str):
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()  # (the argument types make it a pointer)
 
+
+_data_ptr = torch.Tensor.data_ptr  # of a tensor that is there
 
 _ELEM_BYTES = {BF16: 2, FP16: 2, FP8_E4M3: 1}
 _ROW_BYTES = {BF16: 256, FP16: 256, FP8_E4M3: 128, NVFP4: NVFP4_ROW_BYTES}  # per (position, kv head)
@@ -377,14 +379,13 @@ def _need_types(what: str, exact):
             raise MxsaError(1, f"{what}: {name} is {t.dtype}, not {dtype}")
 
 
-def _need_mask(what: str, tree_mask: torch.Tensor, total_q: int) -> int:
-    """The words of a token's mask in tree_mask, int32 (or uint32) [total_q, words]."""
+def _need_mask(what: str, tree_mask: torch.Tensor, total_q: int):
+    """Refuses a tree_mask that is not int32 (or uint32) [total_q, words]."""
     if tree_mask.dtype is not _I32 and tree_mask.dtype is not torch.uint32:
         raise MxsaError(1, f"{what}: tree_mask is {tree_mask.dtype}, not torch.int32")
     if tree_mask.dim() != 2 or tree_mask.shape[0] < total_q:
         raise MxsaError(1, f"{what}: tree_mask is {tuple(tree_mask.shape)}, not [total_q, words]")
     _need(what, "tree_mask", tree_mask, 0)
-    return tree_mask.shape[1]
 
 
 def tree_fwd(prob, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens, tree_mask, group_ptr, prefix_lens,
@@ -398,21 +399,42 @@ def tree_fwd(prob, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens
     if (group_ptr is None) != (prefix_lens is None):
         raise MxsaError(1, f"{what}: group_ptr and prefix_lens come together")
     ng = 0 if prefix_lens is None else prefix_lens.numel()
-    _need_attention(what, prob, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                    cu_seqlens_q=cu_seqlens_q, used_kv_lens=used_kv_lens, out=out, lse=lse)
-    words = _need_mask(what, tree_mask, prob.total_q)
-    _need(what, "group_ptr", group_ptr, (ng + 1) * 4)
-    _need(what, "prefix_lens", prefix_lens, ng * 4)
-    _need(what, "ws", ws, 0)
-    _need(what, "flags", flags, 4)
-    qt, kt = _ROW_TYPE.get(prob.q_dtype), _ROW_TYPE.get(prob.kv_dtype)
-    _refuse_types(what, (("q", q, qt), ("k_cache", k_cache, kt), ("v_cache", v_cache, kt), ("out", out, qt)),
-                  (("block_tables", block_tables, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
-                   ("used_kv_lens", used_kv_lens, _I32), ("group_ptr", group_ptr, _I32),
-                   ("prefix_lens", prefix_lens, _I32), ("lse", lse, _F32), ("flags", flags, _I32)))
-    _check(_lib.mxsa_tree_fwd(ctypes.byref(prob), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                              _ptr(cu_seqlens_q), _ptr(used_kv_lens), _ptr(tree_mask), words, ng, _ptr(group_ptr),
-                              _ptr(prefix_lens), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), _ptr(lse),
+    qd, kd, seqs, total_q = prob.q_dtype, prob.kv_dtype, prob.num_seqs, prob.total_q
+    qt, kt = _ROW_TYPE.get(qd), _ROW_TYPE.get(kd)
+    rows = total_q * prob.num_q_heads
+    cache = prob.num_pages * prob.num_kv_heads * prob.page_size * _ROW_BYTES.get(kd, 256)
+    try:
+        plain = (q.dtype is qt and q.numel() >= rows * 128 and q.is_contiguous() and out.dtype is qt and
+                 out.numel() >= rows * 128 and out.is_contiguous() and k_cache.dtype is kt and
+                 k_cache.nbytes >= cache and k_cache.is_contiguous() and v_cache.dtype is kt and
+                 v_cache.nbytes >= cache and v_cache.is_contiguous() and block_tables.dtype is _I32 and
+                 block_tables.numel() >= seqs * prob.max_pages_per_seq and block_tables.is_contiguous() and
+                 cu_seqlens_q.dtype is _I64 and cu_seqlens_q.numel() > seqs and cu_seqlens_q.is_contiguous() and
+                 used_kv_lens.dtype is _I32 and used_kv_lens.numel() >= seqs and used_kv_lens.is_contiguous() and
+                 tree_mask.dtype is _I32 and tree_mask.dim() == 2 and tree_mask.shape[0] >= total_q and
+                 tree_mask.is_contiguous() and ws.is_contiguous() and
+                 (ng == 0 or (group_ptr.dtype is _I32 and group_ptr.numel() > ng and group_ptr.is_contiguous() and
+                              prefix_lens.dtype is _I32 and prefix_lens.is_contiguous())) and
+                 (lse is None or (lse.dtype is _F32 and lse.numel() >= rows and lse.is_contiguous())) and
+                 (flags is None or (flags.dtype is _I32 and flags.numel() >= 1)))
+    except AttributeError:  # a None: the library says whether it may be one
+        plain = False
+    if not plain:
+        _need_attention(what, prob, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                        cu_seqlens_q=cu_seqlens_q, used_kv_lens=used_kv_lens, out=out, lse=lse)
+        _need_mask(what, tree_mask, max(total_q, 0))
+        _need(what, "group_ptr", group_ptr, (ng + 1) * 4)
+        _need(what, "prefix_lens", prefix_lens, ng * 4)
+        _need(what, "ws", ws, 0)
+        _need(what, "flags", flags, 4)
+        _refuse_types(what, (("q", q, qt), ("k_cache", k_cache, kt), ("v_cache", v_cache, kt), ("out", out, qt)),
+                      (("block_tables", block_tables, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
+                       ("used_kv_lens", used_kv_lens, _I32), ("group_ptr", group_ptr, _I32),
+                       ("prefix_lens", prefix_lens, _I32), ("lse", lse, _F32), ("flags", flags, _I32)))
+    ptr = _data_ptr if plain else _ptr
+    _check(_lib.mxsa_tree_fwd(ctypes.byref(prob), ptr(q), ptr(k_cache), ptr(v_cache), ptr(block_tables),
+                              ptr(cu_seqlens_q), ptr(used_kv_lens), ptr(tree_mask), tree_mask.shape[1], ng,
+                              _ptr(group_ptr), _ptr(prefix_lens), ptr(ws), ws.nbytes, ptr(out), _ptr(lse),
                               _ptr(flags), _stream(stream)), what)
 
 
@@ -422,17 +444,33 @@ def tree_mask(prob, parents, cu_seqlens_q, used_kv_lens, mask, positions=None, f
     last committed token) -> mask int32 [total_q, words], positions int64
     [total_q] (committed tokens + ancestors) or None."""
     what = "mxsa_tree_mask"
-    total_q, seqs = max(prob.total_q, 0), max(prob.num_seqs, 0)
-    words = _need_mask(what, mask, total_q)
-    _need(what, "parents", parents, total_q * 4)
-    _need(what, "cu_seqlens_q", cu_seqlens_q, (seqs + 1) * 8)
-    _need(what, "used_kv_lens", used_kv_lens, seqs * 4)
-    _need(what, "positions", positions, total_q * 8)
-    _need(what, "flags", flags, 4)
-    _need_types(what, (("parents", parents, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
-                       ("used_kv_lens", used_kv_lens, _I32), ("positions", positions, _I64), ("flags", flags, _I32)))
-    _check(_lib.mxsa_tree_mask(ctypes.byref(prob), _ptr(parents), _ptr(cu_seqlens_q), _ptr(used_kv_lens), words,
-                               _ptr(mask), _ptr(positions), _ptr(flags), _stream(stream)), what)
+    total_q, seqs = prob.total_q, prob.num_seqs
+    # (every tensor of the plain type and size: one expression, which costs a
+    # call a third of what the checks by name do)
+    try:
+        plain = (parents.dtype is _I32 and parents.numel() >= total_q and parents.is_contiguous() and
+                 cu_seqlens_q.dtype is _I64 and cu_seqlens_q.numel() > seqs and cu_seqlens_q.is_contiguous() and
+                 used_kv_lens.dtype is _I32 and used_kv_lens.numel() >= seqs and used_kv_lens.is_contiguous() and
+                 mask.dtype is _I32 and mask.dim() == 2 and mask.shape[0] >= total_q and mask.is_contiguous() and
+                 (positions is None or (positions.dtype is _I64 and positions.numel() >= total_q and
+                                        positions.is_contiguous())) and
+                 (flags is None or (flags.dtype is _I32 and flags.numel() >= 1)))
+    except AttributeError:  # a None: the library says whether it may be one
+        plain = False
+    if not plain:
+        total_q, seqs = max(total_q, 0), max(seqs, 0)
+        _need_mask(what, mask, total_q)
+        _need(what, "parents", parents, total_q * 4)
+        _need(what, "cu_seqlens_q", cu_seqlens_q, (seqs + 1) * 8)
+        _need(what, "used_kv_lens", used_kv_lens, seqs * 4)
+        _need(what, "positions", positions, total_q * 8)
+        _need(what, "flags", flags, 4)
+        _need_types(what, (("parents", parents, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
+                           ("used_kv_lens", used_kv_lens, _I32), ("positions", positions, _I64),
+                           ("flags", flags, _I32)))
+    ptr = _data_ptr if plain else _ptr
+    _check(_lib.mxsa_tree_mask(ctypes.byref(prob), ptr(parents), ptr(cu_seqlens_q), ptr(used_kv_lens),
+                               mask.shape[1], ptr(mask), _ptr(positions), _ptr(flags), _stream(stream)), what)
 
 
 def tree_commit(prob, cu_seqlens_q, used_kv_lens, block_tables, path, path_lens, k_cache, v_cache, kv_lens_out=None,
@@ -443,31 +481,47 @@ def tree_commit(prob, cu_seqlens_q, used_kv_lens, block_tables, path, path_lens,
     [pages, index heads, page_size, index dim] in the cache dtype, or None;
     kv_lens_out int32 [B]: committed and accepted tokens."""
     what = "mxsa_tree_commit"
-    seqs = max(prob.num_seqs, 0)
-    _need_attention(what, prob, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                    cu_seqlens_q=cu_seqlens_q, used_kv_lens=used_kv_lens)
-    if path.dim() != 2:
-        raise MxsaError(1, f"{what}: path is {tuple(path.shape)}, not [num_seqs, longest path]")
-    wide = path.shape[1]
-    _need(what, "path", path, seqs * wide * 4)
-    _need(what, "path_lens", path_lens, seqs * 4)
-    _need(what, "kv_lens_out", kv_lens_out, seqs * 4)
-    _need(what, "flags", flags, 4)
+    seqs, kd = prob.num_seqs, prob.kv_dtype
+    cache = prob.num_pages * prob.num_kv_heads * prob.page_size * _ROW_BYTES.get(kd, 256)
+    kt = _ROW_TYPE.get(kd)
     ih = idim = 0
-    if idx_cache is not None:
-        if idx_cache.dim() != 4 or idx_cache.shape[0] < prob.num_pages or idx_cache.shape[2] != prob.page_size:
-            raise MxsaError(1, f"{what}: idx_cache is {tuple(idx_cache.shape)}, not [pages, heads, page_size, dim]")
-        ih, idim = idx_cache.shape[1], idx_cache.shape[3]
-        _need(what, "idx_cache", idx_cache, prob.num_pages * ih * prob.page_size * idim *
-              _ELEM_BYTES.get(prob.kv_dtype, 2))
-    kt = _ROW_TYPE.get(prob.kv_dtype)
-    _refuse_types(what, (("k_cache", k_cache, kt), ("v_cache", v_cache, kt), ("idx_cache", idx_cache, kt)),
-                  (("block_tables", block_tables, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
-                   ("used_kv_lens", used_kv_lens, _I32), ("path", path, _I32), ("path_lens", path_lens, _I32),
-                   ("kv_lens_out", kv_lens_out, _I32), ("flags", flags, _I32)))
-    _check(_lib.mxsa_tree_commit(ctypes.byref(prob), _ptr(cu_seqlens_q), _ptr(used_kv_lens), _ptr(block_tables),
-                                 _ptr(path), wide, _ptr(path_lens), _ptr(k_cache), _ptr(v_cache), _ptr(idx_cache), ih,
-                                 idim, _ptr(kv_lens_out), _ptr(flags), _stream(stream)), what)
+    try:
+        plain = (idx_cache is None and cu_seqlens_q.dtype is _I64 and cu_seqlens_q.numel() > seqs and
+                 cu_seqlens_q.is_contiguous() and used_kv_lens.dtype is _I32 and used_kv_lens.numel() >= seqs and
+                 used_kv_lens.is_contiguous() and block_tables.dtype is _I32 and block_tables.is_contiguous() and
+                 block_tables.numel() >= seqs * prob.max_pages_per_seq and path.dtype is _I32 and path.dim() == 2 and
+                 path.shape[0] >= seqs and path.is_contiguous() and path_lens.dtype is _I32 and
+                 path_lens.numel() >= seqs and path_lens.is_contiguous() and k_cache.dtype is kt and
+                 k_cache.nbytes >= cache and k_cache.is_contiguous() and v_cache.dtype is kt and
+                 v_cache.nbytes >= cache and v_cache.is_contiguous() and
+                 (kv_lens_out is None or (kv_lens_out.dtype is _I32 and kv_lens_out.numel() >= seqs and
+                                          kv_lens_out.is_contiguous())) and
+                 (flags is None or (flags.dtype is _I32 and flags.numel() >= 1)))
+    except AttributeError:  # a None: the library says whether it may be one
+        plain = False
+    if not plain:
+        seqs = max(seqs, 0)
+        _need_attention(what, prob, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                        cu_seqlens_q=cu_seqlens_q, used_kv_lens=used_kv_lens)
+        if path.dim() != 2:
+            raise MxsaError(1, f"{what}: path is {tuple(path.shape)}, not [num_seqs, longest path]")
+        _need(what, "path", path, seqs * path.shape[1] * 4)
+        _need(what, "path_lens", path_lens, seqs * 4)
+        _need(what, "kv_lens_out", kv_lens_out, seqs * 4)
+        _need(what, "flags", flags, 4)
+        if idx_cache is not None:
+            if idx_cache.dim() != 4 or idx_cache.shape[0] < prob.num_pages or idx_cache.shape[2] != prob.page_size:
+                raise MxsaError(1, f"{what}: idx_cache is {tuple(idx_cache.shape)}, not [pages, heads, page_size, dim]")
+            ih, idim = idx_cache.shape[1], idx_cache.shape[3]
+            _need(what, "idx_cache", idx_cache, prob.num_pages * ih * prob.page_size * idim * _ELEM_BYTES.get(kd, 2))
+        _refuse_types(what, (("k_cache", k_cache, kt), ("v_cache", v_cache, kt), ("idx_cache", idx_cache, kt)),
+                      (("block_tables", block_tables, _I32), ("cu_seqlens_q", cu_seqlens_q, _I64),
+                       ("used_kv_lens", used_kv_lens, _I32), ("path", path, _I32), ("path_lens", path_lens, _I32),
+                       ("kv_lens_out", kv_lens_out, _I32), ("flags", flags, _I32)))
+    ptr = _data_ptr if plain else _ptr
+    _check(_lib.mxsa_tree_commit(ctypes.byref(prob), ptr(cu_seqlens_q), ptr(used_kv_lens), ptr(block_tables),
+                                 ptr(path), path.shape[1], ptr(path_lens), ptr(k_cache), ptr(v_cache),
+                                 _ptr(idx_cache), ih, idim, _ptr(kv_lens_out), _ptr(flags), _stream(stream)), what)
 
 
 def prompt_workspace_size(prob: Problem) -> int:
@@ -484,21 +538,32 @@ def prompt_fwd(prob, q, k, v, cu_seqlens, ws, out, lse=None, flags=None, stream=
     [Hq, total_q].  ws: uint8 device tensor of prompt_workspace_size bytes.
     The problem's pages are not used."""
     what = "mxsa_prompt_fwd"
-    n, hq, hkv = max(prob.total_q, 0), prob.num_q_heads, prob.num_kv_heads
+    n, hq, hkv = prob.total_q, prob.num_q_heads, prob.num_kv_heads
     qt = _ROW_TYPE.get(prob.q_dtype)
     q_stride = _token_stride(what, "q", q, qt, n, hq, 128)
     k_stride = _token_stride(what, "k", k, qt, n, hkv, 128)
     v_stride = _token_stride(what, "v", v, qt, n, hkv, 128)
-    _need(what, "cu_seqlens", cu_seqlens, (max(prob.num_seqs, 0) + 1) * 8)
-    _need(what, "ws", ws, 0)
-    _need(what, "out", out, n * hq * 256)
-    _need(what, "lse", lse, n * hq * 4)
-    _need(what, "flags", flags, 4)
-    _refuse_types(what, (("q", q, qt), ("k", k, qt), ("v", v, qt), ("out", out, qt)),
-                  (("cu_seqlens", cu_seqlens, _I64), ("lse", lse, _F32), ("flags", flags, _I32)))
-    _check(_lib.mxsa_prompt_fwd(ctypes.byref(prob), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
-                                _ptr(cu_seqlens), _ptr(ws), ws.numel() * ws.element_size(), _ptr(out), _ptr(lse),
-                                _ptr(flags), _stream(stream)), what)
+    rows = n * hq
+    try:
+        plain = (q.dtype is qt and k.dtype is qt and v.dtype is qt and out.dtype is qt and
+                 out.numel() >= rows * 128 and out.is_contiguous() and cu_seqlens.dtype is _I64 and
+                 cu_seqlens.numel() > prob.num_seqs and cu_seqlens.is_contiguous() and ws.is_contiguous() and
+                 (lse is None or (lse.dtype is _F32 and lse.numel() >= rows and lse.is_contiguous())) and
+                 (flags is None or (flags.dtype is _I32 and flags.numel() >= 1)))
+    except AttributeError:  # a None: the library says whether it may be one
+        plain = False
+    if not plain:
+        _need(what, "cu_seqlens", cu_seqlens, (max(prob.num_seqs, 0) + 1) * 8)
+        _need(what, "ws", ws, 0)
+        _need(what, "out", out, rows * 256)
+        _need(what, "lse", lse, rows * 4)
+        _need(what, "flags", flags, 4)
+        _refuse_types(what, (("q", q, qt), ("k", k, qt), ("v", v, qt), ("out", out, qt)),
+                      (("cu_seqlens", cu_seqlens, _I64), ("lse", lse, _F32), ("flags", flags, _I32)))
+    ptr = _data_ptr if plain else _ptr
+    _check(_lib.mxsa_prompt_fwd(ctypes.byref(prob), ptr(q), q_stride, ptr(k), k_stride, ptr(v), v_stride,
+                                ptr(cu_seqlens), ptr(ws), ws.nbytes, ptr(out), _ptr(lse), _ptr(flags),
+                                _stream(stream)), what)
 
 
 def build_tables(prob, kv_lens, new_lens, pages_held, block_tables, free_pages, free_count, cu_seqlens_q,
@@ -512,27 +577,48 @@ def build_tables(prob, kv_lens, new_lens, pages_held, block_tables, free_pages, 
     free_count_out: None writes pages_held and free_count themselves;
     used_kv_lens may be kv_lens."""
     what = "mxsa_build_tables"
-    seqs, total_q = max(prob.num_seqs, 0), max(prob.total_q, 0)
+    seqs, total_q = prob.num_seqs, prob.total_q
     pages_held_out = pages_held if pages_held_out is None else pages_held_out
     free_count_out = free_count if free_count_out is None else free_count_out
-    ints = (("kv_lens", kv_lens, seqs), ("new_lens", new_lens, seqs), ("pages_held", pages_held, seqs),
-            ("block_tables", block_tables, seqs * max(prob.max_pages_per_seq, 0)),
-            ("free_pages", free_pages, max(prob.num_pages, 0)), ("free_count", free_count, 1),
-            ("used_kv_lens", used_kv_lens, seqs), ("pages_held_out", pages_held_out, seqs),
-            ("free_count_out", free_count_out, 1))
-    for name, t, n in ints:
-        _need(what, name, t, n * 4)
-    _need(what, "cu_seqlens_q", cu_seqlens_q, (seqs + 1) * 8)
-    _need(what, "positions", positions, total_q * 8)
-    _need(what, "loc", loc, total_q * 8)
-    _need(what, "flags", flags, 4)
-    _need_types(what, tuple((name, t, _I32) for name, t, _ in ints) +
-                (("cu_seqlens_q", cu_seqlens_q, _I64), ("positions", positions, _I64), ("loc", loc, _I64),
-                 ("flags", flags, _I32)))
-    _check(_lib.mxsa_build_tables(ctypes.byref(prob), _ptr(kv_lens), _ptr(new_lens), _ptr(pages_held),
-                                  _ptr(block_tables), _ptr(free_pages), _ptr(free_count), _ptr(cu_seqlens_q),
-                                  _ptr(used_kv_lens), _ptr(positions), _ptr(loc), _ptr(pages_held_out),
-                                  _ptr(free_count_out), _ptr(flags), _stream(stream)), what)
+    try:
+        plain = (kv_lens.dtype is _I32 and kv_lens.numel() >= seqs and kv_lens.is_contiguous() and
+                 new_lens.dtype is _I32 and new_lens.numel() >= seqs and new_lens.is_contiguous() and
+                 pages_held.dtype is _I32 and pages_held.numel() >= seqs and pages_held.is_contiguous() and
+                 block_tables.dtype is _I32 and block_tables.numel() >= seqs * prob.max_pages_per_seq and
+                 block_tables.is_contiguous() and free_pages.dtype is _I32 and
+                 free_pages.numel() >= prob.num_pages and free_pages.is_contiguous() and
+                 free_count.dtype is _I32 and free_count.numel() >= 1 and cu_seqlens_q.dtype is _I64 and
+                 cu_seqlens_q.numel() > seqs and cu_seqlens_q.is_contiguous() and used_kv_lens.dtype is _I32 and
+                 used_kv_lens.numel() >= seqs and used_kv_lens.is_contiguous() and positions.dtype is _I64 and
+                 positions.numel() >= total_q and positions.is_contiguous() and loc.dtype is _I64 and
+                 loc.numel() >= total_q and loc.is_contiguous() and
+                 (pages_held_out is pages_held or (pages_held_out.dtype is _I32 and pages_held_out.numel() >= seqs and
+                                                   pages_held_out.is_contiguous())) and
+                 (free_count_out is free_count or (free_count_out.dtype is _I32 and free_count_out.numel() >= 1)) and
+                 (flags is None or (flags.dtype is _I32 and flags.numel() >= 1)))
+    except AttributeError:  # a None: the library says whether it may be one
+        plain = False
+    if not plain:
+        seqs, total_q = max(seqs, 0), max(total_q, 0)
+        ints = (("kv_lens", kv_lens, seqs), ("new_lens", new_lens, seqs), ("pages_held", pages_held, seqs),
+                ("block_tables", block_tables, seqs * max(prob.max_pages_per_seq, 0)),
+                ("free_pages", free_pages, max(prob.num_pages, 0)), ("free_count", free_count, 1),
+                ("used_kv_lens", used_kv_lens, seqs), ("pages_held_out", pages_held_out, seqs),
+                ("free_count_out", free_count_out, 1))
+        for name, t, n in ints:
+            _need(what, name, t, n * 4)
+        _need(what, "cu_seqlens_q", cu_seqlens_q, (seqs + 1) * 8)
+        _need(what, "positions", positions, total_q * 8)
+        _need(what, "loc", loc, total_q * 8)
+        _need(what, "flags", flags, 4)
+        _need_types(what, tuple((name, t, _I32) for name, t, _ in ints) +
+                    (("cu_seqlens_q", cu_seqlens_q, _I64), ("positions", positions, _I64), ("loc", loc, _I64),
+                     ("flags", flags, _I32)))
+    ptr = _data_ptr if plain else _ptr
+    _check(_lib.mxsa_build_tables(ctypes.byref(prob), ptr(kv_lens), ptr(new_lens), ptr(pages_held),
+                                  ptr(block_tables), ptr(free_pages), ptr(free_count), ptr(cu_seqlens_q),
+                                  ptr(used_kv_lens), ptr(positions), ptr(loc), ptr(pages_held_out),
+                                  ptr(free_count_out), _ptr(flags), _stream(stream)), what)
 
 
 def store_kv(prob, loc, k, v, k_cache, v_cache, idx_k=None, idx_cache=None, flags=None, stream=None):
