@@ -251,6 +251,12 @@ __device__ __forceinline__ void quad_transpose(uint32_t* w, int lane) {
   }
 }
 
+#ifdef MXSA_TEST_HOOKS
+// Test builds only: CTA g_skip_record keeps its first tile's record to itself,
+// so that every other role's first wait runs out.
+__device__ int g_skip_record = -1;
+#endif
+
 template <bool kBf16>
 __global__ void __launch_bounds__(kRThreads, 1)
     k_prompt(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -375,9 +381,14 @@ __global__ void __launch_bounds__(kRThreads, 1)
         ok = hwarp_all(
             mbar_wait(&c.work_empty[w], ((n / kRWork) & 1) ^ 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
         if (!ok) break;
+#ifdef MXSA_TEST_HOOKS
+        const bool skip = (int)blockIdx.x == g_skip_record && n == 0;
+#else
+        constexpr bool skip = false;
+#endif
         if (lane == 0) {
           c.work[w] = t;
-          mbar_arrive(&c.work_full[w]);
+          if (!skip) mbar_arrive(&c.work_full[w]);
         }
         const int blocks = max(t.n0, t.n1);
         if (blocks == 0) break;
@@ -759,3 +770,11 @@ cudaError_t launch_prompt(const mxsa_problem& p, const void* q, long long q_stri
 }
 
 }  // namespace mxsa
+
+#ifdef MXSA_TEST_HOOKS
+// Test builds only: the CTA of the next prompt_fwd launches that keeps its
+// first tile's record to itself; -1 turns the switch off.  Synchronous.
+extern "C" mxsa_status mxsa_test_skip_record(int32_t cta) {
+  return cudaMemcpyToSymbol(mxsa::g_skip_record, &cta, sizeof(cta)) == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
+}
+#endif
