@@ -479,9 +479,15 @@ static mxsa_status shared_fwd(const mxsa_problem* problem, const void* q, const 
     return MXSA_ERR_INVALID_ARG;
   if (shared_bytes < shared_workspace_bytes(p)) return MXSA_ERR_WORKSPACE;
   if (!kernel_writable(out) || !kernel_writable(lse)) return MXSA_ERR_INVALID_ARG;
-  cudaError_t e = launch_dense_shared(p, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens, num_groups,
-                                      num_groups > 0 ? group_ptr : nullptr, prefix_lens, tree_mask, mask_words, ws,
-                                      out, lse, device_flags, static_cast<cudaStream_t>(stream));
+  const int cluster = mask_words ? tree_small_cluster(p, num_groups) : 0;
+  cudaError_t e;
+  if (cluster)
+    e = launch_tree_small(p, cluster, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens, tree_mask,
+                          mask_words, out, lse, device_flags, static_cast<cudaStream_t>(stream));
+  else
+    e = launch_dense_shared(p, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens, num_groups,
+                            num_groups > 0 ? group_ptr : nullptr, prefix_lens, tree_mask, mask_words, ws, out, lse,
+                            device_flags, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;
 }
 

@@ -179,6 +179,12 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
                                 const int32_t* block_tables, const int64_t* cu, const int32_t* lens, int num_groups,
                                 const int32_t* group_ptr, const int32_t* prefix_lens, const uint32_t* tree_mask,
                                 int tree_words, void* ws, void* out, float* lse, int32_t* flags, cudaStream_t st);
+// Drafted trees in one launch: the cluster's size where that path is taken, else 0.
+int tree_small_cluster(const mxsa_problem& p, int num_groups);
+cudaError_t launch_tree_small(const mxsa_problem& p, int cluster, const void* q, const void* k_cache,
+                              const void* v_cache, const int32_t* block_tables, const int64_t* cu, const int32_t* lens,
+                              const uint32_t* mask, int words, void* out, float* lse, int32_t* flags,
+                              cudaStream_t st);
 constexpr int kMaxMaskWords = 64;  // of a drafted tree's mask: 2048 tokens
 size_t prompt_workspace_bytes(const mxsa_problem& p);
 cudaError_t launch_prompt(const mxsa_problem& p, const void* q, long long q_stride, const void* k, long long k_stride,

@@ -114,4 +114,48 @@ __device__ __forceinline__ void scale_o(uint32_t tO, float f) {
   }
 }
 
+// P = 2^(S * scale - m) of 64 keys of a row, packed, to TMEM; returns their
+// sum, and the largest S in `most`.
+template <bool kBf16>
+__device__ __forceinline__ float exp_half(const float* sv, float scale_log2, float m, uint32_t tP, float* most) {
+  const uint64_t scale2 = pack_f2(scale_log2, scale_log2), off2 = pack_f2(-m, -m);
+  uint64_t l0 = pack_f2(0.f, 0.f), l1 = l0;
+  float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t pk[16];
+    float2 x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      x[k] = unpack_f2(fma_f2(pack_f2(sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]), scale2, off2));
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      x[k].x = ex2_approx(x[k].x);
+      x[k].y = ex2_approx(x[k].y);
+      if (k & 1) b1 = hmax3(b1, sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]);
+      else b0 = hmax3(b0, sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (k & 1) l1 = add_f2(l1, pack_f2(x[k].x, x[k].y));
+      else l0 = add_f2(l0, pack_f2(x[k].x, x[k].y));
+      pk[k] = hpack2<kBf16>(x[k].x, x[k].y);
+    }
+    tmem_st16(tP + 16 * q, pk);
+  }
+  const float2 ls = unpack_f2(add_f2(l0, l1));
+  *most = fmaxf(b0, b1);
+  return ls.x + ls.y;
+}
+
+// Which of keys o .. o + 31 a row of a drafted tree sees, as bits; keys are
+// numbered from the first drafted one, those before it are seen by all.  row:
+// the token's mask, not read where o <= -32.
+__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int o) {
+  if (o <= -32) return 0xFFFFFFFFu;
+  auto word = [&](int w) { return w < words ? __ldg(row + w) : 0u; };
+  if (o < 0) return (word(0) << -o) | ((1u << -o) - 1);
+  return __funnelshift_r(word(o >> 5), (o & 31) ? word((o >> 5) + 1) : 0u, o & 31);
+}
+
 }  // namespace mxsa

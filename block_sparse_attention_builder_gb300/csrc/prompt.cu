@@ -202,40 +202,6 @@ __global__ void __launch_bounds__(kRPlanThreads) k_prompt_plan(RArgs a, RHeader*
 }
 
 // ---------------------------------------------------------------- forward
-// P = 2^(S * scale - m) of 64 keys of a row, packed, to TMEM; returns their
-// sum, and the largest S in `most`.
-template <bool kBf16>
-__device__ __forceinline__ float exp_half(const float* sv, float scale_log2, float m, uint32_t tP, float* most) {
-  const uint64_t scale2 = pack_f2(scale_log2, scale_log2), off2 = pack_f2(-m, -m);
-  uint64_t l0 = pack_f2(0.f, 0.f), l1 = l0;
-  float b0 = -INFINITY, b1 = -INFINITY;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    uint32_t pk[16];
-    float2 x[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      x[k] = unpack_f2(fma_f2(pack_f2(sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]), scale2, off2));
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      x[k].x = ex2_approx(x[k].x);
-      x[k].y = ex2_approx(x[k].y);
-      if (k & 1) b1 = hmax3(b1, sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]);
-      else b0 = hmax3(b0, sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]);
-    }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if (k & 1) l1 = add_f2(l1, pack_f2(x[k].x, x[k].y));
-      else l0 = add_f2(l0, pack_f2(x[k].x, x[k].y));
-      pk[k] = hpack2<kBf16>(x[k].x, x[k].y);
-    }
-    tmem_st16(tP + 16 * q, pk);
-  }
-  const float2 ls = unpack_f2(add_f2(l0, l1));
-  *most = fmaxf(b0, b1);
-  return ls.x + ls.y;
-}
-
 // The 4 x 4 words that four neighbouring lanes hold, transposed.
 __device__ __forceinline__ void quad_transpose(uint32_t* w, int lane) {
 #pragma unroll

@@ -542,16 +542,6 @@ struct HArgs {
   int32_t tree_words;
 };
 
-// Which of keys o .. o + 31 a row of a drafted tree sees, as bits; keys are
-// numbered from the first drafted one, those before it are seen by all.  row:
-// the token's mask, not read where o <= -32.
-__device__ __forceinline__ uint32_t tree_bits(const uint32_t* row, int words, int o) {
-  if (o <= -32) return 0xFFFFFFFFu;
-  auto word = [&](int w) { return w < words ? __ldg(row + w) : 0u; };
-  if (o < 0) return (word(0) << -o) | ((1u << -o) - 1);
-  return __funnelshift_r(word(o >> 5), (o & 31) ? word((o >> 5) + 1) : 0u, o & 31);
-}
-
 __device__ __forceinline__ HTile load_tile(const HTile* p) {
   HTile t;
   const int4* s = reinterpret_cast<const int4*>(p);

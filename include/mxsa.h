@@ -309,8 +309,9 @@ mxsa_status mxsa_dense_shared_fwd(const mxsa_problem* problem, const void* q, co
  * the smallest base_s of the group's sequences with new tokens), the workspace
  * (mxsa_shared_workspace_size), limits, types, roundings and flags;
  * problem->causal is not used.  The V rows of drafted keys that a row does not
- * see, but others of its sequence do, have to be finite.  Three launches,
- * asynchronous on `stream`. */
+ * see, but others of its sequence do, have to be finite.  One launch for few
+ * sequences with tables of moderate length and no groups (ws is then not used),
+ * else three; asynchronous on `stream`. */
 mxsa_status mxsa_tree_fwd(const mxsa_problem* problem, const void* q, const void* k_cache, const void* v_cache,
                           const int32_t* block_tables, const int64_t* cu_seqlens_q, const int32_t* used_kv_lens,
                           const uint32_t* tree_mask, int32_t mask_words, int32_t num_groups,

@@ -50,7 +50,7 @@ class Trees:
     """seqs: (new tokens, committed keys); groups: (first, end, prefix)."""
 
     def __init__(self, seqs, hq=16, hkv=2, q="bf16", ps=64, seed=0, lead=0, tail=0, words=None, groups=None,
-                 masks="tree", scale=0.0):
+                 masks="tree", scale=0.0, wide=False):
         r = np.random.RandomState(seed)
         g = torch.Generator().manual_seed(seed)
         t = TDT[q]
@@ -63,6 +63,8 @@ class Trees:
         self.total = self.cu[-1] + tail
         lens = [n + c for n, c in seqs]
         width = max(1, max(-(-L // ps) for L in lens))
+        if wide:  # a table of long rows: the general path also where one launch would do
+            width = max(width, 130 * 128 // ps)
         table, pages = np.full((B, width), -3, np.int32), 0
         first_of, common = list(range(B)), [0] * B
         for a, b, P in groups or []:
@@ -177,13 +179,20 @@ CASES = {
                           hkv=8),
     "two_groups": dict(seqs=[(5, 700)] * 6 + [(33, 260)] * 5, groups=[(0, 6, 650), (6, 11, 129)], q="fp16", hq=12,
                        hkv=4),
+    # a cluster of 8, 4, 2 and 1 CTAs, sequences of very different lengths
+    "cluster_8": dict(seqs=[(9, 8183)], ps=128),
+    "cluster_4": dict(seqs=[(5, 4000), (12, 3), (0, 9), (16, 1100)], hq=64, hkv=8),
+    "cluster_2": dict(seqs=[(16, n) for n in rand(7, 0, 2000, 6)], hq=64, hkv=8, q="fp16"),
+    "cluster_1": dict(seqs=[(n, m) for n, m in zip(rand(14, 0, 16, 7), rand(14, 0, 1000, 8))], hq=64, hkv=8, lead=1,
+                      tail=2),
     "many": dict(seqs=[(n, m) for n, m in zip(rand(200, 0, 12, 4), rand(200, 0, 600, 5))], hq=8, hkv=1, tail=3),
 }
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("name", list(CASES))
-def test_attention_against_the_definition(name):
-    Trees(seed=len(name), **CASES[name]).run().check()
+def test_attention_against_the_definition(name, wide):
+    Trees(seed=len(name), wide=wide, **CASES[name]).run().check()
 
 
 def test_a_causal_chain_is_the_dense_causal_call():
@@ -198,9 +207,10 @@ def test_a_causal_chain_is_the_dense_causal_call():
     assert ((lse - t.lse).abs() <= 1e-3).all()
 
 
-def test_nan_and_infinite_keys_that_a_row_does_not_see():
+@pytest.mark.parametrize("wide", [False, True])
+def test_nan_and_infinite_keys_that_a_row_does_not_see(wide):
     """K of drafted tokens outside a row's ancestors does not matter, whatever it holds."""
-    t = Trees([(40, 100)], masks="chain", seed=2).run().check()
+    t = Trees([(40, 100)], masks="chain", seed=2, wide=wide).run().check()
     want = t.out[:20].clone()
     page, off = (x.cuda() for x in t.slots[0])
     t.k[page[130:], :, off[130:]] = float("nan")
@@ -210,13 +220,15 @@ def test_nan_and_infinite_keys_that_a_row_does_not_see():
     assert torch.equal(t.out[:20], want)
 
 
-def test_too_many_tokens_for_the_mask():
-    t = Trees([(40, 100), (9, 3)], words=1, seed=6)
+@pytest.mark.parametrize("wide", [False, True])
+def test_too_many_tokens_for_the_mask(wide):
+    t = Trees([(40, 100), (9, 3)], words=1, seed=6, wide=wide)
     t.run().check(flags=1024)  # (the further tokens' keys are seen by nobody)
 
 
-def test_shorter_than_its_new_tokens():
-    t = Trees([(10, 0), (4, 50)], masks="chain", seed=8)
+@pytest.mark.parametrize("wide", [False, True])
+def test_shorter_than_its_new_tokens(wide):
+    t = Trees([(10, 0), (4, 50)], masks="chain", seed=8, wide=wide)
     t.dl.copy_(torch.tensor([6, 54]))
     t.run()
     torch.cuda.synchronize()
@@ -250,6 +262,70 @@ def test_repeated_captured_and_two_at_once():
     t.check()
     b.check()
     assert torch.equal(t.out, out)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_lengths_pages_and_starts_that_do_not_fit(wide):
+    t = Trees([(9, 100), (4, 700), (16, 30)], hq=64, hkv=8, seed=9, wide=wide).run().check()
+    good = t.out.clone()
+    t.dcu.copy_(torch.tensor([0, 9, 8, 29]))
+    t.out.fill_(9)
+    t.run()
+    torch.cuda.synchronize()
+    assert t.flags.item() == 128 and (t.out == 9).all()
+    t.dcu.copy_(torch.tensor(t.cu))
+    t.flags.zero_()
+    t.dl[0] = t.prob.max_pages_per_seq * 64 + 1
+    t.dl[2] = -1
+    t.run()
+    torch.cuda.synchronize()
+    # (the first one's further pages are no pages of the cache; the other length
+    # may split the second one's keys otherwise: both within u (|o| + A) of the
+    # definition, A <= 4.5 sigma of V here)
+    assert t.flags.item() == 16 + 8 + 4
+    mine, want = t.out[9:13].double(), good[9:13].double()
+    assert ((mine - want).abs() <= 2 * 2.0 ** -8 * (want.abs() + 4.5)).all()
+    assert (t.out[13:] == 0).all() and t.lse[:, 13:].isneginf().all()
+    t.dl.copy_(torch.tensor(t.lens))
+    t.flags.zero_()
+    page = t.dt[1, 3].clone()
+    t.dt[1, 3] = 10 ** 6
+    t.run()
+    torch.cuda.synchronize()
+    assert t.flags.item() == 4
+    t.dt[1, 3] = page
+    t.flags.zero_()
+    t.run().check()
+    assert torch.equal(t.out, good)
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_scores_that_grow_along_the_keys(wide):
+    """The running maximum is passed again and again, also within a block's second half."""
+    t = Trees([(16, 3000), (7, 500)], hq=16, hkv=2, seed=10, wide=wide, q="fp16")
+    t.q.abs_()
+    for page, off in t.slots:
+        at = torch.arange(len(page), device="cuda")[:, None, None]
+        rows = t.k[page.cuda(), :, off.cuda()].float()
+        t.k[page.cuda(), :, off.cuda()] = ((rows * 0.1 + 1) * (at * 0.004 - 2) + 10 * (at % 300 == 290)).half()
+    t.run()
+    torch.cuda.synchronize()
+    u = U["fp16"]
+    for s, (n, base) in enumerate(t.seqs):
+        a, b, L = t.cu[s], t.cu[s + 1], t.lens[s]
+        page, off = (x.cuda() for x in t.slots[s])
+        q = t.q[a:b].double().view(n, t.hkv, -1, 128)
+        k, v = t.k[page, :, off].double(), t.v[page, :, off].double()
+        x = torch.einsum("tgrd,pgd->tgrp", q, k) * t.scale
+        mag = (torch.einsum("tgrd,pgd->tgrp", q.abs(), k.abs()) * t.scale).max().item()
+        seen = torch.ones(n, L, dtype=torch.bool)
+        seen[:, base:] = torch.from_numpy(t.seen[s])
+        x.masked_fill_(~seen.cuda()[:, None, None], -math.inf)
+        p = torch.softmax(x, -1)
+        o, A = (torch.einsum("tgrp,pgd->tgrd", p, y).reshape(n, t.hq, 128) for y in (v, v.abs()))
+        # FP32 sums of 128 products: a score is off by 128 * 2^-24 of its magnitudes' sum, p / l by twice that
+        tol = u * (o.abs() + A) * 1.01 + (2 * 128 * 2.0 ** -24 * mag + 1e-5) * A + L * 2.0 ** -25 * 5
+        assert ((t.out[a:b].double() - o).abs() <= tol).all()
 
 
 # ------------------------------------------------------------------ the masks
