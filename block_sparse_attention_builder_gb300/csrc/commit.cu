@@ -5,39 +5,82 @@
 //
 // One CTA for each sequence and head.  A row may be the source of one move and
 // the destination of another, so a CTA first loads what it moves into
-// registers, up to kMovePieces pieces of 8 bytes a thread, and stores after a
-// barrier.  A longer path goes in passes: path[j] >= j, and a pass writes
-// places before its own end only, so no later pass reads a row that an earlier
-// one has written.  Bound: latency (lengths, path, tables, rows: four rounds to
-// memory and a launch); the rows of 128 paths of eight heads are 2 MB.
+// registers, kMoveDepth pieces a thread, and stores after a barrier.  A longer
+// path goes in passes: path[j] >= j, and a pass writes places before its own end
+// only, so no later pass reads a row that an earlier one has written.
+//
+// Bound: latency (lengths, path, tables, rows: four rounds to memory and a
+// launch): 1.3 us for one path of two heads, 4.1 us for 128 of eight (FP8, 2 MB).
 #include "internal.h"
 
 namespace mxsa {
 
 namespace {
 
-constexpr int kMoveThreads = 256, kMovePieces = 4;
+constexpr int kMoveThreads = 256, kMoveDepth = 4;
 
 struct CommitArgs {
   const int64_t* cu;
   const int32_t *lens, *block_tables, *path, *path_lens;
-  uint8_t* cache[3];      // K, V, index keys (may be null)
-  int32_t* lens_out;      // may be null
-  int32_t* flags;         // may be null
-  int32_t total_q, Hkv, idx_heads, page_shift, max_pages, num_pages, max_path;
-  int32_t row[2];         // bytes of a row: K / V, index keys
-  int32_t fp4;            // K and V rows are 64 bytes of codes, and 8 of scales behind the page's codes
+  uint8_t *k_cache, *v_cache, *idx_cache;  // (index keys may be null)
+  int32_t* lens_out;                       // may be null
+  int32_t* flags;                          // may be null
+  int32_t total_q, Hkv, idx_heads, idx_row, page_shift, max_pages, num_pages, max_path;  // idx_row: bytes
 };
 
+// Moves the rows of one sequence and head.  A pass takes kMoveDepth rounds of
+// kMoveThreads pieces; piece x belongs to path entry x / (1 << kShift) where the
+// pieces of an entry are a power of two (kShift >= 0), else x / per.  at(slot,
+// part): a piece's address; null where it is padding.
+template <typename Piece, int kShift, typename At>
+__device__ __forceinline__ void move_rows(const CommitArgs& a, const int32_t* path, const int32_t* table, int n,
+                                          int base, int per, At at) {
+  const int tid = threadIdx.x;
+  auto slot = [&](int p) -> long long {  // -1: no page there
+    const int page = table[p >> a.page_shift];
+    return page < 0 || page >= a.num_pages ? -1
+                                           : ((long long)page << a.page_shift) | (p & ((1 << a.page_shift) - 1));
+  };
+  for (long long x0 = 0; x0 < (long long)n * per; x0 += kMoveThreads * kMoveDepth) {
+    Piece v[kMoveDepth];
+    Piece* to[kMoveDepth];
+#pragma unroll
+    for (int i = 0; i < kMoveDepth; ++i) {
+      const long long x = x0 + i * kMoveThreads + tid;
+      const int k = kShift >= 0 ? (int)(x >> (kShift >= 0 ? kShift : 0)) : (int)(x / per), part = (int)(x - (long long)k * per);
+      to[i] = nullptr;
+      if (k >= n) continue;
+      const int from = path[k];
+      if (from == k) continue;
+      const long long src = slot(base + from), dst = slot(base + k);
+      if (src < 0 || dst < 0) {
+        if (a.flags) atomicOr(a.flags, MXSA_FLAG_PAGE);
+        continue;
+      }
+      const Piece* p = at(src, part);
+      if (!p) continue;
+      v[i] = *p;
+      to[i] = at(dst, part);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMoveDepth; ++i)
+      if (to[i]) *to[i] = v[i];
+  }
+}
+
+template <int kKind>
 __global__ void __launch_bounds__(kMoveThreads) k_commit(CommitArgs a) {
   const int tid = threadIdx.x, heads = a.Hkv + a.idx_heads;
   const int s = blockIdx.x / heads, hx = blockIdx.x - s * heads;
-  const bool idx = hx >= a.Hkv;
   pdl_launch_dependents();
   pdl_wait();
   const long long c0 = a.cu[s], c1 = a.cu[s + 1];
   const int len = a.lens[s], n = a.path_lens[s], max_len = a.max_pages << a.page_shift;
   const int32_t* path = a.path + (size_t)s * a.max_path;
+  const int32_t* table = a.block_tables + (size_t)s * a.max_pages;
+  // (the path's first entries are on their way before its length is known)
+  const int mine = tid < a.max_path ? path[tid] : 0, before = tid > 0 && tid < a.max_path ? path[tid - 1] : -1;
   int bad = c0 < 0 || c1 < c0 || c1 > a.total_q ? MXSA_FLAG_CU : 0;
   const int tq = bad ? 0 : (int)(c1 - c0);
   if (len < 0 || len > max_len) bad |= MXSA_FLAG_LEN;
@@ -45,8 +88,8 @@ __global__ void __launch_bounds__(kMoveThreads) k_commit(CommitArgs a) {
   if (base < 0) bad |= MXSA_FLAG_CAUSAL_LEN;
   if (!(bad & MXSA_FLAG_CU) && (n < 0 || n > a.max_path || n > tq)) bad |= MXSA_FLAG_TREE;
   if (!bad) {
-    int wrong = 0;
-    for (int k = tid; k < n; k += kMoveThreads) wrong |= path[k] <= (k ? path[k - 1] : -1) || path[k] >= tq;
+    int wrong = tid < n && (mine <= before || mine >= tq);
+    for (int k = tid + kMoveThreads; k < n; k += kMoveThreads) wrong |= path[k] <= path[k - 1] || path[k] >= tq;
     if (__syncthreads_or(wrong)) bad = MXSA_FLAG_TREE;
   }
   if (hx == 0 && tid == 0) {
@@ -54,50 +97,32 @@ __global__ void __launch_bounds__(kMoveThreads) k_commit(CommitArgs a) {
     if (bad && a.flags) atomicOr(a.flags, bad);
   }
   if (bad) return;  // (the same in every thread)
-
-  const int row_bytes = idx ? a.row[1] : a.row[0];
-  const int per_row = row_bytes / 8, caches = idx ? 1 : 2;          // pieces of a row, rows of a token
-  const int rows = max(kMoveThreads * kMovePieces / (per_row * caches), 1);  // tokens of a pass
-  const int hn = idx ? a.idx_heads : a.Hkv, h = idx ? hx - a.Hkv : hx;
-  // byte offset of piece x of the row at position p; -1: no page there
-  auto at = [&](int p, int x) -> long long {
-    const int page = a.block_tables[(size_t)s * a.max_pages + (p >> a.page_shift)];
-    if (page < 0 || page >= a.num_pages) return -1;
-    const long long slab = ((long long)page * hn + h) << a.page_shift;
-    const int off = p & ((1 << a.page_shift) - 1);
-    if (a.fp4 && !idx) return x < 8 ? slab * 72 + off * 64 + 8 * x : slab * 72 + (64LL << a.page_shift) + off * 8;
-    return (slab + off) * row_bytes + 8 * x;
-  };
-  for (int k0 = 0; k0 < n; k0 += rows) {
-    const int pieces = min(rows, n - k0) * caches * per_row;
-    for (int x0 = 0; x0 < pieces; x0 += kMoveThreads * kMovePieces) {  // (more than one round: rows == 1 only)
-      uint2 v[kMovePieces];
-      long long to[kMovePieces];
-#pragma unroll
-      for (int i = 0; i < kMovePieces; ++i) {
-        const int x = x0 + i * kMoveThreads + tid;
-        to[i] = -1;
-        if (x >= pieces) continue;
-        const int r = x / per_row, k = k0 + r / caches, c = idx ? 2 : r % caches;
-        const int from = path[k];
-        if (from == k) continue;
-        const long long src = at(base + from, x - r * per_row);
-        to[i] = at(base + k, x - r * per_row);
-        if (src < 0 || to[i] < 0) {
-          if (a.flags) atomicOr(a.flags, MXSA_FLAG_PAGE);
-          to[i] = -1;
-          continue;
-        }
-        v[i] = *reinterpret_cast<const uint2*>(a.cache[c] + src);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kMovePieces; ++i)
-        if (to[i] >= 0) {
-          const int r = (x0 + i * kMoveThreads + tid) / per_row;
-          *reinterpret_cast<uint2*>(a.cache[idx ? 2 : r % caches] + to[i]) = v[i];
-        }
-    }
+  const long long ps = 1LL << a.page_shift, in_page = ps - 1;
+  if (hx >= a.Hkv) {  // index keys, pieces of 8 bytes
+    const int h = hx - a.Hkv;
+    move_rows<uint2, -1>(a, path, table, n, base, a.idx_row / 8, [&](long long slot, int part) {
+      const long long row = (((slot >> a.page_shift) * a.idx_heads + h) << a.page_shift) | (slot & in_page);
+      return reinterpret_cast<uint2*>(a.idx_cache + row * a.idx_row) + part;
+    });
+    return;
+  }
+  // K and V, pieces of 16 bytes: 16 (or 8) of a K row, then as many of the V row.
+  constexpr int kShift = kKind == kKind16 ? 5 : 4, kPieces = 1 << (kShift - 1);
+  if (kKind != kKindFp4) {
+    move_rows<uint4, kShift>(a, path, table, n, base, 2 * kPieces, [&](long long slot, int part) {
+      const long long row = (((slot >> a.page_shift) * a.Hkv + hx) << a.page_shift) | (slot & in_page);
+      uint8_t* cache = part < kPieces ? a.k_cache : a.v_cache;
+      return reinterpret_cast<uint4*>(cache + row * (16 * kPieces)) + (part & (kPieces - 1));
+    });
+  } else {
+    // (pieces of 8: eight of the codes and one of the scales, K and V, 32 with padding)
+    move_rows<uint2, 5>(a, path, table, n, base, 32, [&](long long slot, int part) -> uint2* {
+      uint8_t* slab = (part < 16 ? a.k_cache : a.v_cache) + (((slot >> a.page_shift) * a.Hkv + hx) << a.page_shift) * 72;
+      const int x = part & 15;
+      if (x > 8) return nullptr;
+      return reinterpret_cast<uint2*>(x < 8 ? slab + (slot & in_page) * 64 + 8 * x
+                                            : slab + 64 * ps + (slot & in_page) * 8);
+    });
   }
 }
 
@@ -113,9 +138,9 @@ cudaError_t launch_tree_commit(const mxsa_problem& p, const int64_t* cu, const i
   a.block_tables = block_tables;
   a.path = path;
   a.path_lens = path_lens;
-  a.cache[0] = static_cast<uint8_t*>(k_cache);
-  a.cache[1] = static_cast<uint8_t*>(v_cache);
-  a.cache[2] = static_cast<uint8_t*>(idx_cache);
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.idx_cache = static_cast<uint8_t*>(idx_cache);
   a.lens_out = lens_out;
   a.flags = flags;
   a.total_q = p.total_q;
@@ -125,11 +150,10 @@ cudaError_t launch_tree_commit(const mxsa_problem& p, const int64_t* cu, const i
   a.max_pages = p.max_pages_per_seq;
   a.num_pages = p.num_pages;
   a.max_path = max_path;
-  const int kind = cache_kind(p), elem = kind == kKind16 ? 2 : 1;
-  a.fp4 = kind == kKindFp4;
-  a.row[0] = a.fp4 ? 72 : 128 * elem;
-  a.row[1] = idx_cache ? idx_dim * elem : 8;
-  return launch_pdl(k_commit, dim3((unsigned)(p.num_seqs * (a.Hkv + a.idx_heads))), dim3(kMoveThreads), 0, st, a);
+  const int kind = cache_kind(p);
+  a.idx_row = idx_cache ? idx_dim * (kind == kKind16 ? 2 : 1) : 8;
+  auto* kern = kind == kKind16 ? k_commit<kKind16> : (kind == kKindFp8 ? k_commit<kKindFp8> : k_commit<kKindFp4>);
+  return launch_pdl(kern, dim3((unsigned)(p.num_seqs * (a.Hkv + a.idx_heads))), dim3(kMoveThreads), 0, st, a);
 }
 
 }  // namespace mxsa
