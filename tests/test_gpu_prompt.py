@@ -233,3 +233,29 @@ def test_equals_the_paged_path():
     p.check()
     # (each within u (|o| + A) of the definition, A <= 4.5 sigma of V here)
     assert ((out.double() - p.out.double()).abs() <= 2 * 2.0 ** -8 * (p.out.double().abs() + 4.5)).all()
+
+
+def test_strides_of_their_own_and_sixteen_byte_offsets():
+    """q, k, v and out that begin at any 16 bytes, each with another distance between its tokens."""
+    a = Prompts([150, 37, 300], hq=12, hkv=4, q="fp16", seed=13, packed=False)
+    a.run().check()
+    want = a.out.clone()
+    for t, pad in (("q", 8), ("k", 24), ("v", 128)):
+        x = getattr(a, t)
+        n, h, _ = x.shape
+        flat = torch.full((n * (h * 128 + pad) + 8,), float("nan"), dtype=x.dtype, device="cuda")
+        view = flat[8:].view(n, h * 128 + pad)[:, :h * 128].unflatten(1, (h, 128))
+        view.copy_(x)
+        setattr(a, t, view)
+    flat = torch.full((a.out.numel() + 16,), 9.0, dtype=a.out.dtype, device="cuda")
+    out = flat[8:-8].view_as(a.out)
+    a.run(out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and (flat[:8] == 9).all() and (flat[-8:] == 9).all()
+
+
+def test_rows_past_two_to_the_31_elements():
+    """More than 2^31 elements of q and out: many short prompts, the last ones checked."""
+    p = Prompts([270] * 1000, hq=64, hkv=4, seed=14)
+    assert p.out.numel() > 2 ** 31 and p.q.numel() > 2 ** 31
+    p.run().check(seqs=[0, 499, 998, 999])

@@ -474,6 +474,54 @@ def test_commit_data_errors():
     assert run(table=((7, -1), (1, 2))) == (4, [15, 95], second)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "nvfp4"])
+def test_caches_past_two_to_the_32_bytes(kind):
+    """Drafted tokens in the last pages of a cache of more than 2^32 bytes: commit and, in 16 bits, attention."""
+    row, hkv, ps = {"bf16": 256, "fp8": 128, "nvfp4": 72}[kind], 8, 128
+    pages = 2 ** 32 // (hkv * ps * row) + 5
+    qd, kd = KINDS[kind]
+    k, v = (torch.zeros(pages, hkv, ps * row, dtype=torch.uint8, device="cuda") for _ in range(2))
+    table = torch.tensor([[pages - 1, pages - 3, pages - 4]], dtype=I32, device="cuda")
+    tq, base = 20, 250
+    view = lambda c: c if kind == "nvfp4" else c.view(kd).view(pages, hkv, ps, 128)
+    prob = mx.make_problem(1, tq, 16, hkv, 0, ps, pages, 3, q_dtype=qd, kv_dtype=kd)
+    cu, lens, f = dev([0, tq], I64), dev([tq + base], I32), dev([0], I32)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    if kind == "bf16":
+        for page in table[0].tolist():
+            for c in (k, v):
+                view(c)[page].copy_(torch.randn(hkv, ps, 128, device="cuda", generator=g))
+        q = torch.randn(tq, 16, 128, device="cuda", generator=g).to(qd)
+        mask = dev(words_of(ancestors(list(range(-1, tq - 1))), 1), I32)
+        out = torch.empty_like(q)
+        ws = torch.empty(mx.dense_shared_workspace_size(prob), dtype=torch.uint8, device="cuda")
+        mx.tree_fwd(prob, q, view(k), view(v), table, cu, lens, mask, None, None, ws, out, flags=f)
+        pos = torch.arange(tq + base, device="cuda")
+        kk, vv = (view(c)[table[0].long()[pos // ps], :, pos % ps].double() for c in (k, v))
+        x = torch.einsum("tgrd,pgd->tgrp", q.double().view(tq, hkv, 2, 128), kk) / math.sqrt(128)
+        late = pos[None] > base + torch.arange(tq, device="cuda")[:, None]
+        x.masked_fill_(late[:, None, None], -math.inf)
+        p = torch.softmax(x, -1)
+        o, A = (torch.einsum("tgrp,pgd->tgrd", p, y).reshape(tq, 16, 128) for y in (vv, vv.abs()))
+        assert ((out.double() - o).abs() <= 2.0 ** -8 * (o.abs() + A) * 1.01 + 6.2e-4 * A).all()
+    else:
+        for page in table[0].tolist():
+            for c in (k, v):
+                c[page].random_(0, 256, generator=g)
+    before = [c[table[0].long()].clone() for c in (k, v)]
+    path = [1, 7, 8, 19]
+    mx.tree_commit(prob, cu, lens, table, dev([path], I32), dev([4], I32), view(k), view(v), flags=f)
+    assert f.item() == 0
+    parts = [(0, 64), (ps * 64, 8)] if kind == "nvfp4" else [(0, row)]
+    for c, old in zip((k, v), before):
+        new = old.clone()
+        for i, j in enumerate(path):
+            a, b = base + j, base + i
+            for at, n in parts:
+                new[b // ps, :, at + b % ps * n:at + b % ps * n + n] = old[a // ps, :, at + a % ps * n:at + a % ps * n + n]
+        assert torch.equal(c[table[0].long()], new)
+
+
 # ------------------------------------------------------------- all in a row
 def test_speculative_steps_in_a_row():
     """Prompts into the cache, then two rounds of drafted trees: tables, masks, norm + rotation + store, attention
