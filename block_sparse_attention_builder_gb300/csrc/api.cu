@@ -541,9 +541,11 @@ mxsa_status mxsa_tree_commit(const mxsa_problem* problem, const int64_t* cu_seql
   if (max_path < 1) return MXSA_ERR_INVALID_ARG;
   if (p.kv_dtype == MXSA_NVFP4 && idx_cache) return MXSA_ERR_UNSUPPORTED;  // index keys stay 16-bit or FP8
   if (idx_cache && (idx_heads <= 0 || idx_dim <= 0 || idx_dim % 8 != 0)) return MXSA_ERR_INVALID_ARG;
-  if (!cu_seqlens_q || !used_kv_lens || !block_tables || !path || !path_lens || !k_cache || !v_cache ||
-      kv_lens_out == used_kv_lens)
+  if (!cu_seqlens_q || !used_kv_lens || !block_tables || !path || !path_lens || !k_cache || !v_cache)
     return MXSA_ERR_INVALID_ARG;
+  // (one CTA would write a length that another has not read yet)
+  const uintptr_t len0 = (uintptr_t)used_kv_lens, len1 = (uintptr_t)kv_lens_out, len_bytes = 4 * (uintptr_t)p.num_seqs;
+  if (kv_lens_out && len0 < len1 + len_bytes && len1 < len0 + len_bytes) return MXSA_ERR_INVALID_ARG;
   if (!aligned(cu_seqlens_q, 8) || !aligned(used_kv_lens, 4) || !aligned(block_tables, 4) || !aligned(path, 4) ||
       !aligned(path_lens, 4) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(idx_cache, 16) ||
       !aligned(kv_lens_out, 4) || !aligned(device_flags, 4))

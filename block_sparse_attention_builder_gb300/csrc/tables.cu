@@ -206,8 +206,9 @@ __global__ void __launch_bounds__(kFillThreads) k_tables_fill(TablesArgs a, int 
     if (i < a.num_seqs) base[i] = a.used[i] - ((int)a.cu[i + 1] - c);
   }
   __syncthreads();
-  const int t0 = blockIdx.x * per_cta, t1 = min(a.total_q, t0 + per_cta);
-  for (int t = t0 + 2 * (int)threadIdx.x; t < t1; t += 2 * kFillThreads) fill_tokens(a, start, base, t);
+  // (64 bits: the last round may pass 2^31)
+  const long long t0 = (long long)blockIdx.x * per_cta, t1 = min((long long)a.total_q, t0 + per_cta);
+  for (long long t = t0 + 2 * threadIdx.x; t < t1; t += 2 * kFillThreads) fill_tokens(a, start, base, (int)t);
 }
 
 struct MaskArgs {

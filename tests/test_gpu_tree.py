@@ -613,3 +613,115 @@ def test_speculative_steps_in_a_row():
             page, off = table[s].long()[dev(pos // ps, I64)], dev(pos % ps, I64)
             for cache, i in ((kc, 0), (vc, 1)):
                 assert torch.equal(cache[page, :, off], torch.stack([h[i] for h in held_rows[s]]))
+
+
+@pytest.mark.parametrize("width", [6, 400])  # tables that the one launch takes, and ones that the three do
+def test_captured_steps_give_what_eager_ones_do(width):
+    """Tables, masks, store, attention and commit of a step as one graph on a stream of its own, replayed with other
+    trees and paths: the same bits as the same calls one by one."""
+    B, n, hq, hkv, ps, pages, t = 6, 12, 16, 2, 64, 60, torch.float16
+    cap = B * n + 3
+    prob = mx.make_problem(B, cap, hq, hkv, 0, ps, pages, width, q_dtype=t)
+    half = torch.arange(64, dtype=torch.float64, device="cuda") / 64
+    angle = torch.arange(400, dtype=torch.float64, device="cuda")[:, None] * 10000.0 ** -half
+    cos_sin = torch.cat([angle.cos(), angle.sin()], 1).float()
+
+    def play(captured):
+        r, g = np.random.RandomState(8), torch.Generator(device="cuda").manual_seed(4)
+        e = lambda *s, dt=I32: torch.zeros(*s, dtype=dt, device="cuda")
+        lens, held, table, free, count = e(B), e(B), e(B, width), dev(np.arange(pages), I32), dev([pages], I32)
+        new, parents, path, plens, f = e(B), e(cap), e(B, n), e(B), e(1)
+        kc, vc = (e(pages, hkv, ps, 128, dt=t) for _ in range(2))
+        cu, used, positions, loc, mask = e(B + 1, dt=I64), e(B), e(cap, dt=I64), e(cap, dt=I64), e(cap, 1)
+        qkv, q, out = e(cap, (hq + 2 * hkv) * 128, dt=t), e(cap, hq, 128, dt=t), e(cap, hq, 128, dt=t)
+        lse = e(hq, cap, dt=torch.float32)
+        ws = torch.empty(mx.dense_shared_workspace_size(prob), dtype=torch.uint8, device="cuda")
+        rows = [qkv[:, a * 128:b * 128].unflatten(1, (b - a, 128)) for a, b in
+                ((0, hq), (hq, hq + hkv), (hq + hkv, hq + 2 * hkv))]
+
+        def step():
+            mx.build_tables(prob, lens, new, held, table, free, count, cu, used, positions, loc, flags=f)
+            mx.tree_mask(prob, parents, cu, used, mask, positions, flags=f)
+            mx.norm_rope_store(prob, positions, loc, cos_sin, *rows, q, kc, vc, flags=f)
+            mx.tree_fwd(prob, q, kc, vc, table, cu, used, mask, None, None, ws, out, lse, flags=f)
+            mx.tree_commit(prob, cu, used, table, path, plens, kc, vc, lens, flags=f)
+
+        graph, side, got = torch.cuda.CUDAGraph(), torch.cuda.Stream(), []
+        if captured:
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph, stream=side):
+                step()
+        for i in range(6):
+            sizes = [int(x) for x in r.randint(0, n + 1, B)]
+            trees = [random_parents(r, x) for x in sizes]
+            ends = [np.flatnonzero(ancestors(p)[r.randint(len(p))]).tolist() if len(p) else [] for p in trees]
+            new.copy_(dev(sizes, I32))
+            parents[:sum(sizes)].copy_(dev(sum((list(p) for p in trees), []), I32))
+            path.copy_(dev([x + [-1] * (n - len(x)) for x in ends], I32))
+            plens.copy_(dev([len(x) for x in ends], I32))
+            qkv.copy_(torch.randn(qkv.shape, device="cuda", generator=g))
+            torch.cuda.synchronize()
+            if captured:
+                with torch.cuda.stream(side):
+                    graph.replay()
+            else:
+                step()
+            torch.cuda.synchronize()
+            assert f.item() == 0
+            got.append([x.clone() for x in (out, lse, kc, vc, lens, table, mask, positions, loc)])
+        return got
+
+    for a, b in zip(play(False), play(True)):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_commits_at_once_and_captured(kind):
+    """Two layers' caches committed on two streams at once, then both in replayed graphs with other paths."""
+    qd, kd = KINDS[kind]
+    r = np.random.RandomState(6)
+    B, hkv, ps, pages, width, n = 40, 4, 64, 400, 6, 50
+    prob = mx.make_problem(B, B * n, 16, hkv, 0, ps, pages, width, q_dtype=qd, kv_dtype=kd)
+    table = dev(r.permutation(pages)[:B * width].reshape(B, width), I32)
+    cu, lens = dev(np.arange(B + 1) * n, I64), dev(r.randint(n, width * ps + 1, B), I32)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    layers = [[torch.randint(0, 256, (pages, hkv, ps, 256 if kind == "bf16" else 128), dtype=torch.uint8, device="cuda",
+                             generator=g) for _ in range(2)] for _ in range(2)]
+    path, plens, f = torch.zeros(B, n, dtype=I32, device="cuda"), torch.zeros(B, dtype=I32, device="cuda"), dev([0], I32)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    # raw bytes of a cache as its rows' type
+    views = [[c.view(kd).view(pages, hkv, ps, 128) for c in x] for x in layers]
+    commit = lambda i: mx.tree_commit(prob, cu, lens, table, path, plens, *views[i], flags=f)
+
+    def draw_paths():
+        paths = [random_path(r, n, n) for _ in range(B)]
+        path.copy_(dev([x + [0] * (n - len(x)) for x in paths], I32))
+        plens.copy_(dev([len(x) for x in paths], I32))
+        return paths
+
+    def check(run):
+        paths, old = draw_paths(), [[c.clone() for c in x] for x in layers]
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                run(i)
+        torch.cuda.synchronize()
+        tab, ln = table.cpu().numpy(), lens.tolist()
+        for x, was in zip(layers, old):
+            for c, o in zip(x, was):
+                want = o.clone()
+                for s, p in enumerate(paths):
+                    src, dst = (np.asarray(p, int) + ln[s] - n, np.arange(len(p)) + ln[s] - n)
+                    a, b = (dev(tab[s][y // ps], I64) for y in (src, dst))
+                    want[b, :, dev(dst % ps, I64)] = o[a, :, dev(src % ps, I64)]
+                assert torch.equal(c, want)
+        assert f.item() == 0
+
+    check(commit)
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            commit(i)
+    for _ in range(3):
+        check(lambda i: graphs[i].replay())

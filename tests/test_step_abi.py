@@ -80,6 +80,8 @@ def test_tree_commit(lib):
     refuses(call, None, dict(cu=8, k=16, v=16, idx=16), ["cu", "lens", "bt", "path", "n", "k", "v"], ["out", "flags"])
     assert call(wide=0) == 1
     assert call(out=FAKE) == 1  # the lengths themselves: other heads still read them
+    for off in (-4, 4):  # nor part of them
+        assert call(out=P((1 << 20) + off)) == 1
     other = P(1 << 21)
     assert call(out=other, idx=FAKE, ih=0, idim=64) == 1 and call(idx=FAKE, ih=1, idim=60) == 1
     assert call(idx=FAKE8, ih=1, idim=64) == 1
