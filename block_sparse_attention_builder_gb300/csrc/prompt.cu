@@ -284,7 +284,6 @@ __global__ void __launch_bounds__(kRThreads, 1)
     return t->n0 > 0;
   };
 
-  // 384 x 168 registers at launch: 256 x 208 for the softmax, 128 x 88 for the others
   if (warp < 4) {
     if (warp == kRProducer) {
       // -------------------------------------------------------------- producer

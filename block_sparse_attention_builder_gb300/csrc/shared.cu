@@ -27,6 +27,12 @@
 // (persistent, one CTA per SM) and k_shared_join.  64 decoding sequences of
 // 64 + 8 heads on a prefix of 32768 keys and 128 to 2048 of their own: 7, 84
 // and 8 us, 109 to 110 us in all.
+//
+// Drafted trees (mxsa_tree_fwd, kTree): the same plan, forward and join.  The
+// keys of a sequence's new tokens are seen where the row's mask has their bit
+// set, read a word of 32 keys at a time in the blocks that reach them; all
+// other blocks take the path without a mask.  64 trees of 16 tokens on 4096 to
+// 32768 keys, 64 + 8 heads: 804 us, 6.1 TB/s.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

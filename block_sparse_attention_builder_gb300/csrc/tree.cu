@@ -14,7 +14,9 @@
 // to shared memory, where the ring was; after a barrier of the cluster each CTA
 // joins every C-th row from the cluster's 2 C pieces and writes it.
 //
-// Bound: latency, a chain of lengths, table, keys, q k^T, softmax, P V, join.
+// Bound: latency, a chain of lengths, table, keys, q k^T, softmax, P V, join: one
+// sequence of 8 tokens on 1000 keys, 16 + 2 heads, 8.7 us (17.6 in three
+// launches); 4 of 5 on 2000, 64 + 8 heads, 13.1 (21.4).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
