@@ -114,13 +114,32 @@ __device__ __forceinline__ void scale_o(uint32_t tO, float f) {
   }
 }
 
-// P = 2^(S * scale - m) of 64 keys of a row, packed, to TMEM; returns their
-// sum, and the largest S in `most`.
+// The largest of 64.
+__device__ __forceinline__ float max64(const float* sv) {
+  float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 64; k += 4) {
+    b0 = hmax3(b0, sv[k], sv[k + 1]);
+    b1 = hmax3(b1, sv[k + 2], sv[k + 3]);
+  }
+  return fmaxf(b0, b1);
+}
+
+// How large the P of 64 keys may be before the reference m is raised.  Their sum,
+// which is there anyway, stands for their maximum (it is within 2^6 of it).  In
+// the second half of a block, where raising has to wait for a product, the limit
+// is what fp16 holds: what is left so is found in the next block's first half.
+constexpr float kSumLow = 1024.f, kSumHigh = 16384.f;
+// How far (log2 units) the maximum may be above m where it is found anyway, and
+// where such a sum asked for it: there less than the 2^4 that kSumLow says, so that
+// P are made twice once and not in every block.
+constexpr float kGapKnown = 8.f, kGapSum = 3.f;
+
+// P = 2^(S * scale - m) of 64 keys of a row, packed, to TMEM; returns their sum.
 template <bool kBf16>
-__device__ __forceinline__ float exp_half(const float* sv, float scale_log2, float m, uint32_t tP, float* most) {
+__device__ __forceinline__ float exp_half(const float* sv, float scale_log2, float m, uint32_t tP) {
   const uint64_t scale2 = pack_f2(scale_log2, scale_log2), off2 = pack_f2(-m, -m);
   uint64_t l0 = pack_f2(0.f, 0.f), l1 = l0;
-  float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     uint32_t pk[16];
@@ -132,8 +151,6 @@ __device__ __forceinline__ float exp_half(const float* sv, float scale_log2, flo
     for (int k = 0; k < 16; ++k) {
       x[k].x = ex2_approx(x[k].x);
       x[k].y = ex2_approx(x[k].y);
-      if (k & 1) b1 = hmax3(b1, sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]);
-      else b0 = hmax3(b0, sv[32 * q + 2 * k], sv[32 * q + 2 * k + 1]);
     }
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -144,7 +161,6 @@ __device__ __forceinline__ float exp_half(const float* sv, float scale_log2, flo
     tmem_st16(tP + 16 * q, pk);
   }
   const float2 ls = unpack_f2(add_f2(l0, l1));
-  *most = fmaxf(b0, b1);
   return ls.x + ls.y;
 }
 

@@ -56,10 +56,6 @@ constexpr int kRThreads = 384;
 constexpr int kRProducer = 0, kRQuery = 1, kRMma = 2;  // warps 2, 3: the issuers of groups 0, 1
 constexpr uint32_t kRTile = 32768;  // 128 rows x 128 x 16-bit
 constexpr int kRStages = 5, kRWork = 2;
-// How far (log2 units) a row's scores may pass the reference m before it is
-// raised; in the second half of a block it may wait for the next block up to
-// kRLag (fp16 holds 2^15).
-constexpr float kRRescale = 8.f, kRLag = 14.f;
 constexpr uint32_t kROffKV = 2 * kRTile;
 constexpr uint32_t kROffCtrl = kROffKV + kRStages * kRTile;
 
@@ -93,6 +89,7 @@ struct RArgs {
   RHeader* hdr;    // null: CTA i has tile i and no other
   const RTile* tiles;
   int32_t num_seqs, total_q, Hq, Hkv, G, T, causal;
+  uint32_t inv_G;  // x / G == x * inv_G >> 16 for x < 128
   float scale_log2;
 };
 
@@ -518,7 +515,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
     const int h = (warp >> 2) - 1, r = tid & 127;  // row of the half == TMEM lane
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + h * 256 + lane_addr, tO = tS + 128;
-    const int rt = r / a.G, tt = h * a.T + rt, hh = r - rt * a.G;
+    const int rt = r * a.inv_G >> 16, tt = h * a.T + rt;
     int at = 0, n_s = 0, n_o = 0;
     bool ok = true;
     RTile t;
@@ -532,8 +529,11 @@ __global__ void __launch_bounds__(kRThreads, 1)
       // keys that the row sees (padding rows see all: nobody reads them)
       const int see = live ? (a.causal ? t.t0 + tt + 1 : t.len) : INT_MAX;
       const int warp_see = __reduce_min_sync(0xffffffffu, see);
-      float m = -INFINITY, l = 0.f, bm = -INFINITY;
-      bool late = false;  // the block before passed m by more than kRRescale, and by kRLag at most
+      // A row that is not live, whose q may be anything, has P of zero: it must have
+      // no say in what its warp does, or the others' bits would not be the same
+      // every time.
+      float m = live ? -INFINITY : INFINITY, l = 0.f;
+      bool fresh = true;  // there are rows without a finite maximum
       for (int i = 0; i < n && ok; ++i, ++n_s) {
         const int k0 = i << 7;
         ok = hwarp_all(mbar_wait(&c.s_full[h], n_s & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
@@ -562,46 +562,41 @@ __global__ void __launch_bounds__(kRThreads, 1)
             tmem_ld32(tS + 64 * hf + 32, sv + 32);
             tmem_ld_wait();
             const int kh = k0 + 64 * hf;
-            bool up = late;  // (the same in every lane) rows have passed m
-            if (kh + 64 > warp_see || kh == 0) {  // masked keys, or no maximum yet
-              if (kh + 64 > warp_see) {
-#pragma unroll
-                for (int k = 0; k < 64; ++k) sv[k] = kh + k < see ? sv[k] : -INFINITY;
-              }
-              float b0 = -INFINITY, b1 = -INFINITY;
-#pragma unroll
-              for (int k = 0; k < 64; k += 4) {
-                b0 = hmax3(b0, sv[k], sv[k + 1]);
-                b1 = hmax3(b1, sv[k + 2], sv[k + 3]);
-              }
-              bm = fmaxf(late ? bm : -INFINITY, fmaxf(b0, b1) * a.scale_log2);
-              up = __any_sync(0xffffffffu, bm > m + kRRescale);
-            }
+            const bool masked = kh + 64 > warp_see;
             float sum;
-            while (true) {
-              if (up) {
-                // O is complete up to the block before (S's barrier follows
-                // every product issued before it); in the second half the
-                // first one's product has to be done too
-                if (hf) {
-                  ok = hwarp_all(mbar_wait(&c.lo_done[h], n_s & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
-                  if (!ok) break;
-                  tc_fence_after();
+            // m is looked at first where keys are masked or there is none yet, else
+            // once the P say that they are too large (all these conditions are the same
+            // in every lane)
+            float gap = kGapKnown;
+            for (bool known = masked || fresh;; known = true, gap = kGapSum) {
+              if (__builtin_expect(known, 0)) {
+                if (masked) {
+#pragma unroll
+                  for (int k = 0; k < 64; ++k) sv[k] = kh + k < see ? sv[k] : -INFINITY;
                 }
-                const bool raise = bm > m + kRRescale;
-                const float f = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - bm)) : 1.f;
-                tmem_st_wait();
-                if (kh > 0) scale_o(tO, f);
-                if (raise) {
-                  l *= f;
-                  m = bm;
+                const float bm = max64(sv) * a.scale_log2;
+                const bool raise = bm > m + gap;
+                if (__any_sync(0xffffffffu, raise)) {
+                  // O is complete up to the block before (S's barrier follows
+                  // every product issued before it); in the second half the
+                  // first one's product has to be done too
+                  if (hf) {
+                    ok = hwarp_all(mbar_wait(&c.lo_done[h], n_s & 1, abort_flag, fl, MXSA_FLAG_TIMEOUT, kWaitLimitNs));
+                    if (!ok) break;
+                    tc_fence_after();
+                  }
+                  const float f = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - bm)) : 1.f;
+                  tmem_st_wait();
+                  if (kh > 0) scale_o(tO, f);
+                  if (raise) {
+                    l *= f;
+                    m = bm;
+                  }
+                  fresh = __any_sync(0xffffffffu, m == -INFINITY);
                 }
               }
-              sum = exp_half<kBf16>(sv, a.scale_log2, m == -INFINITY ? 0.f : m, tS + 32 * hf, &bm);
-              bm *= a.scale_log2;
-              up = late = __any_sync(0xffffffffu, bm > m + kRRescale);
-              if (!up) break;
-              if (hf && !__any_sync(0xffffffffu, bm > m + kRLag)) break;
+              sum = exp_half<kBf16>(sv, a.scale_log2, m == -INFINITY ? 0.f : m, tS + 32 * hf);
+              if (__builtin_expect(known || !__any_sync(0xffffffffu, sum > (hf ? kSumHigh : kSumLow)), 1)) break;
             }
             if (!ok) break;
             l += sum;
@@ -622,7 +617,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
       ++n_o;
       if (warp_live) {
         tc_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN stays one)
+        const float inv = l == 0.f ? 0.f : rcp_approx(l);  // (a NaN stays one; off by 2^-23 at most)
         // 16 rows and 64 columns at a time, a row's columns spread over four
         // lanes, which then exchange words until each has 16 consecutive bytes:
         // a store then covers 64 bytes of 8 rows.  (With a row to a thread it
@@ -642,7 +637,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
             for (int k = 0; k < 8; ++k) w[k] = hpack2<kBf16>(v[4 * k + 2 * x] * f, v[4 * k + 2 * x + 1] * f);
             quad_transpose(w, lane);
             quad_transpose(w + 4, lane);
-            const int to = row / a.G, ho = row - to * a.G;
+            const int to = row * a.inv_G >> 16, ho = row - to * a.G;
             if (to < a.T && h * a.T + to < t.ntok) {
               uint8_t* orow = a.out + (((size_t)t.key0 + t.t0 + h * a.T + to) * a.Hq + (size_t)t.g * a.G + ho) * 256 +
                               c0 * 2 + (lane & 3) * 16;
@@ -652,7 +647,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
           }
         }
         if (live && a.lse)
-          a.lse[(size_t)(t.g * a.G + hh) * a.total_q + t.key0 + t.t0 + tt] =
+          a.lse[(size_t)(t.g * a.G + r - rt * a.G) * a.total_q + t.key0 + t.t0 + tt] =
               l == 0.f ? -INFINITY : (m + lg2_approx(l)) * 0.69314718055994530942f;
       }
       tc_fence_before();
@@ -718,6 +713,7 @@ cudaError_t launch_prompt(const mxsa_problem& p, const void* q, long long q_stri
   a.Hkv = p.num_kv_heads;
   a.G = G;
   a.T = T;
+  a.inv_G = 65535 / G + 1;
   a.causal = p.causal;
   const float scale = p.softmax_scale > 0.f ? p.softmax_scale : 0.08838834764831845f;  // 1/sqrt(128)
   a.scale_log2 = scale * 1.4426950408889634f;

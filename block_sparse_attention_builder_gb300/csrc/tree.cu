@@ -37,7 +37,6 @@ constexpr int kTThreads = 384;
 constexpr int kTProducer = 0, kTMma = 2;
 constexpr uint32_t kTTile = 32768;  // 128 rows x 128 x 16-bit
 constexpr int kTStages = 5;
-constexpr float kTRescale = 8.f, kTLag = 14.f;  // (prompt.cu's)
 constexpr uint32_t kTOffKV = kTTile;
 constexpr uint32_t kTOffCtrl = kTOffKV + kTStages * kTTile;
 constexpr uint32_t kTPiece = 128 * 512;         // O of one group, over the ring
@@ -335,8 +334,8 @@ __global__ void __launch_bounds__(kTThreads, 1)
     const int base = live ? t.base : INT_MAX / 2;
     const uint32_t* const mask = live ? a.mask + (size_t)(t.tok0 + rt) * a.words : a.mask;
     const int warp_see = __reduce_min_sync(0xffffffffu, min(base, t.len));
-    float m = -INFINITY, l = 0.f, bm = -INFINITY;
-    bool late = false;  // the block before passed m by more than kTRescale, and by kTLag at most
+    float m = live ? -INFINITY : INFINITY, l = 0.f;  // (P of zero where it is not: as in prompt.cu)
+    bool fresh = true;  // there are rows without a finite maximum
     for (int i = 0; i < n && ok; ++i) {
       const int j = 2 * i + h, k0 = (rank + j * C) << 7;
       ok = wait(&c.s_full[h], i & 1);
@@ -361,49 +360,41 @@ __global__ void __launch_bounds__(kTThreads, 1)
           tmem_ld32(tS + 64 * hf + 32, sv + 32);
           tmem_ld_wait();
           const int kh = k0 + 64 * hf;
-          bool up = late;
-          if (kh + 64 > warp_see || (i == 0 && hf == 0)) {  // masked keys, or no maximum yet
-            if (kh + 64 > warp_see) {
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int kq = kh + 32 * q;
-                uint32_t seen = tree_bits(mask, a.words, kq - base);
-                if (kq + 32 > t.len) seen &= kq >= t.len ? 0u : 0xFFFFFFFFu >> (kq + 32 - t.len);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) sv[32 * q + k] = seen >> k & 1 ? sv[32 * q + k] : -INFINITY;
-              }
-            }
-            float b0 = -INFINITY, b1 = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 64; k += 4) {
-              b0 = hmax3(b0, sv[k], sv[k + 1]);
-              b1 = hmax3(b1, sv[k + 2], sv[k + 3]);
-            }
-            bm = fmaxf(late ? bm : -INFINITY, fmaxf(b0, b1) * a.scale_log2);
-            up = __any_sync(0xffffffffu, bm > m + kTRescale);
-          }
+          const bool masked = kh + 64 > warp_see;
           float sum;
-          while (true) {
-            if (up) {
-              if (hf) {  // (as in prompt.cu: the first half's product has to be done)
-                ok = wait(&c.lo_done[h], i & 1);
-                if (!ok) break;
-                tc_fence_after();
+          float gap = kGapKnown;
+          for (bool known = masked || fresh;; known = true, gap = kGapSum) {  // (as in prompt.cu)
+            if (__builtin_expect(known, 0)) {
+              if (masked) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const int kq = kh + 32 * q;
+                  uint32_t seen = tree_bits(mask, a.words, kq - base);
+                  if (kq + 32 > t.len) seen &= kq >= t.len ? 0u : 0xFFFFFFFFu >> (kq + 32 - t.len);
+#pragma unroll
+                  for (int k = 0; k < 32; ++k) sv[32 * q + k] = seen >> k & 1 ? sv[32 * q + k] : -INFINITY;
+                }
               }
-              const bool raise = bm > m + kTRescale;
-              const float f = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - bm)) : 1.f;
-              tmem_st_wait();
-              if (i > 0 || hf) scale_o(tO, f);
-              if (raise) {
-                l *= f;
-                m = bm;
+              const float bm = max64(sv) * a.scale_log2;
+              const bool raise = bm > m + gap;
+              if (__any_sync(0xffffffffu, raise)) {
+                if (hf) {  // (the first half's product has to be done)
+                  ok = wait(&c.lo_done[h], i & 1);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+                const float f = raise ? (m == -INFINITY ? 0.f : ex2_approx(m - bm)) : 1.f;
+                tmem_st_wait();
+                if (i > 0 || hf) scale_o(tO, f);
+                if (raise) {
+                  l *= f;
+                  m = bm;
+                }
+                fresh = __any_sync(0xffffffffu, m == -INFINITY);
               }
             }
-            sum = exp_half<kBf16>(sv, a.scale_log2, m == -INFINITY ? 0.f : m, tS + 32 * hf, &bm);
-            bm *= a.scale_log2;
-            up = late = __any_sync(0xffffffffu, bm > m + kTRescale);
-            if (!up) break;
-            if (hf && !__any_sync(0xffffffffu, bm > m + kTLag)) break;
+            sum = exp_half<kBf16>(sv, a.scale_log2, m == -INFINITY ? 0.f : m, tS + 32 * hf);
+            if (__builtin_expect(known || !__any_sync(0xffffffffu, sum > (hf ? kSumHigh : kSumLow)), 1)) break;
           }
           if (!ok) break;
           l += sum;

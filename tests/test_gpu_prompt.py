@@ -126,6 +126,40 @@ def test_against_the_definition(name):
     Prompts(seed=len(name), **CASES[name]).run().check()
 
 
+# how far the scores of each 64 keys lie above those of the first ones (log2 units): below what raises the reference,
+# in the first half of a block, in its second half below and past what may stay, far down, far up, and a first key
+# above all others
+STEPS = [0, 3, 5, 5, 5, 11, 11, 17, 17, 40, 40, 12, 200, 200, 150, 206, 215, 215, 226, -300, 226, 231, 226]
+
+
+@pytest.mark.parametrize("q,sink", [("bf16", 0), ("fp16", 0), ("fp16", 240), ("bf16", 240)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_scores_in_steps(q, sink, causal):
+    n = 64 * len(STEPS) - 10
+    p = Prompts([n], hq=12, hkv=4, q=q, causal=causal, seed=15, packed=False)
+    up = torch.tensor(STEPS, dtype=torch.float32, device="cuda").repeat_interleave(64)[:n]
+    up[0] = sink
+    p.q.mul_(0.25)
+    p.q[..., 0] = 16
+    p.k[..., 0] = (up * math.log(2) / (16 * p.scale))[:, None].to(p.k.dtype)
+    p.run().check()
+
+
+def test_rows_that_are_no_tokens_change_no_bits():
+    """Three heads to a kv head leave two rows of a half without a query: whatever stands there."""
+    p = Prompts([700, 41, 130], hq=12, hkv=4, seed=16)
+    p.run().check()
+    want, lse = p.out.clone(), p.lse.clone()
+    for size in (1e-3, 300.0, float("inf")):
+        other = Prompts([900] * 3, hq=16, hkv=4, seed=17, packed=False)
+        other.q.copy_(torch.full_like(other.q, size))
+        other.run()
+        p.out.fill_(9)
+        p.run()
+        torch.cuda.synchronize()
+        assert torch.equal(p.out, want) and torch.equal(p.lse, lse)
+
+
 def test_without_lse_and_flags_and_on_a_given_stream():
     p = Prompts([300, 20], seed=5).run()
     torch.cuda.synchronize()

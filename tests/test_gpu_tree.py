@@ -328,6 +328,21 @@ def test_scores_that_grow_along_the_keys(wide):
         assert ((t.out[a:b].double() - o).abs() <= tol).all()
 
 
+def test_rows_that_are_no_tokens_change_no_bits():
+    """Three heads to a kv head leave rows of a tile without a query: whatever stands there."""
+    t = Trees([(16, 700), (7, 500), (42, 130)], hq=12, hkv=4, seed=11)
+    t.run().check()
+    want, lse = t.out.clone(), t.lse.clone()
+    for size in (1e-3, 300.0, float("inf")):
+        other = Trees([(16, 900)] * 3, hq=16, hkv=4, seed=12)
+        other.q.fill_(size)
+        other.run()
+        t.out.fill_(9)
+        t.run()
+        torch.cuda.synchronize()
+        assert torch.equal(t.out, want) and torch.equal(t.lse, lse)
+
+
 # ------------------------------------------------------------------ the masks
 @pytest.mark.parametrize("sizes,words", [([1], 1), ([8, 16, 3], 1), ([0, 33, 0, 64, 65], 3), ([2048], 64),
                                          ([125] * 30, 4), ([5, 7], 64), (rand(1024, 0, 6, 7), 1)])
