@@ -17,24 +17,28 @@
 // TMEM: S (P over it) and O of each group, 512 columns.
 //
 // Softmax of a block, 64 keys at a time.  P = 2^(S - m) is made with the
-// reference m of the blocks before while the keys' own maximum is found beside
-// it; only when a row passes m by 2^8 (rare past the first blocks) is m raised,
-// O in TMEM rescaled and P made again.  So neither the maximum nor a second
-// reading of S is in the way of the exponentials.  First and masked blocks find
-// their maximum first.
+// reference m of the blocks before; the sum of the 64, which is there anyway, says
+// whether a row has passed m by much (rare past the first blocks).  Only then the
+// maximum is looked for, m raised, O in TMEM rescaled and P made again.  So neither
+// a maximum nor a second reading of S is in the way of the exponentials.  First and
+// masked keys have their maximum found first.
 //
-// Bound: a group's chain of softmax (1400 cycles a block, one warp of the group
-// per scheduler at a time: 64 exponentials of 32 rows take 256 of the 590 that
-// their code takes), its hand-overs (230 and 300) and its products (1024); with
-// both groups in turn 2870 cycles a block pair, of which the tensor pipe works
-// 2048.  8192 tokens of 64 + 8 heads, causal: 681 us, 1.61 PFLOP/s; 16384: 2.56
-// ms, 1.72 PFLOP/s (the SM clock then falls to 1.82 GHz).  On the way there:
-// one issuer for both groups 841 us (its own bookkeeping of 600 cycles a block
-// stood between the products), without turns 731, P handed over whole 747, rows
-// written one to a thread 705.  A row's 128 scores held at once, loads of the
-// second 64 ahead of the first ones' exponentials, a split of the registers
-// between the warps and a hand-over of the turn before q k^T's last products
-// were each slower.
+// Bound: a group's chain of softmax (1300 cycles a block; 64 exponentials, sums and
+// conversions of 32 rows take 356 at least while the other group is at its own),
+// its hand-overs (230 and 300) and its products (1024); with both groups in turn
+// 2690 cycles a block pair, of which the tensor pipe works 2048.  8192 tokens of
+// 64 + 8 heads, causal: 634 us, 1.73 PFLOP/s; 16384: 2.43 ms, 1.81; 32768: 10.5
+// ms, 1.68 (the SM clock then falls below 1.85 GHz).  On the way there, 8192
+// tokens: one issuer for both groups 841 us (its own bookkeeping of 600 cycles a
+// block stood between the products), without turns 731, P handed over whole 747,
+// rows written one to a thread 705, a maximum found beside the exponentials 681.
+// Two warps to a row, each with 64 of a block's keys and 104 registers a thread,
+// were slower (716: they meet at barriers, and the unit that makes exponentials and
+// conversions is the same), and so were a row's 128 scores held at once, loads of
+// the second 64 ahead of the first ones' exponentials, a split of the registers
+// between the warps, masks as bits, and a hand-over of the turn before q k^T's last
+// products.  A run over the rows' code ahead of the first tile, so that it is
+// fetched by then, changed nothing.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
