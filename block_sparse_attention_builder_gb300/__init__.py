@@ -222,15 +222,17 @@ def _need_attention(what: str, prob: Problem, q=None, k_cache=None, v_cache=None
 
 
 # the current stream's handle without a Stream object around it (a fifth of a
-# small call's host time), where this torch has it
+# small call's host time), where this torch has it, and the current device
+# without a look at whether CUDA has started (0.15 us; tensors on it are there)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream) -> int:
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return torch.cuda.current_stream().cuda_stream
 
 
