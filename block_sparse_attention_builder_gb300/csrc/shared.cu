@@ -1346,6 +1346,7 @@ struct HJoinArgs {
   int32_t Hkv, G, total_q;
   int32_t tokens;  // of one CTA
   int32_t slots;   // rows at once: a power of two, at most the warps
+  int32_t rows;    // of one CTA (blockIdx.y), a multiple of slots
   int32_t cap;     // partials of one row, at most
 };
 
@@ -1386,7 +1387,8 @@ __global__ void __launch_bounds__(kHJoinWarps * 32) k_shared_join(HJoinArgs a) {
   }
   __syncthreads();
   const int splits = kHJoinWarps / a.slots, slot = warp & (a.slots - 1), part = warp / a.slots;
-  for (int i0 = 0; i0 < nt * a.G; i0 += a.slots) {
+  const int row0 = blockIdx.y * a.rows, row1 = min(nt * a.G, row0 + a.rows);
+  for (int i0 = row0; i0 < row1; i0 += a.slots) {
     const int row = i0 + slot, x = row / a.G, hh = row - x * a.G;
     const int n = row < nt * a.G ? count[x] : -1;
     const int32_t* list = lists + x * a.cap;
@@ -1555,7 +1557,14 @@ cudaError_t launch_dense_shared(const mxsa_problem& p, const void* q, const void
   ja.slots = 1;
   while (ja.slots < G * ja.tokens && ja.slots < kHJoinWarps) ja.slots *= 2;
   const long long blocks = (long long)((p.total_q + ja.tokens - 1) / ja.tokens) * p.num_kv_heads;
-  return launch_pdl(bf16 ? k_shared_join<true> : k_shared_join<false>, dim3((unsigned)blocks), dim3(kHJoinWarps * 32),
+  // A token's rows to several CTAs where SMs would have none (5 tokens of 128 + 1
+  // heads on 8000 keys: the call 132 us with a CTA to a token, 28 so).
+  // A row's pieces are added in the same order either way.
+  const int passes = (G * ja.tokens + ja.slots - 1) / ja.slots;
+  const int parts = (int)std::max(1LL, std::min<long long>(passes, 4LL * sms / blocks));
+  ja.rows = (passes + parts - 1) / parts * ja.slots;
+  const unsigned ys = (unsigned)((G * ja.tokens + ja.rows - 1) / ja.rows);
+  return launch_pdl(bf16 ? k_shared_join<true> : k_shared_join<false>, dim3((unsigned)blocks, ys), dim3(kHJoinWarps * 32),
                     (size_t)ja.tokens * ja.cap * 4, st, ja);
 }
 
