@@ -113,6 +113,9 @@ CASES = {
     "many": dict(lens=rand(60, 1, 700, 1), hq=16, hkv=4, lead=2, tail=5),
     "many_full": dict(lens=rand(40, 1, 500, 2), hq=16, hkv=4, causal=False, q="fp16"),
     "seqs_1024": dict(lens=rand(1024, 0, 9, 3), hq=8, hkv=1, tail=1),
+    # tiles of one half, which the groups take in turn
+    "one_half_each": dict(lens=rand(300, 0, 128, 4), hq=4, hkv=4, lead=1),
+    "one_half_now_and_then": dict(lens=rand(150, 1, 90, 5), hq=12, hkv=4, q="fp16", causal=False, tail=2),
     "long": dict(lens=[5000, 77], hq=16, hkv=2),
     "scaled": dict(lens=[400], scale=0.03),
     # the running maximum is raised in most blocks (P made twice)

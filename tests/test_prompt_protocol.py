@@ -23,7 +23,7 @@ STAGES, WORK = 5, 2
 
 class Forward:
     def __init__(self, tiles, rnd):
-        """tiles: (n0, n1, whether rows of V behind the sequence are cleared); n1 is 0, n0 or n0 + 1."""
+        """tiles: (n0, n1, whether rows of V behind the sequence are cleared); n1 is 0, n0 or n0 + 1, or n0 is 0."""
         self.tiles, self.rnd = tiles, rnd
         self.bar, self.landing, self.abort = {}, {}, False
         for name, count, n in (("q_full", 1, 2), ("q_empty", 1, 2), ("kv_full", 1, 2 * STAGES),
@@ -70,7 +70,7 @@ class Forward:
         roles.update({("mma", h): self.issuer(h) for h in range(2)})
         roles.update({("soft", h, w): self.softmax(h, w) for h in range(2) for w in range(4)})
         waits = {k: None for k in roles}
-        steps, limit = 0, self.rnd.randint(1, 60 * sum(t[0] for t in self.tiles)) if give_up else None
+        steps, limit = 0, self.rnd.randint(1, 60 * sum(max(t[:2]) for t in self.tiles)) if give_up else None
         while roles or any(self.landing.values()):
             steps += 1
             can = [k for k in roles if waits[k] is None or self.ready(waits[k])]
@@ -136,7 +136,9 @@ class Forward:
             if tile is None:
                 break
             taken += 1
-            for h in range(2 if tile[1] else 1):
+            for h in range(2):
+                if not tile[h]:
+                    continue
                 ok = yield "q_empty", h, n[h] - 1
                 if not ok:
                     break
@@ -158,7 +160,7 @@ class Forward:
             if tile is None:
                 break
             taken += 1
-            n, blocks, both = tile[h], max(tile[:2]), tile[1] > 0
+            n, blocks, both = tile[h], max(tile[:2]), min(tile[:2]) > 0
             start = place
             for i in range((blocks if both else n) + 1):
                 if i > n or n == 0:
@@ -284,7 +286,10 @@ def random_tiles(r):
     tiles = []
     for _ in range(r.randint(1, 8)):
         n0 = r.choice([1, 1, 2, 3, r.randint(1, 9), r.randint(8, 25)])
-        tiles.append((n0, r.choice([0, n0, n0, n0 + 1]), r.random() < 0.5))
+        n1 = r.choice([0, 0, n0, n0, n0 + 1])
+        if n1 == 0 and r.random() < 0.5:  # a tile of one half that the second group has
+            n0, n1 = 0, n0
+        tiles.append((n0, n1, r.random() < 0.5))
     return tiles
 
 
@@ -301,6 +306,7 @@ def test_a_group_that_passes_over_long_tiles():
     r = random.Random(7)
     for _ in range(20):
         Forward([(2, 3, True), (23, 0, True), (1, 1, False), (12, 0, False), (9, 10, True)], r).run()
+        Forward([(2, 3, True), (0, 23, True), (1, 0, False), (0, 12, True), (11, 0, False), (9, 9, True)], r).run()
 
 
 @pytest.mark.parametrize("seed", range(40))
