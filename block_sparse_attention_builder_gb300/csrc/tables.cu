@@ -145,6 +145,17 @@ __global__ void __launch_bounds__(kPlanThreads) k_tables_plan(TablesArgs a) {
   if (total[0] > a.total_q) bad |= MXSA_FLAG_CU;
   const bool list_ok = count >= 0 && count + total[2] <= a.num_pages;
   if (!len_bad && (!list_ok || total[1] > count + total[2])) bad |= MXSA_FLAG_PAGES;
+  const int gives = bad ? 0 : (int)total[2];
+  if (gives > 0) {  // (uniform) what goes back has to be pages: looked at before anything is written
+    if (s < B) back0[s] = (int)(x[2] - v[2]);
+    __syncthreads();
+    int wrong = 0;
+    for (int k = s; k < gives; k += kPlanThreads) {
+      const int r = find_le(back0, B, k), page = a.block_tables[(size_t)r * a.max_pages + k - back0[r]];
+      wrong |= page < 0 || page >= a.num_pages;
+    }
+    if (__syncthreads_or(wrong)) bad = MXSA_FLAG_PAGES;
+  }
   if (bad) {  // (the same in every thread) nothing is given out or taken back
     if (s < B) {
       a.used[s] = o_in;
@@ -159,11 +170,10 @@ __global__ void __launch_bounds__(kPlanThreads) k_tables_plan(TablesArgs a) {
       if (a.flags) atomicOr(a.flags, bad);
     }
   } else {
-    const int top = count + (int)total[2], wants = (int)total[1], gives = (int)total[2];
+    const int top = count + gives, wants = (int)total[1];
     if (s < B) {
       start[s] = (int)(x[0] - v[0]);
       want0[s] = (int)(x[1] - v[1]);
-      back0[s] = (int)(x[2] - v[2]);
       held[s] = h;
       base[s] = o;
       a.cu[s] = x[0] - v[0];
@@ -176,7 +186,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_tables_plan(TablesArgs a) {
       *a.free_count_out = top - wants;
     }
     __syncthreads();
-    if (gives > 0) {  // (uniform) finished requests' pages, behind the free ones
+    if (gives > 0) {  // finished requests' pages, behind the free ones
       for (int k = s; k < gives; k += kPlanThreads) {
         const int r = find_le(back0, B, k);
         a.free_pages[count + k] = a.block_tables[(size_t)r * a.max_pages + k - back0[r]];

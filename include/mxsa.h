@@ -80,7 +80,8 @@ typedef enum { MXSA_BF16 = 0, MXSA_FP16 = 1, MXSA_FP8_E4M3 = 2, MXSA_NVFP4 = 3 }
 #define MXSA_FLAG_POS 256       /* a token's position lies past the rotation table: token left out */
 #define MXSA_FLAG_GROUP 512     /* group_ptr is not a non-decreasing list of sequences: groups ignored */
 #define MXSA_FLAG_TREE 1024     /* a drafted tree's parents, path or mask width do not fit it */
-#define MXSA_FLAG_PAGES 2048    /* free list with too few pages, or one that does not fit: nothing given out */
+#define MXSA_FLAG_PAGES 2048    /* free list with too few pages, or one that does not fit, or no pages given back:
+                                 * nothing given out */
 
 /* Problem description (sizes and flags of one call).  The sources: the
  * Quick-start signature and the supported-feature list of the
@@ -420,7 +421,8 @@ mxsa_status mxsa_prompt_fwd(const mxsa_problem* problem, const void* q, int64_t 
  * than total_q (MXSA_FLAG_CU), a length, a held count or a row does not fit
  * (MXSA_FLAG_LEN: kv_lens[s] < 0 or beyond the held pages, pages_held[s]
  * outside [0, max_pages_per_seq], more tokens than a row's pages hold), or the
- * list has too few pages or would outgrow num_pages (MXSA_FLAG_PAGES), no page
+ * list has too few pages or would outgrow num_pages, or an entry that a finished
+ * request gives back lies outside [0, num_pages) (MXSA_FLAG_PAGES), no page
  * moves: cu_seqlens_q is all 0, positions and loc all -1, the lengths, held
  * counts and list as they came.  A slot in a page outside [0, num_pages) is -1
  * (MXSA_FLAG_PAGE).  Of the problem the call reads num_seqs (<= 1024), total_q,
