@@ -577,7 +577,9 @@ def build_tables(prob, kv_lens, new_lens, pages_held, block_tables, free_pages, 
     cu_seqlens_q int64 [B + 1], used_kv_lens int32 [B], positions and loc int64
     [total_q] (-1: padding) and the rows of block_tables.  pages_held_out and
     free_count_out: None writes pages_held and free_count themselves;
-    used_kv_lens may be kv_lens."""
+    used_kv_lens may be kv_lens.  Pages that go back must be held by no other request: a
+    prefix that others still read has to leave a finished request's first
+    pages_held[s] entries before the call."""
     what = "mxsa_build_tables"
     seqs, total_q = prob.num_seqs, prob.total_q
     pages_held_out = pages_held if pages_held_out is None else pages_held_out

@@ -416,6 +416,16 @@ mxsa_status mxsa_prompt_fwd(const mxsa_problem* problem, const void* q, int64_t 
  *   cu_seqlens_q   device int64 [B + 1]; used_kv_lens, pages_held_out device
  *                  int32 [B]; positions, loc device int64 [total_q]
  *                  (total_q: the step's capacity); free_count_out int32 [1]
+ * The call does not look for pages that several rows hold: what a finished
+ * request gives back is free from then on, whoever else reads it, and a page
+ * given back twice is handed out twice.  So a page that goes back must be among
+ * no other request's first pages_held entries, finished or not, nor in the free
+ * list already.  Requests that share a prefix's pages (the groups of
+ * mxsa_dense_shared_fwd and mxsa_tree_fwd) may have them in their rows and
+ * counts as long as they run; before one of them is finished here while others
+ * still read them, they have to leave its first pages_held[s] entries (its own
+ * pages moved to the front and pages_held[s] their number; 0: nothing goes
+ * back).  The last one gives them back.
  * used_kv_lens may be kv_lens, pages_held_out pages_held and free_count_out
  * free_count; otherwise no two arrays overlap.  When the new tokens are more
  * than total_q (MXSA_FLAG_CU), a length, a held count or a row does not fit
