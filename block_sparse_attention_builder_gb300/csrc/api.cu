@@ -17,6 +17,12 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether two arrays have bytes in common (a null pointer has none).
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + b_bytes && y < x + a_bytes;
+}
+
 int sm_count() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -543,9 +549,12 @@ mxsa_status mxsa_tree_commit(const mxsa_problem* problem, const int64_t* cu_seql
   if (idx_cache && (idx_heads <= 0 || idx_dim <= 0 || idx_dim % 8 != 0)) return MXSA_ERR_INVALID_ARG;
   if (!cu_seqlens_q || !used_kv_lens || !block_tables || !path || !path_lens || !k_cache || !v_cache)
     return MXSA_ERR_INVALID_ARG;
-  // (one CTA would write a length that another has not read yet)
-  const uintptr_t len0 = (uintptr_t)used_kv_lens, len1 = (uintptr_t)kv_lens_out, len_bytes = 4 * (uintptr_t)p.num_seqs;
-  if (kv_lens_out && len0 < len1 + len_bytes && len1 < len0 + len_bytes) return MXSA_ERR_INVALID_ARG;
+  // (one CTA would write over what another, of another head, has not read yet)
+  const size_t B = p.num_seqs;
+  if (overlap(kv_lens_out, 4 * B, used_kv_lens, 4 * B) || overlap(kv_lens_out, 4 * B, path_lens, 4 * B) ||
+      overlap(kv_lens_out, 4 * B, path, 4 * B * max_path) || overlap(kv_lens_out, 4 * B, cu_seqlens_q, 8 * (B + 1)) ||
+      overlap(kv_lens_out, 4 * B, block_tables, 4 * B * p.max_pages_per_seq))
+    return MXSA_ERR_INVALID_ARG;
   if (!aligned(cu_seqlens_q, 8) || !aligned(used_kv_lens, 4) || !aligned(block_tables, 4) || !aligned(path, 4) ||
       !aligned(path_lens, 4) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(idx_cache, 16) ||
       !aligned(kv_lens_out, 4) || !aligned(device_flags, 4))

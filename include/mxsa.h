@@ -351,7 +351,7 @@ mxsa_status mxsa_tree_mask(const mxsa_problem* problem, const int32_t* parents, 
  *   path        device int32 [B][max_path], read up to path_lens[s]
  *   path_lens   device int32 [B], 0 .. max_path
  *   idx_cache   as for mxsa_store_kv, or NULL (idx_heads, idx_dim unused)
- *   kv_lens_out device int32 [B], apart from used_kv_lens, or NULL
+ *   kv_lens_out device int32 [B], apart from every other array, or NULL
  * A path that is not ascending within [0, Tq_s), or longer than max_path, sets
  * MXSA_FLAG_TREE; a length out of range MXSA_FLAG_LEN or, below Tq_s,
  * MXSA_FLAG_CAUSAL_LEN; cu_seqlens_q out of order MXSA_FLAG_CU: of such a
