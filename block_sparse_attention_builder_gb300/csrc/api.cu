@@ -530,6 +530,13 @@ mxsa_status mxsa_tree_mask(const mxsa_problem* problem, const int32_t* parents, 
   if (!aligned(parents, 4) || !aligned(cu_seqlens_q, 8) || !aligned(used_kv_lens, 4) || !aligned(tree_mask, 4) ||
       !aligned(positions, 8) || !aligned(device_flags, 4))
     return MXSA_ERR_INVALID_ARG;
+  // (one thread would write over what another, that walks the same tree, has not read yet)
+  const size_t B = p.num_seqs, n = p.total_q, mask_bytes = 4 * n * mask_words;
+  if (overlap(tree_mask, mask_bytes, parents, 4 * n) || overlap(tree_mask, mask_bytes, cu_seqlens_q, 8 * (B + 1)) ||
+      overlap(tree_mask, mask_bytes, used_kv_lens, 4 * B) || overlap(tree_mask, mask_bytes, positions, 8 * n) ||
+      overlap(positions, 8 * n, parents, 4 * n) || overlap(positions, 8 * n, cu_seqlens_q, 8 * (B + 1)) ||
+      overlap(positions, 8 * n, used_kv_lens, 4 * B))
+    return MXSA_ERR_INVALID_ARG;
   cudaError_t e = launch_tree_mask(p, parents, cu_seqlens_q, used_kv_lens, mask_words, tree_mask, positions,
                                    device_flags, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? MXSA_OK : MXSA_ERR_CUDA;

@@ -333,9 +333,10 @@ mxsa_status mxsa_tree_fwd(const mxsa_problem* problem, const void* q, const void
  * further tokens' bits left out.  MXSA_FLAG_LEN and MXSA_FLAG_CAUSAL_LEN as for
  * the calls that read the lengths (clamped; L < Tq_s: positions below zero).
  * Tokens before cu_seqlens_q[0] and from cu_seqlens_q[B] on are not written;
- * cu_seqlens_q out of order: MXSA_FLAG_CU and nothing is.  Of the problem the
- * call reads num_seqs (<= 1024), total_q, page_size and max_pages_per_seq.
- * One launch, asynchronous on `stream`. */
+ * cu_seqlens_q out of order: MXSA_FLAG_CU and nothing is.  The outputs overlap
+ * neither an input nor one another.  Of the problem the call reads num_seqs
+ * (<= 1024), total_q, page_size and max_pages_per_seq.  One launch,
+ * asynchronous on `stream`. */
 mxsa_status mxsa_tree_mask(const mxsa_problem* problem, const int32_t* parents, const int64_t* cu_seqlens_q,
                            const int32_t* used_kv_lens, int32_t mask_words, uint32_t* tree_mask, int64_t* positions,
                            int32_t* device_flags, void* stream);

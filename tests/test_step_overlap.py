@@ -3,6 +3,7 @@ read: refused before any launch (no GPU)."""
 import ctypes
 
 import pytest
+import torch
 
 import block_sparse_attention_builder_gb300 as mx
 from block_sparse_attention_builder_gb300 import build as B
@@ -40,3 +41,28 @@ def test_tree_commit(lib, name):
         assert call(out) == 1, (name, out - begin)
     for out in (begin - 4 * 3, end):  # next to it
         assert call(out) == 2, (name, out - begin)
+
+
+# the masks' call reads parents, starts and lengths and writes masks (one word a token) and positions
+MASK = dict(parents=4 * 9, cu=8 * 4, lens=4 * 3)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is not refused would run on these pointers")
+@pytest.mark.parametrize("out,size", [("mask", 4 * 9), ("pos", 8 * 9)])
+@pytest.mark.parametrize("name", list(MASK) + ["the other output"])
+def test_tree_mask(lib, name, out, size):
+    at = {x: BASE * (i + 1) for i, x in enumerate(list(MASK) + ["mask", "pos"])}
+    sizes = dict(MASK, mask=4 * 9, pos=8 * 9)
+    name = {"mask": "pos", "pos": "mask"}[out] if name == "the other output" else name
+
+    def call(where):
+        p = {x: P(v) for x, v in dict(at, **{out: where}).items()}
+        return lib.mxsa_tree_mask(ctypes.byref(problem()), p["parents"], p["cu"], p["lens"], 1, p["mask"], p["pos"],
+                                  None, None)
+
+    begin, end = at[name], at[name] + sizes[name]
+    for where in (begin - size + 8, begin, end - 8 if end % 8 == 0 else end - 4):
+        if out == "mask" or where % 8 == 0:
+            assert call(where) == 1, where - begin
+    for where in (begin - size, (end + 7) // 8 * 8):  # next to it: nothing to refuse (and no GPU here)
+        assert call(where) == 4, where - begin
