@@ -187,6 +187,13 @@ def _need(what: str, name: str, t: Optional[torch.Tensor], nbytes: int):
     raise MxsaError(1, f"{what}: {name} holds {t.nbytes} bytes, the problem needs {nbytes}")
 
 
+def _need_given(what: str, **tensors):
+    """Refuses a None where the binding itself looks at the tensor."""
+    for name, t in tensors.items():
+        if t is None:
+            raise MxsaError(1, f"{what}: {name} is None")
+
+
 _I32, _I64, _F32 = torch.int32, torch.int64, torch.float32
 _ROW_TYPE = {BF16: torch.bfloat16, FP16: torch.float16, FP8_E4M3: torch.float8_e4m3fn, NVFP4: torch.uint8}
 
@@ -419,9 +426,10 @@ def tree_fwd(prob, q, k_cache, v_cache, block_tables, cu_seqlens_q, used_kv_lens
                               prefix_lens.dtype is _I32 and prefix_lens.is_contiguous())) and
                  (lse is None or (lse.dtype is _F32 and lse.numel() >= rows and lse.is_contiguous())) and
                  (flags is None or (flags.dtype is _I32 and flags.numel() >= 1)))
-    except AttributeError:  # a None: the library says whether it may be one
+    except AttributeError:  # a None: refused below, or the library says whether it may be one
         plain = False
     if not plain:
+        _need_given(what, tree_mask=tree_mask, ws=ws)
         _need_attention(what, prob, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
                         cu_seqlens_q=cu_seqlens_q, used_kv_lens=used_kv_lens, out=out, lse=lse)
         _need_mask(what, tree_mask, max(total_q, 0))
@@ -457,10 +465,11 @@ def tree_mask(prob, parents, cu_seqlens_q, used_kv_lens, mask, positions=None, f
                  (positions is None or (positions.dtype is _I64 and positions.numel() >= total_q and
                                         positions.is_contiguous())) and
                  (flags is None or (flags.dtype is _I32 and flags.numel() >= 1)))
-    except AttributeError:  # a None: the library says whether it may be one
+    except AttributeError:  # a None: refused below, or the library says whether it may be one
         plain = False
     if not plain:
         total_q, seqs = max(total_q, 0), max(seqs, 0)
+        _need_given(what, mask=mask)
         _need_mask(what, mask, total_q)
         _need(what, "parents", parents, total_q * 4)
         _need(what, "cu_seqlens_q", cu_seqlens_q, (seqs + 1) * 8)
@@ -499,12 +508,13 @@ def tree_commit(prob, cu_seqlens_q, used_kv_lens, block_tables, path, path_lens,
                  (kv_lens_out is None or (kv_lens_out.dtype is _I32 and kv_lens_out.numel() >= seqs and
                                           kv_lens_out.is_contiguous())) and
                  (flags is None or (flags.dtype is _I32 and flags.numel() >= 1)))
-    except AttributeError:  # a None: the library says whether it may be one
+    except AttributeError:  # a None: refused below, or the library says whether it may be one
         plain = False
     if not plain:
         seqs = max(seqs, 0)
         _need_attention(what, prob, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
                         cu_seqlens_q=cu_seqlens_q, used_kv_lens=used_kv_lens)
+        _need_given(what, path=path)
         if path.dim() != 2:
             raise MxsaError(1, f"{what}: path is {tuple(path.shape)}, not [num_seqs, longest path]")
         _need(what, "path", path, seqs * path.shape[1] * 4)
@@ -552,9 +562,10 @@ def prompt_fwd(prob, q, k, v, cu_seqlens, ws, out, lse=None, flags=None, stream=
                  cu_seqlens.numel() > prob.num_seqs and cu_seqlens.is_contiguous() and ws.is_contiguous() and
                  (lse is None or (lse.dtype is _F32 and lse.numel() >= rows and lse.is_contiguous())) and
                  (flags is None or (flags.dtype is _I32 and flags.numel() >= 1)))
-    except AttributeError:  # a None: the library says whether it may be one
+    except AttributeError:  # a None: refused below, or the library says whether it may be one
         plain = False
     if not plain:
+        _need_given(what, ws=ws)
         _need(what, "cu_seqlens", cu_seqlens, (max(prob.num_seqs, 0) + 1) * 8)
         _need(what, "ws", ws, 0)
         _need(what, "out", out, rows * 256)
@@ -685,6 +696,8 @@ def load_kv(prob, loc, k_cache, v_cache, k, v, idx_cache=None, idx_k=None, flags
 def _token_stride(what: str, name: str, t: torch.Tensor, dtype, n: int, heads: int, dim: int) -> int:
     """Elements between the tokens of t [n, heads, dim], a dense tensor or a
     view of a packed projection (a token's heads next to each other)."""
+    if t is None:
+        raise MxsaError(1, f"{what}: {name} is None")
     if t.shape != (n, heads, dim) or (t.dtype is not dtype and t.element_size() != 2):
         raise MxsaError(1, f"{what}: {name} is {tuple(t.shape)} of {t.dtype}, the problem needs "
                            f"{(n, heads, dim)} of a 16-bit type")
