@@ -330,7 +330,8 @@ mxsa_status mxsa_tree_fwd(const mxsa_problem* problem, const void* q, const void
  *   positions      device int64 [total_q]
  * A parent outside [-1, own index) sets MXSA_FLAG_TREE and stands for -1; a
  * sequence of more than 32 * mask_words tokens (1..64 words) sets it too, its
- * further tokens' bits left out.  MXSA_FLAG_LEN and MXSA_FLAG_CAUSAL_LEN as for
+ * further tokens' bits left out and, of a token with more than 2048 ancestors,
+ * those beyond the nearest 2048 neither set nor counted.  MXSA_FLAG_LEN and MXSA_FLAG_CAUSAL_LEN as for
  * the calls that read the lengths (clamped; L < Tq_s: positions below zero).
  * Tokens before cu_seqlens_q[0] and from cu_seqlens_q[B] on are not written;
  * cu_seqlens_q out of order: MXSA_FLAG_CU and nothing is.  The outputs overlap
