@@ -485,27 +485,47 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
 // The cluster's size where the one-launch path is taken, 0 where it is not.  As
 // large as leaves all clusters of the row tiles on the SMs at once (of 8 CTAs 14
-// do, 16 took twice as long), for tables of at most so many blocks: past them a
-// cluster's own keys take longer than the general path's plan and join.  Tiles
-// are counted as if the sequences had equally many tokens (more of them only
-// wait for their turn).  Microseconds of this and of the general path, page 64,
-// lengths from a third of L to L:
-//   1 sequence of 5 tokens, 16 + 2 heads (C = 8): L 500 8.0 and 16.4, 2000 11.2
-//   and 18.7, 8000 15.8 and 30.1, 24000 27.9 and 44.4;
-//   16 of 5, 16 + 2 (C = 4): 500 9.3 and 18.7, 8000 23.6 and 30.9, 24000 57 and
-//   66.6; 4 of 40, 12 + 4 heads: 8000 28.4 and 25.0;
-//   16 of 40, 12 + 4 (C = 2): 500 16.0 and 24.7, 8000 48.6 and 58.1, 24000 113
-//   and 117; 4 of 40, 64 + 8 (C = 1): 2000 29.8 and 36.3, 8000 70.1 and 57.2.
+// do, 16 took twice as long).  Tiles are counted as if the sequences had equally
+// many tokens (more of them only wait for their turn).  A cluster's own keys cost
+// 0.8 us a block and CTA, the general path's plan and join 8 to 15 us; the fewer
+// SMs the clusters leave idle, the later the general path, which uses all of
+// them, is ahead.  The host knows the tables' width and not the lengths: the
+// limits are widths at which the longest tables' worth of keys took no longer
+// here (5% for the spread), and shorter sequences in such tables gain up to
+// twofold.  Microseconds of this and of the general path, page 64, lengths from a
+// third of L to L, inputs from memory:
+//   C = 8, 2 tiles (one sequence of 5 tokens, 16 + 2 heads): L 1000 8 and 16, 8000
+//   17 and 30, 16000 23 and 42, 24000 30 and 45, 64000 63 and 52; 1 tile (8 + 1):
+//   16000 22 and 24, 24000 29 and 28; 4 tiles (8 tokens, 12 + 4): 16000 23 and 25,
+//   24000 30 and 28; 8 tiles (60 tokens, 16 + 2): 16000 28 and 30, 24000 35 and 31;
+//   10 to 14 tiles: 24000 31 and 36, 35 and 38, 36 and 36, 38 and 43;
+//   C = 4, 16 and 20 tiles: 8000 28 and 28, 27 and 29, 16000 42 and 39, 41 and 39; 24
+//   to 32 tiles: 16000 38 and 40, 45 and 48, 42 and 47, 24000 51 and 48, 57 and 55;
+//   C = 2, 40 to 72 tiles: 8000 42 and 41, 44 and 46, 47 and 50, 44 and 55, 16000 66
+//   and 64, 73 and 72, 77 and 82, 24000 109 and 107;
+//   C = 1, 80 to 104 tiles: 4000 43 and 46, 46 and 47, 46 and 53, 8000 69 and 58, 75
+//   and 75; 109 to 152 tiles: 8000 74 and 78, 72 and 75, 82 and 91, 84 and 98, 16000
+//   134 and 120; 110 sequences of 20 tokens, 8 + 1 heads, which are 138 tiles in
+//   number but 220 as they lie: 4000 73 and 69, 8000 114 and 97.
+// Where several row tiles read the same keys the general path, which takes two of
+// a sequence at a time, is ahead earlier: 5 sequences of 8 tokens, 128 + 1 heads
+// (C = 2), 4000 28 and 27, 8000 42 and 33; 6 of 14, 64 + 4, 8000 42 and 36.
 int tree_small_cluster(const mxsa_problem& p, int num_groups) {
   if (num_groups > 0) return 0;
-  const long long T = 128 / (p.num_q_heads / p.num_kv_heads);
-  const long long tiles = std::max<long long>(p.num_seqs, (p.total_q + T - 1) / T) * p.num_kv_heads;
+  const long long T = 128 / (p.num_q_heads / p.num_kv_heads), B = p.num_seqs;
+  const long long tiles = std::max(B, (p.total_q + T - 1) / T) * p.num_kv_heads;
+  // (as they lie, where the sequences have equally many tokens: none has two sequences' rows)
+  const long long whole = B * (((p.total_q + B - 1) / B + T - 1) / T) * p.num_kv_heads;
   const long long blocks = max_blocks_per_seq(p);
+  // Up to so many tiles; for tables of up to so many blocks, and of more with at
+  // least so many tiles that do all have their SMs.
   struct Rule {
-    int cluster, tiles, blocks;
+    int cluster, tiles, blocks, many, many_blocks;
   };
-  for (const Rule r : {Rule{8, 14, 128}, Rule{4, 32, 64}, Rule{2, 72, 64}, Rule{1, 152, 32}})
-    if (tiles <= r.tiles) return blocks <= r.blocks ? r.cluster : 0;
+  for (const Rule r : {Rule{8, 14, 128, 9, 192}, Rule{4, 32, 64, 23, 128}, Rule{2, 72, 64, 0, 64},
+                       Rule{1, 152, 32, 109, 64}})
+    if (tiles <= r.tiles)
+      return blocks <= (tiles >= r.many && whole <= r.tiles ? r.many_blocks : r.blocks) ? r.cluster : 0;
   return 0;
 }
 
