@@ -27,9 +27,10 @@
 // conversions of 32 rows take 356 at least while the other group is at its own),
 // its hand-overs (230 and 300) and its products (1024); with both groups in turn
 // 2690 cycles a block pair, of which the tensor pipe works 2048.  8192 tokens of
-// 64 + 8 heads, causal: 634 us, 1.73 PFLOP/s; 16384: 2.43 ms, 1.81; 32768: 10.5
-// ms, 1.68 (the SM clock then falls below 1.85 GHz).  On the way there, 8192
-// tokens: one issuer for both groups 841 us (its own bookkeeping of 600 cycles a
+// 64 + 8 heads, causal, the GPU at rest before: 634 us, 1.73 PFLOP/s; 16384: 2.44
+// ms, 1.80.  Under lasting load power lowers the SM clock from 2.07 GHz, to 1.83,
+// 1.79 and, at 32768 tokens, 1.73: 688 us, 2.69 and 10.75 ms, 1.60 to 1.64.  On the
+// way there, 8192 tokens: one issuer for both groups 841 us (its own bookkeeping of 600 cycles a
 // block stood between the products), without turns 731, P handed over whole 747,
 // rows written one to a thread 705, a maximum found beside the exponentials 681.
 // Two warps to a row, each with 64 of a block's keys and 104 registers a thread,

@@ -310,9 +310,11 @@ mxsa_status mxsa_dense_shared_fwd(const mxsa_problem* problem, const void* q, co
  * the smallest base_s of the group's sequences with new tokens), the workspace
  * (mxsa_shared_workspace_size), limits, types, roundings and flags;
  * problem->causal is not used.  The V rows of drafted keys that a row does not
- * see, but others of its sequence do, have to be finite.  One launch for few
- * sequences with tables of moderate length and no groups (ws is then not used),
- * else three; asynchronous on `stream`. */
+ * see, but others of its sequence do, have to be finite.  kv_dtype equals
+ * q_dtype as there: rows of FP8 and NVFP4 caches, which mxsa_tree_commit does
+ * take, have to be widened first (mxsa_load_kv).  One launch for few sequences
+ * with tables (max_pages_per_seq, whatever the lengths) of moderate width and no
+ * groups: ws is then given but not used; else three; asynchronous on `stream`. */
 mxsa_status mxsa_tree_fwd(const mxsa_problem* problem, const void* q, const void* k_cache, const void* v_cache,
                           const int32_t* block_tables, const int64_t* cu_seqlens_q, const int32_t* used_kv_lens,
                           const uint32_t* tree_mask, int32_t mask_words, int32_t num_groups,
@@ -331,8 +333,9 @@ mxsa_status mxsa_tree_fwd(const mxsa_problem* problem, const void* q, const void
  * A parent outside [-1, own index) sets MXSA_FLAG_TREE and stands for -1; a
  * sequence of more than 32 * mask_words tokens (1..64 words) sets it too, its
  * further tokens' bits left out and, of a token with more than 2048 ancestors,
- * those beyond the nearest 2048 neither set nor counted.  MXSA_FLAG_LEN and MXSA_FLAG_CAUSAL_LEN as for
- * the calls that read the lengths (clamped; L < Tq_s: positions below zero).
+ * those beyond the nearest 2048 neither set nor counted.  MXSA_FLAG_LEN and
+ * MXSA_FLAG_CAUSAL_LEN as for the calls that read the lengths (clamped; L <
+ * Tq_s: positions below zero).
  * Tokens before cu_seqlens_q[0] and from cu_seqlens_q[B] on are not written;
  * cu_seqlens_q out of order: MXSA_FLAG_CU and nothing is.  The outputs overlap
  * neither an input nor one another.  Of the problem the call reads num_seqs
