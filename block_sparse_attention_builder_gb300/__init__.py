@@ -490,7 +490,8 @@ def tree_commit(prob, cu_seqlens_q, used_kv_lens, block_tables, path, path_lens,
     (mxsa_tree_commit): rows of new tokens path[s, :path_lens[s]] (int32,
     ascending) to the first places behind the committed keys.  idx_cache:
     [pages, index heads, page_size, index dim] in the cache dtype, or None;
-    kv_lens_out int32 [B]: committed and accepted tokens."""
+    kv_lens_out int32 [B], apart from every other tensor: committed and
+    accepted tokens."""
     what = "mxsa_tree_commit"
     seqs, kd = prob.num_seqs, prob.kv_dtype
     cache = prob.num_pages * prob.num_kv_heads * prob.page_size * _ROW_BYTES.get(kd, 256)
@@ -588,9 +589,9 @@ def build_tables(prob, kv_lens, new_lens, pages_held, block_tables, free_pages, 
     cu_seqlens_q int64 [B + 1], used_kv_lens int32 [B], positions and loc int64
     [total_q] (-1: padding) and the rows of block_tables.  pages_held_out and
     free_count_out: None writes pages_held and free_count themselves;
-    used_kv_lens may be kv_lens.  Pages that go back must be held by no other request: a
-    prefix that others still read has to leave a finished request's first
-    pages_held[s] entries before the call."""
+    used_kv_lens may be kv_lens.  Pages that go back must be held by no other
+    request: a prefix that others still read has to leave a finished request's
+    first pages_held[s] entries before the call."""
     what = "mxsa_build_tables"
     seqs, total_q = prob.num_seqs, prob.total_q
     pages_held_out = pages_held if pages_held_out is None else pages_held_out

@@ -80,8 +80,8 @@ typedef enum { MXSA_BF16 = 0, MXSA_FP16 = 1, MXSA_FP8_E4M3 = 2, MXSA_NVFP4 = 3 }
 #define MXSA_FLAG_POS 256       /* a token's position lies past the rotation table: token left out */
 #define MXSA_FLAG_GROUP 512     /* group_ptr is not a non-decreasing list of sequences: groups ignored */
 #define MXSA_FLAG_TREE 1024     /* a drafted tree's parents, path or mask width do not fit it */
-#define MXSA_FLAG_PAGES 2048    /* free list with too few pages, or one that does not fit, or no pages given back:
-                                 * nothing given out */
+#define MXSA_FLAG_PAGES 2048    /* free list with too few pages, or one that does not fit, or what goes back is no
+                                 * page of the cache: nothing given out */
 
 /* Problem description (sizes and flags of one call).  The sources: the
  * Quick-start signature and the supported-feature list of the
